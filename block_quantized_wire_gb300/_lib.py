@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "BQ_OK", 1: "BQ_ERR_NULL", 2: "BQ_ERR_SHAPE", 3: "BQ_ERR_ALIG
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_INT = ctypes.c_int
 _PROTOS = {
     "bq_abi_version": ([], ctypes.c_int),
     "bq_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -43,6 +44,14 @@ _PROTOS = {
     "bq_quant_e4m3": ([_P, _I64, _P, _P, _P], ctypes.c_int),
     "bq_dequant_e4m3": ([_P, _P, _I64, _P, _P], ctypes.c_int),
     "bq_reduce_quant_e4m3": ([_P, ctypes.c_int, _I64, _P, _P, _P, _P], ctypes.c_int),
+    "bq_expert_sort": ([_P, _INT, _I64, _INT, _INT, _P, _P, _P, _P, _P], _INT),
+    "bq_expert_gather": ([_P, _INT, _I64, _I64, _I64, _P, _INT, _P, _INT, _P, _I64, _P], _INT),
+    "bq_expert_combine": ([_P, _INT, _I64, _P, _P, _I64, _INT, _I64, _P, _I64, _P], _INT),
+    "bq_expert_combine_grad": ([_P, _INT, _I64, _P, _I64, _P, _P, _P, _INT, _I64, _INT, _I64, _P, _I64, _P, _P],
+                               _INT),
+    "bq_matvec_w4": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _P, _INT, _INT, _I64, _P, _I64, _P], _INT),
+    "bq_matvec_w4_experts": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _INT, _INT, _I64, _I64, _P, _INT,
+                              _P, _INT, _I64, _P, _I64, _P], _INT),
     "bq_take_wait_timeouts": ([_P], ctypes.c_int),
     "bq_take_wait_unlanded": ([_P], ctypes.c_int),
     "bq_take_index_errors": ([_P], ctypes.c_int),

@@ -11,6 +11,9 @@
 #define BQ_DEBUG 0
 #endif
 
+static_assert(BQ_BF16 == bqk::kBf16 && BQ_F16 == bqk::kF16 && BQ_F32 == bqk::kF32, "row types");
+static_assert(BQ_MAX_EXPERTS == bqk::kMaxExperts && BQ_SORT_PARTS == bqk::kSortParts, "expert limits");
+
 namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -430,6 +433,181 @@ bq_status bq_reduce_quant_e4m3(const void *const *x_srcs, int W, int64_t n, uint
 
 }  // extern "C"
 
+// ------------------------------------------------------------------ expert layer
+namespace {
+// The row ranges and shape rules that the expert-layer calls share.
+bool row_type(int type) { return type == BQ_BF16 || type == BQ_F16 || type == BQ_F32; }
+
+bool plan_shape(int64_t tokens, int top_k)
+{
+    return tokens >= 0 && top_k >= 1 && top_k <= BQ_MAX_TOP_K && tokens <= INT32_MAX / top_k;
+}
+
+// rows x cols values of a row type, ld values apart: shape and alignment
+bq_status check_rows(const void *p, int type, int64_t rows, int64_t cols, int64_t ld)
+{
+    if (rows > 0 && ld < cols) return BQ_ERR_SHAPE;
+    if (!p) return BQ_ERR_NULL;
+    return aligned(p, bqk::row_type_bytes(type)) ? BQ_OK : BQ_ERR_ALIGN;
+}
+
+Range rows_span(const void *p, int type, int64_t rows, int64_t cols, int64_t ld)
+{
+    const int size = bqk::row_type_bytes(type);
+    return span2d(p, rows, size * cols, size * ld);
+}
+}  // namespace
+
+extern "C" {
+
+bq_status bq_expert_sort(const void *ids, int ids_are_i64, int64_t tokens, int top_k, int n_experts, int32_t *offsets,
+                         int32_t *order, int32_t *inverse, int32_t *workspace, cudaStream_t stream)
+{
+    if (!plan_shape(tokens, top_k) || n_experts < 1 || n_experts > BQ_MAX_EXPERTS) return BQ_ERR_SHAPE;
+    const int64_t slots = tokens * top_k, id_bytes = ids_are_i64 ? 8 : 4;
+    if (!offsets || !workspace || (slots > 0 && (!ids || !order || !inverse))) return BQ_ERR_NULL;
+    if (!aligned(ids, id_bytes) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(inverse, 4) ||
+        !aligned(workspace, 4))
+        return BQ_ERR_ALIGN;
+    const Range ins[] = {span(ids, id_bytes * slots)};
+    const Range outs[] = {span(offsets, 4 * (n_experts + 1)), span(order, 4 * slots), span(inverse, 4 * slots),
+                          span(workspace, 4ll * BQ_SORT_PARTS * n_experts)};
+    if (any_alias(outs, 4, ins, 1)) return BQ_ERR_ALIAS;
+    return from_cuda(
+        bqk::launch_expert_sort(ids, ids_are_i64 != 0, slots, n_experts, offsets, order, inverse, workspace, stream));
+}
+
+bq_status bq_expert_gather(const void *x, int type, int64_t tokens, int64_t hidden, int64_t ld_x,
+                           const int32_t *inverse, int top_k, const int32_t *offsets, int n_experts, void *out,
+                           int64_t ld_out, cudaStream_t stream)
+{
+    if (!row_type(type) || !plan_shape(tokens, top_k) || hidden < 0 || n_experts < 1 || n_experts > BQ_MAX_EXPERTS)
+        return BQ_ERR_SHAPE;
+    if (tokens == 0 || hidden == 0) return BQ_OK;
+    const int64_t slots = tokens * top_k;
+    if (bq_status e = check_rows(x, type, tokens, hidden, ld_x)) return e;
+    if (bq_status e = check_rows(out, type, slots, hidden, ld_out)) return e;
+    if (!inverse || !offsets) return BQ_ERR_NULL;
+    if (!aligned(inverse, 4) || !aligned(offsets, 4)) return BQ_ERR_ALIGN;
+    const Range ins[] = {rows_span(x, type, tokens, hidden, ld_x), span(inverse, 4 * slots),
+                         span(offsets, 4 * (n_experts + 1))};
+    const Range outs[] = {rows_span(out, type, slots, hidden, ld_out)};
+    if (any_alias(outs, 1, ins, 3)) return BQ_ERR_ALIAS;
+    const bqk::RowArgs a = {tokens, hidden, inverse, top_k};
+    return from_cuda(bqk::launch_expert_gather(type, a, x, ld_x, offsets, n_experts, out, ld_out, stream));
+}
+
+bq_status bq_expert_combine(const void *y, int type, int64_t ld_y, const float *weights, const int32_t *inverse,
+                            int64_t tokens, int top_k, int64_t hidden, void *out, int64_t ld_out, cudaStream_t stream)
+{
+    if (!row_type(type) || !plan_shape(tokens, top_k) || hidden < 0) return BQ_ERR_SHAPE;
+    if (tokens == 0 || hidden == 0) return BQ_OK;
+    const int64_t slots = tokens * top_k;
+    if (bq_status e = check_rows(y, type, slots, hidden, ld_y)) return e;
+    if (bq_status e = check_rows(out, type, tokens, hidden, ld_out)) return e;
+    if (!inverse) return BQ_ERR_NULL;
+    if (!aligned(inverse, 4) || !aligned(weights, 4)) return BQ_ERR_ALIGN;
+    const Range ins[] = {rows_span(y, type, slots, hidden, ld_y), span(inverse, 4 * slots),
+                         span(weights, weights ? 4 * slots : 0)};
+    const Range outs[] = {rows_span(out, type, tokens, hidden, ld_out)};
+    if (any_alias(outs, 1, ins, 3)) return BQ_ERR_ALIAS;
+    const bqk::RowArgs a = {tokens, hidden, inverse, top_k};
+    return from_cuda(bqk::launch_expert_combine(type, a, y, ld_y, weights, out, ld_out, stream));
+}
+
+bq_status bq_expert_combine_grad(const void *dout, int type, int64_t ld_dout, const void *y, int64_t ld_y,
+                                 const float *weights, const int32_t *inverse, const int32_t *offsets, int n_experts,
+                                 int64_t tokens, int top_k, int64_t hidden, void *dy, int64_t ld_dy, float *dweights,
+                                 cudaStream_t stream)
+{
+    if (!row_type(type) || !plan_shape(tokens, top_k) || hidden < 0 || n_experts < 1 || n_experts > BQ_MAX_EXPERTS)
+        return BQ_ERR_SHAPE;
+    if (tokens == 0) return BQ_OK;
+    const int64_t slots = tokens * top_k;
+    if (hidden > 0) {  // without columns only dweights is written
+        if (bq_status e = check_rows(dout, type, tokens, hidden, ld_dout)) return e;
+        if (bq_status e = check_rows(y, type, slots, hidden, ld_y)) return e;
+        if (bq_status e = check_rows(dy, type, slots, hidden, ld_dy)) return e;
+    }
+    if (!weights || !inverse || !offsets || !dweights) return BQ_ERR_NULL;
+    if (!aligned(weights, 4) || !aligned(inverse, 4) || !aligned(offsets, 4) || !aligned(dweights, 4))
+        return BQ_ERR_ALIGN;
+    const bool rows = hidden > 0;
+    const Range none = span(dweights, 0);
+    const Range ins[] = {rows ? rows_span(dout, type, tokens, hidden, ld_dout) : none,
+                         rows ? rows_span(y, type, slots, hidden, ld_y) : none, span(weights, 4 * slots),
+                         span(inverse, 4 * slots), span(offsets, 4 * (n_experts + 1))};
+    const Range outs[] = {rows ? rows_span(dy, type, slots, hidden, ld_dy) : none, span(dweights, 4 * slots)};
+    if (any_alias(outs, 2, ins, 5)) return BQ_ERR_ALIAS;
+    const bqk::RowArgs a = {tokens, hidden, inverse, top_k};
+    return from_cuda(bqk::launch_expert_combine_grad(type, a, dout, ld_dout, y, ld_y, weights, offsets, n_experts, dy,
+                                                     ld_dy, dweights, stream));
+}
+}  // extern "C"
+
+namespace {
+// Shared checks of the 4-bit products, and the launch. x_rows rows of x, slots rows of out.
+bq_status matvec_w4(int type, int scale_type, int group, bqk::W4Args &a, cudaStream_t stream)
+{
+    if ((type != BQ_BF16 && type != BQ_F16) || (scale_type != type && scale_type != BQ_F32)) return BQ_ERR_SHAPE;
+    if (group != 32 && group != 64 && group != 128) return BQ_ERR_SHAPE;
+    if (a.x_rows < 0 || a.slots < 0 || a.slots > INT32_MAX || a.n < 0 || a.k < 0 || a.k % group) return BQ_ERR_SHAPE;
+    if (a.slots == 0 || a.n == 0) return BQ_OK;
+    if (a.ld_x < a.k || a.ld_q < a.k / 2 || a.ld_s < a.k / group || a.ld_out < a.n) return BQ_ERR_SHAPE;
+    const int64_t q_bytes = (a.n - 1) * a.ld_q + a.k / 2, s_values = (a.n - 1) * a.ld_s + a.k / group;
+    if (a.n_experts > 1 && (a.expert_q < q_bytes || a.expert_s < s_values)) return BQ_ERR_SHAPE;
+    if (!a.out || (a.k > 0 && (!a.q || !a.s || (a.x_rows > 0 && !a.x)))) return BQ_ERR_NULL;
+    if (!aligned(a.out, 2) || !aligned(a.offsets, 4) || !aligned(a.order, 4)) return BQ_ERR_ALIGN;
+    if (a.k > 0 && (!aligned(a.x, 16) || a.ld_x % 8 || !aligned(a.q, 16) || a.ld_q % 16 || !aligned(a.s, 4) ||
+                    (a.n_experts > 1 && a.expert_q % 16)))
+        return BQ_ERR_ALIGN;
+    const int s_size = bqk::row_type_bytes(scale_type);
+    const Range none = span(a.out, 0);
+    const Range ins[] = {
+        a.k > 0 && a.x_rows > 0 ? rows_span(a.x, type, a.x_rows, a.k, a.ld_x) : none,
+        a.k > 0 ? span(a.q, (a.n_experts - 1) * a.expert_q + q_bytes) : none,
+        a.k > 0 ? span(a.s, s_size * ((a.n_experts - 1) * a.expert_s + s_values)) : none,
+        a.offsets ? span(a.offsets, 4 * (a.n_experts + 1)) : none, a.order ? span(a.order, 4 * a.slots) : none};
+    const Range outs[] = {rows_span(a.out, type, a.slots, a.n, a.ld_out)};
+    if (any_alias(outs, 1, ins, 5)) return BQ_ERR_ALIAS;
+    return from_cuda(bqk::launch_matvec_w4(type, scale_type, group, a, stream));
+}
+}  // namespace
+
+extern "C" {
+
+bq_status bq_matvec_w4(const void *x, int type, int64_t rows, int64_t k, int64_t ld_x, const uint8_t *q, int64_t n,
+                       int64_t ld_q, const void *scales, int scale_type, int group, int64_t ld_s, void *out,
+                       int64_t ld_out, cudaStream_t stream)
+{
+    bqk::W4Args a = {};
+    a.x = x, a.ld_x = ld_x, a.x_rows = rows, a.slots = rows;
+    a.q = q, a.ld_q = ld_q, a.s = scales, a.ld_s = ld_s;
+    a.out = out, a.ld_out = ld_out, a.n = n, a.k = k;
+    a.n_experts = 1, a.top_k = 1;
+    return matvec_w4(type, scale_type, group, a, stream);
+}
+
+bq_status bq_matvec_w4_experts(const void *x, int type, int64_t x_rows, int64_t k, int64_t ld_x, const uint8_t *q,
+                               int64_t n, int64_t ld_q, int64_t expert_q, const void *scales, int scale_type, int group,
+                               int64_t ld_s, int64_t expert_s, const int32_t *offsets, int n_experts,
+                               const int32_t *order, int top_k, int64_t slots, void *out, int64_t ld_out,
+                               cudaStream_t stream)
+{
+    if (n_experts < 1 || n_experts > BQ_MAX_EXPERTS || top_k < 1 || top_k > BQ_MAX_TOP_K) return BQ_ERR_SHAPE;
+    if (slots > 0 && !offsets) return BQ_ERR_NULL;
+    // every place's row exists: a place p takes row order[p] / top_k, or row p
+    if (slots > 0 && x_rows < (order ? (slots + top_k - 1) / top_k : slots)) return BQ_ERR_SHAPE;
+    bqk::W4Args a = {};
+    a.x = x, a.ld_x = ld_x, a.x_rows = x_rows, a.slots = slots;
+    a.q = q, a.ld_q = ld_q, a.expert_q = expert_q, a.s = scales, a.ld_s = ld_s, a.expert_s = expert_s;
+    a.out = out, a.ld_out = ld_out, a.n = n, a.k = k;
+    a.offsets = offsets, a.n_experts = n_experts, a.order = order, a.top_k = top_k;
+    return matvec_w4(type, scale_type, group, a, stream);
+}
+
+}  // extern "C"
+
 namespace {
 // Growth of the current device's counter `which` (0: abandoned waits, 1: copies that
 // did not land after one, 2: accesses a debug build declined) since the previous call
@@ -446,7 +624,7 @@ bq_status take_wait_counter(int which, int64_t *count)
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BQ_ERR_CUDA;
     unsigned long long total = 0;
     for (auto read : {bqk::read_wait_counters_i8, bqk::read_wait_counters_mx_wire, bqk::read_wait_counters_mx,
-                      bqk::read_wait_counters_e4m3}) {
+                      bqk::read_wait_counters_e4m3, bqk::read_wait_counters_experts, bqk::read_wait_counters_w4}) {
         unsigned long long v[3] = {0, 0, 0};
         if (read(v) != cudaSuccess) return BQ_ERR_CUDA;
         total += v[which];

@@ -68,6 +68,48 @@ cudaError_t launch_dequant_e4m3(const uint8_t *q, const float *s, int64_t nblk, 
 cudaError_t launch_reduce_quant_e4m3(const Bf16List &src, int W, int64_t nblk, uint8_t *q, float *s, uint16_t *out,
                                      cudaStream_t st);
 
+// The expert layer (bq_experts.cu, bq_w4.cu).
+constexpr int kMaxExperts = 1024;
+constexpr int kSortParts = 128;  // rows of the sort's workspace
+enum RowType { kBf16 = 0, kF16 = 1, kF32 = 2 };
+constexpr int row_type_bytes(int type) { return type == kF32 ? 4 : 2; }
+// What the row kernels share: `tokens` rows of `hidden` values, top_k slots each, and the
+// places of the slots.
+struct RowArgs {
+    int64_t tokens, hidden;
+    const int32_t *inverse;
+    int top_k;
+};
+cudaError_t launch_expert_sort(const void *ids, bool ids_are_i64, int64_t slots, int n_experts, int32_t *offsets,
+                               int32_t *order, int32_t *inverse, int32_t *ws, cudaStream_t st);
+cudaError_t launch_expert_gather(int type, const RowArgs &a, const void *x, int64_t ld_x, const int32_t *offsets,
+                                 int n_experts, void *out, int64_t ld_out, cudaStream_t st);
+// weights: nullptr for the plain sum
+cudaError_t launch_expert_combine(int type, const RowArgs &a, const void *y, int64_t ld_y, const float *weights,
+                                  void *out, int64_t ld_out, cudaStream_t st);
+cudaError_t launch_expert_combine_grad(int type, const RowArgs &a, const void *dout, int64_t ld_dout, const void *y,
+                                       int64_t ld_y, const float *weights, const int32_t *offsets, int n_experts,
+                                       void *dy, int64_t ld_dy, float *dweights, cudaStream_t st);
+// A product of rows with 4-bit weights. Strides in values of the array's own type (q:
+// bytes). With offsets == nullptr the weights are one matrix and the rows are
+// x[0..slots); else row p belongs to the expert e with offsets[e] <= p < offsets[e + 1],
+// takes its values from x[order[p] / top_k] (x[p] without order), and rows past
+// offsets[n_experts] of out are zeros.
+struct W4Args {
+    const void *x;
+    int64_t ld_x, x_rows;
+    const uint8_t *q;
+    int64_t ld_q, expert_q;
+    const void *s;
+    int64_t ld_s, expert_s;
+    void *out;
+    int64_t ld_out;
+    const int32_t *offsets, *order;
+    int64_t slots, n, k;
+    int n_experts, top_k;
+};
+cudaError_t launch_matvec_w4(int x_type, int scale_type, int group, const W4Args &a, cudaStream_t st);
+
 // Programmatic dependent launch: every codec kernel is launched with programmatic
 // stream serialization and begins with griddepcontrol.wait, which returns once the
 // previous grid in the stream has completed and its memory is visible. The kernel then
@@ -121,6 +163,8 @@ cudaError_t read_wait_counters_i8(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_mx_wire(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_mx(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_e4m3(unsigned long long (&v)[3]);
+cudaError_t read_wait_counters_experts(unsigned long long (&v)[3]);
+cudaError_t read_wait_counters_w4(unsigned long long (&v)[3]);
 cudaError_t launch_wait_selftest(cudaStream_t st);
 // Debug build: one listed 256-byte range of buf and one load at byte 512 (declined).
 cudaError_t launch_index_selftest(void *buf, cudaStream_t st);

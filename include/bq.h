@@ -296,6 +296,96 @@ BQ_API bq_status bq_dequant_e4m3(const uint8_t *q, const float *scales, int64_t 
 BQ_API bq_status bq_reduce_quant_e4m3(const void *const *x_srcs, int W, int64_t n, uint8_t *q,
                                float *scales, void *out_bf16, cudaStream_t stream);
 
+/* ------------------------------------------------------------------ expert layer
+ * The two sides of a mixture-of-experts layer around the payloads above: the tokens of a
+ * batch sorted by expert, gathered and combined, with the gradients, and products of a few
+ * rows with 4-bit weights. Rows are BF16, FP16 or FP32 (bq_row_type); every sum is binary32
+ * in a fixed order (no atomics on values), rounded once to the row type, to nearest even.
+ *
+ * A slot is one choice of the router: slot t * top_k + j is token t's j-th expert, top_k in
+ * [1, BQ_MAX_TOP_K], tokens * top_k < 2^31. A place is a position in the order by expert.
+ * An id outside [0, n_experts) names an expert held elsewhere: its slot is dropped. A
+ * dropped slot has no place, nothing of it is read, and its weight (NaN or not) enters no
+ * sum. Rows at the places past the kept ones are written as zeros.
+ *
+ * Here pointers to rows are aligned to the row type's size only, and leading dimensions are
+ * free (>= the columns); rows that start on 16-byte boundaries and are whole 16-byte pieces
+ * are moved faster. The 4-bit products have rules of their own, below. */
+typedef enum { BQ_BF16 = 0, BQ_F16 = 1, BQ_F32 = 2 } bq_row_type;
+#define BQ_MAX_TOP_K 64
+#define BQ_MAX_EXPERTS 1024
+#define BQ_SORT_PARTS 128
+
+/* Sorts the slots of a batch by expert, stably: within an expert places go by slot.
+ *   ids        [tokens][top_k] int32, or int64 when ids_are_i64 != 0 (read)
+ *   offsets    [n_experts + 1] (written): expert e's places are [offsets[e],
+ *              offsets[e + 1]); offsets[n_experts] is the number of kept slots
+ *   order      [tokens * top_k] (written): the slot at each place, -1 past the kept ones
+ *   inverse    [tokens * top_k] (written): the place of each slot, -1 where dropped
+ *   workspace  [BQ_SORT_PARTS * n_experts] int32 of scratch (written), used by this call
+ *              only; its content means nothing afterwards.
+ * 1 <= n_experts <= BQ_MAX_EXPERTS. tokens == 0 writes offsets of zeros. */
+BQ_API bq_status bq_expert_sort(const void *ids, int ids_are_i64, int64_t tokens, int top_k, int n_experts,
+                                int32_t *offsets, int32_t *order, int32_t *inverse, int32_t *workspace,
+                                cudaStream_t stream);
+
+/* Token rows copied to their places: out[inverse[t][j]] = x[t].
+ *   x [tokens][ld_x], inverse and offsets as bq_expert_sort writes them (read);
+ *   out [tokens * top_k][ld_out] (written, zeros past the kept places).
+ * The gradient with respect to x is bq_expert_combine without weights. */
+BQ_API bq_status bq_expert_gather(const void *x, int type, int64_t tokens, int64_t hidden, int64_t ld_x,
+                                  const int32_t *inverse, int top_k, const int32_t *offsets, int n_experts, void *out,
+                                  int64_t ld_out, cudaStream_t stream);
+
+/* Expert rows brought back: out[t] = sum over j of weights[t][j] * y[inverse[t][j]], j
+ * ascending, one fused multiply-add each; a token without kept slots gives zeros.
+ *   y [tokens * top_k][ld_y], weights [tokens][top_k] FP32 or NULL for the plain sum,
+ *   inverse as bq_expert_sort writes it (read); out [tokens][ld_out] (written). */
+BQ_API bq_status bq_expert_combine(const void *y, int type, int64_t ld_y, const float *weights,
+                                   const int32_t *inverse, int64_t tokens, int top_k, int64_t hidden, void *out,
+                                   int64_t ld_out, cudaStream_t stream);
+
+/* The gradients of bq_expert_combine: dy[inverse[t][j]] = weights[t][j] * dout[t] and
+ * dweights[t][j] = sum over the columns of dout[t] * y[inverse[t][j]].
+ *   dout [tokens][ld_dout], y [tokens * top_k][ld_y], weights, inverse, offsets (read);
+ *   dy [tokens * top_k][ld_dy] (written, zeros past the kept places), dweights
+ *   [tokens][top_k] FP32 (written, 0 for dropped slots). */
+BQ_API bq_status bq_expert_combine_grad(const void *dout, int type, int64_t ld_dout, const void *y, int64_t ld_y,
+                                        const float *weights, const int32_t *inverse, const int32_t *offsets,
+                                        int n_experts, int64_t tokens, int top_k, int64_t hidden, void *dy,
+                                        int64_t ld_dy, float *dweights, cudaStream_t stream);
+
+/* A few rows times a 4-bit weight matrix with group scales:
+ *   out[m][i] = sum over c of x[m][c] * code[i][c] * scale[i][c / group].
+ *   x       [rows][ld_x] BF16 or FP16 (read); 16-byte aligned, ld_x % 8 == 0
+ *   q       [n][ld_q] bytes (read): two signed 4-bit codes (two's complement, -8..7) a
+ *           byte, column 2c in the low half; 16-byte aligned, ld_q % 16 == 0
+ *   scales  [n][ld_s] of scale_type (read): the type of x, or FP32; 4-byte aligned
+ *   group   32, 64 or 128 columns per scale; k % group == 0
+ *   out     [rows][ld_out] of x's type (written)
+ * A group's sum of x * code is exact products added in binary32; it is multiplied by the
+ * scale and added to the output's sum in binary32. Any number of rows is right; the
+ * kernels are made for up to 32, and read the weights once for every 32 rows (8 rows up
+ * to that number). A wrong group, type or k returns BQ_ERR_SHAPE. */
+BQ_API bq_status bq_matvec_w4(const void *x, int type, int64_t rows, int64_t k, int64_t ld_x, const uint8_t *q,
+                              int64_t n, int64_t ld_q, const void *scales, int scale_type, int group, int64_t ld_s,
+                              void *out, int64_t ld_out, cudaStream_t stream);
+
+/* The same product with an expert's own weights for each place: place p of expert e (see
+ * bq_expert_sort) gives out[p] = row * weights of e, where the row is x[order[p] / top_k]
+ * (no gathered copy is needed), or x[p] when order is NULL.
+ *   x        [x_rows][ld_x], x_rows at least slots / top_k (slots without order)
+ *   q        [n_experts][n][ld_q], experts expert_q bytes apart (a multiple of 16)
+ *   scales   [n_experts][n][ld_s], experts expert_s values apart
+ *   offsets  [n_experts + 1]; order [slots] or NULL; slots = tokens * top_k
+ *   out      [slots][ld_out] (written, zeros past the kept places)
+ * Only the weights of experts that have rows are read. */
+BQ_API bq_status bq_matvec_w4_experts(const void *x, int type, int64_t x_rows, int64_t k, int64_t ld_x,
+                                      const uint8_t *q, int64_t n, int64_t ld_q, int64_t expert_q, const void *scales,
+                                      int scale_type, int group, int64_t ld_s, int64_t expert_s,
+                                      const int32_t *offsets, int n_experts, const int32_t *order, int top_k,
+                                      int64_t slots, void *out, int64_t ld_out, cudaStream_t stream);
+
 /* Number of bounded waits inside codec kernels on the current device that ran out
  * since the previous call of this function there (the first call counts from library
  * load). Kernels that stage their inputs through shared memory (the bulk-copy ring

@@ -1,0 +1,208 @@
+"""The 4-bit products against the definition in 64 bits.
+
+Tolerance. Products of an activation with a code are exact in binary32. A group's sum is
+formed on the tensor cores in binary32 with at most one truncation per term, then scaled
+and added: the error is at most (group + k / group + 16) * 2^-23 * sum |x w| to first order
+(16: the column warps' sums and the scale's product), the factor 1.01 covering the rest.
+One rounding to the output's type adds 2^-p * |result| (p = 8 for BF16, 11 for FP16) or
+half its smallest subnormal.
+"""
+import numpy as np
+import pytest
+import torch
+
+from block_quantized_wire_gb300 import _lib, build, codec, experts, w4
+from tests.helpers import Guarded
+from tests.test_gpu_experts import ids_of, plan_of
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": (torch.bfloat16, 8, 2.0 ** -134), "f16": (torch.float16, 11, 2.0 ** -25)}
+
+
+def make_weights(rng, lead, n, k, group, s_dtype, q_pad=0, s_pad=0):
+    """Packed codes (all sixteen, -8 among them), scales, and the weights in 64 bits."""
+    code = rng.integers(-8, 8, (*lead, n, k))
+    packed = ((code[..., 0::2] & 15) | ((code[..., 1::2] & 15) << 4)).astype(np.uint8)
+    wide = np.full((*lead, n, k // 2 + q_pad), 0x5A, np.uint8)
+    wide[..., :k // 2] = packed
+    s = torch.from_numpy((rng.standard_normal((*lead, n, k // group + s_pad)) * 0.02).astype(np.float32)).to(s_dtype)
+    if s_pad:
+        s[..., k // group:] = float("nan")
+    s64 = s[..., :k // group].double().numpy()
+    q = torch.from_numpy(wide).cuda()[..., :k // 2]
+    return q, s.cuda()[..., :k // group], code * np.repeat(s64, group, axis=-1)
+
+
+def make_x(rng, rows, k, dtype, pad=0):
+    x = torch.from_numpy(rng.standard_normal((rows, k + pad)).astype(np.float32)).to(dtype)
+    if pad:
+        x[:, k:] = float("nan")
+    x = x.cuda()[:, :k]
+    return x, x.double().cpu().numpy()
+
+
+def check(got, want, terms, k, group, p, tiny):
+    bound = 1.01 * ((group + k // group + 16) * 2.0 ** -23 * terms + 2.0 ** -p * np.abs(want)) + tiny
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= bound), float((err - bound).max())
+
+
+def guarded_out(rows, n, dtype, pad=0):
+    g = Guarded(2 * rows * (n + pad))
+    return g.view(dtype, (rows, n + pad))[:, :n], g
+
+
+# rows, n, k, paddings of x, q, scales, out
+DENSE = [(1, 1, 128, 0, 0, 0, 0), (1, 7168, 1024, 0, 0, 0, 0), (1, 33, 7168, 0, 0, 0, 0), (2, 100, 384, 8, 16, 2, 3),
+         (7, 65, 640, 0, 0, 0, 0), (8, 129, 2176, 16, 0, 1, 0), (9, 64, 1152, 0, 32, 3, 1), (16, 300, 896, 0, 0, 0, 0),
+         (17, 31, 256, 0, 0, 0, 0), (32, 515, 4224, 0, 0, 0, 0), (33, 50, 1408, 0, 0, 0, 0), (100, 97, 512, 0, 0, 0, 0)]
+
+
+@pytest.mark.parametrize("wide_scales", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("shape", DENSE)
+def test_matvec(shape, name, group, wide_scales):
+    rows, n, k, x_pad, q_pad, s_pad, out_pad = shape
+    dtype, p, tiny = TYPES[name]
+    rng = np.random.default_rng(rows * n + k + group)
+    q, s, w = make_weights(rng, (), n, k, group, torch.float32 if wide_scales else dtype, q_pad, s_pad)
+    x, x64 = make_x(rng, rows, k, dtype, x_pad)
+    out, g = guarded_out(rows, n, dtype, out_pad)
+    w4.matvec_w4(x, q, s, out)
+    check(out, x64 @ w.T, np.abs(x64) @ np.abs(w).T, k, group, p, tiny)
+    assert g.bands_intact()
+    if out_pad:
+        assert bool((g.view(torch.uint8).view(rows, -1)[:, 2 * n:] == Guarded.SENTINEL).all())
+
+
+@pytest.mark.parametrize("k", [32, 64, 96, 160, 224, 1056])
+def test_matvec_with_columns_that_end_inside_a_step(k):
+    for group in (32, 64):
+        if k % group:
+            continue
+        for s_dtype in (torch.bfloat16, torch.float32):
+            rng = np.random.default_rng(k)
+            q, s, w = make_weights(rng, (), 40, k, group, s_dtype)
+            x, x64 = make_x(rng, 3, k, torch.bfloat16)
+            out, g = guarded_out(3, 40, torch.bfloat16)
+            w4.matvec_w4(x, q, s, out)
+            check(out, x64 @ w.T, np.abs(x64) @ np.abs(w).T, k, group, 8, 2.0 ** -134)
+            assert g.bands_intact()
+
+
+# tokens, top_k, n_experts, n, k, group
+EXPERTS = [(1, 1, 1, 16, 128, 128), (1, 8, 64, 100, 512, 32), (3, 2, 5, 33, 256, 64), (24, 6, 48, 70, 1024, 64),
+           (32, 8, 8, 65, 384, 128), (50, 4, 3, 40, 640, 32), (200, 2, 300, 20, 256, 64), (700, 3, 9, 24, 128, 32),
+           (2, 3, 1024, 16, 128, 64)]
+
+
+@pytest.mark.parametrize("by_token", [True, False])
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("shape", EXPERTS)
+def test_matvec_experts(shape, name, by_token):
+    tokens, top_k, n_experts, n, k, group = shape
+    dtype, p, tiny = TYPES[name]
+    rng = np.random.default_rng(tokens * 7 + n)
+    ids = ids_of(rng, tokens, top_k, n_experts, skew=True)
+    offsets, order, _ = plan_of(ids, n_experts)
+    slots, kept = tokens * top_k, int(offsets[-1])
+    q, s, w = make_weights(rng, (n_experts,), n, k, group, dtype if by_token else torch.float32)
+    x, x64 = make_x(rng, tokens if by_token else slots, k, dtype)
+    if not by_token:
+        x[kept:] = float("nan")  # rows at places that no slot takes are not read
+    out, g = guarded_out(slots, n, dtype)
+    w4.matvec_w4_experts(x, q, s, torch.from_numpy(offsets).cuda(), out,
+                         order=torch.from_numpy(order).cuda() if by_token else None, top_k=top_k)
+    want, terms = np.zeros((slots, n)), np.zeros((slots, n))
+    for e in range(n_experts):
+        at = np.arange(offsets[e], offsets[e + 1])
+        rows = x64[order[at] // top_k if by_token else at]
+        want[at], terms[at] = rows @ w[e].T, np.abs(rows) @ np.abs(w[e]).T
+    check(out, want, terms, k, group, p, tiny)
+    assert not out[kept:].any() and g.bands_intact()
+
+
+def test_an_infinite_row_leaves_the_others_alone():
+    rng = np.random.default_rng(3)
+    q, s, _ = make_weights(rng, (), 48, 256, 32, torch.bfloat16)
+    x, _ = make_x(rng, 5, 256, torch.bfloat16)
+    clean = torch.empty((5, 48), dtype=torch.bfloat16, device="cuda")
+    w4.matvec_w4(x, q, s, clean)
+    x[2, 7], x[3, 9] = float("inf"), float("nan")
+    out = torch.empty_like(clean)
+    w4.matvec_w4(x, q, s, out)
+    assert not bool(out[2].isfinite().any()) and bool(out[3].isnan().all())
+    for r in (0, 1, 4):
+        assert torch.equal(out[r], clean[r])
+
+
+def test_rows_do_not_depend_on_their_company():
+    # row 0 alone, with 7 and with 31 others, and repeated calls: the same bits wherever the
+    # same kernel runs, and within one launch wherever the row stands
+    rng = np.random.default_rng(4)
+    q, s, _ = make_weights(rng, (), 200, 2048, 64, torch.float16)
+    x, _ = make_x(rng, 8, 2048, torch.float16)
+    x[5] = x[0]
+    outs = []
+    for _ in range(3):
+        out = torch.empty((8, 200), dtype=torch.float16, device="cuda")
+        w4.matvec_w4(x, q, s, out)
+        outs.append(out)
+    one = torch.empty((1, 200), dtype=torch.float16, device="cuda")
+    w4.matvec_w4(x[:1], q, s, one)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    assert torch.equal(outs[0][0], outs[0][5]) and torch.equal(one[0], outs[0][0])
+
+
+def test_no_rows_no_columns_and_an_empty_sum():
+    e = torch.empty
+    q, s = e((8, 64), dtype=torch.uint8, device="cuda"), torch.ones((8, 1), dtype=torch.bfloat16, device="cuda")
+    w4.matvec_w4(e((0, 128), dtype=torch.bfloat16, device="cuda"), q, s, e((0, 8), dtype=torch.bfloat16, device="cuda"))
+    w4.matvec_w4(e((3, 128), dtype=torch.bfloat16, device="cuda"), q[:0], s[:0],
+                 e((3, 0), dtype=torch.bfloat16, device="cuda"))
+    out = torch.full((3, 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    w4.matvec_w4(e((3, 0), dtype=torch.bfloat16, device="cuda"), e((8, 0), dtype=torch.uint8, device="cuda"),
+                 e((8, 0), dtype=torch.bfloat16, device="cuda"), out)
+    assert not out.any()
+
+
+def test_weights_past_2_32_bytes():
+    # 300 experts of 16 MB: the last one's codes start past 2^32 bytes
+    n_experts, n, k, group = 300, 4096, 8192, 128
+    q = torch.zeros((n_experts, n, k // 2), dtype=torch.uint8, device="cuda")
+    s = torch.ones((n_experts, n, k // group), dtype=torch.bfloat16, device="cuda")
+    q[-1] = 0x21  # codes 1 (even columns) and 2 (odd columns)
+    ids = np.array([[299, 0]])
+    offsets, order, _ = plan_of(ids, n_experts)
+    x = torch.ones((1, k), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((2, n), dtype=torch.bfloat16, device="cuda")
+    w4.matvec_w4_experts(x, q, s, torch.from_numpy(offsets).cuda(), out, order=torch.from_numpy(order).cuda(), top_k=2)
+    assert not out[0].any() and bool((out[1] == 3 * k // 2).all())
+
+
+def test_a_wrong_plan_stays_in_bounds():
+    rng = np.random.default_rng(9)
+    q, s, _ = make_weights(rng, (4,), 40, 256, 64, torch.bfloat16)
+    x, _ = make_x(rng, 6, 256, torch.bfloat16)
+    out, g = guarded_out(12, 40, torch.bfloat16)
+    for offsets, order in (([0, 2 ** 30, 3, 2 ** 30, 2 ** 31 - 1], [2 ** 30] * 12), ([-5, 4, -9, 12, -1], [-1] * 12)):
+        w4.matvec_w4_experts(x, q, s, torch.tensor(offsets, dtype=torch.int32, device="cuda"), out,
+                             order=torch.tensor(order, dtype=torch.int32, device="cuda"), top_k=2)
+        torch.cuda.synchronize()
+        assert g.bands_intact()
+
+
+def test_the_debug_build_declines_no_access(bq_lib):
+    with _lib.use_library(build.build_debug_library()):
+        codec.take_index_errors()
+        for shape in DENSE:
+            for group in (32, 128):
+                test_matvec(shape, "bf16", group, False)
+                test_matvec(shape, "f16", group, True)
+        for shape in EXPERTS:
+            test_matvec_experts(shape, "bf16", True)
+            test_matvec_experts(shape, "f16", False)
+        torch.cuda.synchronize()
+        assert codec.take_index_errors() == 0
