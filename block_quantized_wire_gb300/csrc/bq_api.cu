@@ -71,15 +71,30 @@ int g_occ_n = 0;
 std::mutex g_occ_mu;
 }  // namespace
 
-cudaError_t grid_for(const void *kernel, int64_t nchunk, int *grid, size_t smem, int block)
+namespace {
+cudaError_t sm_count_of(int dev, int *sms)
+{
+    *sms = (dev >= 0 && dev < kMaxDevices) ? g_sms[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms == 0) {
+        if (cudaError_t e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) return e;
+        if (dev >= 0 && dev < kMaxDevices) g_sms[dev].store(*sms, std::memory_order_relaxed);
+    }
+    return cudaSuccess;
+}
+}  // namespace
+
+cudaError_t sm_count(int *sms)
 {
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
-    int sms = (dev >= 0 && dev < kMaxDevices) ? g_sms[dev].load(std::memory_order_relaxed) : 0;
-    if (sms == 0) {
-        if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
-        if (dev >= 0 && dev < kMaxDevices) g_sms[dev].store(sms, std::memory_order_relaxed);
-    }
+    return sm_count_of(dev, sms);
+}
+
+cudaError_t grid_for(const void *kernel, int64_t nchunk, int *grid, size_t smem, int block)
+{
+    int dev = 0, sms = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (cudaError_t e = sm_count_of(dev, &sms)) return e;
     int occ = 0;
     {
         std::lock_guard<std::mutex> lock(g_occ_mu);
@@ -551,7 +566,8 @@ bq_status matvec_w4(int type, int scale_type, int group, bqk::W4Args &a, cudaStr
 {
     if ((type != BQ_BF16 && type != BQ_F16) || (scale_type != type && scale_type != BQ_F32)) return BQ_ERR_SHAPE;
     if (group != 32 && group != 64 && group != 128) return BQ_ERR_SHAPE;
-    if (a.x_rows < 0 || a.slots < 0 || a.slots > INT32_MAX || a.n < 0 || a.k < 0 || a.k % group) return BQ_ERR_SHAPE;
+    if (a.x_rows < 0 || a.x_rows > INT32_MAX || a.slots < 0 || a.slots > INT32_MAX) return BQ_ERR_SHAPE;
+    if (a.n < 0 || a.n > BQ_MAX_W4_DIM || a.k < 0 || a.k > BQ_MAX_W4_DIM || a.k % group) return BQ_ERR_SHAPE;
     if (a.slots == 0 || a.n == 0) return BQ_OK;
     if (a.ld_x < a.k || a.ld_q < a.k / 2 || a.ld_s < a.k / group || a.ld_out < a.n) return BQ_ERR_SHAPE;
     const int64_t q_bytes = (a.n - 1) * a.ld_q + a.k / 2, s_values = (a.n - 1) * a.ld_s + a.k / group;

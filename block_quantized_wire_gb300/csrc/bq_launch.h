@@ -107,6 +107,7 @@ struct W4Args {
     const int32_t *offsets, *order;
     int64_t slots, n, k;
     int n_experts, top_k;
+    int staged_rows, ctas_per_sm;  // filled by the launcher
 };
 cudaError_t launch_matvec_w4(int x_type, int scale_type, int group, const W4Args &a, cudaStream_t st);
 
@@ -156,6 +157,9 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), int grid, cudaStream_t st, A
 // first call for a kernel also raises its dynamic shared memory limit to `smem`. Returns
 // the error of the device queries, if any.
 cudaError_t grid_for(const void *kernel, int64_t nchunk, int *grid, size_t smem = 0, int block = kThreads);
+
+// The current device's number of SMs.
+cudaError_t sm_count(int *sms);
 
 // Each kernel translation unit's counters {wait timeouts, unlanded copies, debug index errors} (see
 // g_wait_timeouts in bq_device.cuh): totals since the library was loaded, never reset.

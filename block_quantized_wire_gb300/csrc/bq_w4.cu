@@ -10,19 +10,18 @@
 // 16 x 16 tiles of weights are the A operand of mma.m16n8k16, up to 8 rows of x are B,
 // and the binary32 sums of a group are multiplied by its scale outside the mma. Sums are
 // binary32 throughout; the output is rounded once.
+#include <climits>
+#include <type_traits>
+
 #include "bq_rows.cuh"
 
 namespace bqk {
 namespace {
 
-constexpr int kW4Warps = kThreads / 32;
-constexpr int kRowTiles = 2;                 // 16-row tiles per warp
-constexpr int kWarpRows = 16 * kRowTiles;    // weight rows per warp
-constexpr int kStepCols = 128;               // columns per warp and step
-constexpr int kW4Stages = 4;                 // steps in flight per warp
-constexpr int kCodeBytes = kWarpRows * kStepCols / 2;
-constexpr int kScaleSlot = 16;               // bytes per weight row and step: at most 4 FP32 scales
-constexpr int kStageBytes = kCodeBytes + kWarpRows * kScaleSlot;
+// A warp's step is 2 KB of codes: kRowTiles tiles of 16 weight rows by 256 / kRowTiles
+// columns. One tile makes items small and leaves registers for more warps; two tiles share
+// each fragment of x between them.
+constexpr int kStepCodeBytes = 2048;
 
 // ---------------------------------------------------------------- codes to numbers
 // Eight codes of a word -> four pairs of exact integers, pair i = codes (i, i + 4). The
@@ -31,23 +30,38 @@ constexpr int kStageBytes = kCodeBytes + kWarpRows * kScaleSlot;
 template <class T>
 struct Codes;
 
+// (w & mask) ^ x in one instruction
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t x)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(mask), "r"(x));
+    return r;
+}
+
 template <>
 struct Codes<__nv_bfloat16> {
     static __device__ __forceinline__ void widen(uint32_t w, uint32_t (&v)[4])
     {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const uint32_t h = ((w >> (4 * i)) & 0x000f000fu) ^ 0x43084308u;  // 128 + 8 + c
+            const uint32_t h = and_xor(w >> (4 * i), 0x000f000fu, 0x43084308u);  // 128 + 8 + c
             asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(h), "r"(0x43084308u));
         }
     }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    // c = a * b, or c += a * b
+    template <bool kFirst>
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t *a, uint32_t b0, uint32_t b1)
     {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        if constexpr (kFirst)
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                "{%8, %9}, {%10, %10, %10, %10};"
+                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+        else
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                "{%8, %9}, {%0, %1, %2, %3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 };
 
@@ -55,19 +69,30 @@ template <>
 struct Codes<__half> {
     static __device__ __forceinline__ void widen(uint32_t w, uint32_t (&v)[4])
     {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t h = ((w >> (4 * i)) & 0x000f000fu) ^ 0x64086408u;  // 1024 + 8 + c
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(h), "r"(0x64086408u));
-        }
+        // The mantissa holds both codes of a byte: 1024 + 8 + c from the low one, 1024 + 16 (8 +
+        // c) from the high one, whose sixteenth the fused multiply-add takes on its way.
+        const uint32_t w8 = w >> 8;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[0]) : "r"(and_xor(w, 0x000f000fu, 0x64086408u)), "r"(0x64086408u));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+            : "=r"(v[1]) : "r"(and_xor(w, 0x00f000f0u, 0x64806480u)), "r"(0x2c002c00u), "r"(0xd480d480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[2]) : "r"(and_xor(w8, 0x000f000fu, 0x64086408u)), "r"(0x64086408u));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;"
+            : "=r"(v[3]) : "r"(and_xor(w8, 0x00f000f0u, 0x64806480u)), "r"(0x2c002c00u), "r"(0xd480d480u));
     }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    // c = a * b, or c += a * b
+    template <bool kFirst>
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t *a, uint32_t b0, uint32_t b1)
     {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        if constexpr (kFirst)
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                "{%8, %9}, {%10, %10, %10, %10};"
+                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+        else
+            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                "{%8, %9}, {%0, %1, %2, %3};"
+                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 };
 
@@ -82,8 +107,16 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t a)
 __device__ __forceinline__ uint4 lds_v4(uint32_t a)
 {
     uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(a)
+                 : "memory");
     return r;
+}
+
+__device__ __forceinline__ void lds_v2(uint32_t a, uint32_t &x, uint32_t &y)
+{
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a) : "memory");
 }
 
 // Copies `bytes` of kSize bytes and fills the rest with zeros.
@@ -94,91 +127,173 @@ __device__ __forceinline__ void lane_copy_part(uint32_t dst, const void *src, in
     if constexpr (kSize == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kSize), "r"(bytes) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kSize), "r"(bytes)
+                     : "memory");
 }
 
-// Bytes into a warp's stage at which the 16 bytes (32 codes) c of weight row r lie. Two
-// 64-byte rows share a 128-byte line, and the four pieces of a row are permuted by the
-// line's number, so that the eight rows that a mma fragment reads at once lie in
+// Bytes into a warp's stage at which the 16 bytes (32 codes) c of weight row r lie. The
+// 16-byte pieces of a 128-byte line (one row of 256 columns or two of 128) are permuted by
+// the line's number, so that the eight rows that a mma fragment reads at once lie in
 // different banks.
+template <int kRowTiles>
 __device__ __forceinline__ uint32_t code_at(int r, int c)
 {
+    if (kRowTiles == 1) return (uint32_t)(r * 128 + ((c ^ (r & 7)) * 16));
     return (uint32_t)((r >> 1) * 128 + (((r & 1) * 4 + (c ^ ((r >> 1) & 3))) * 16));
 }
 
+// code_at(r + i * (4 or 8 rows), c) from code_at(r, c), for the rows r < 4 (one tile) or
+// r < 8 (two) that a warp's copy covers.
+template <int kRowTiles>
+__device__ __forceinline__ uint32_t code_row(uint32_t at, int i)
+{
+    return (kRowTiles == 1 ? at ^ (64 * (i & 1)) : at) + 512 * i;
+}
+
+// 16 bytes that other warps will read too: through L1.
+__device__ __forceinline__ uint4 ld_keep_v4(const void *p)
+{
+    if (!dbg_ok(p, 16, false)) return make_uint4(0, 0, 0, 0);
+    return __ldg(static_cast<const uint4 *>(p));
+}
+
 // ---------------------------------------------------------------- scales
-// A row's scales of one step: 128 / group values, copied as the 4-byte words that hold
-// them. `skew` is 1 where 16-bit scales start in the upper half of their first word.
-template <class S, int kGroup>
+// A row's kCount scales of one step, copied as the 4-byte words that hold them: 16-bit
+// scales of rows with odd strides may start in the upper half of their first word.
+template <class S, int kCount>
 struct Scales {
-    static constexpr int kCount = kStepCols / kGroup;
     static constexpr int kSize = sizeof(S);
+    static constexpr int kBytes = kCount * kSize;  // 2 to 32
+    static constexpr int kWords = (kBytes + 3) / 4;
 
     // p: the row's first scale of the step; valid: how many of kCount lie in the row
     static __device__ __forceinline__ void fetch(uint32_t dst, const S *p, int valid)
     {
         const uintptr_t a = reinterpret_cast<uintptr_t>(p), base = a & ~(uintptr_t)3;
         const int end = valid > 0 ? (int)(a - base) + valid * kSize : 0;  // valid bytes from base
-        constexpr int kWords = (kCount * kSize + 3) / 4;
-        if constexpr (kWords == 4) {
-            if ((a & 15) == 0) return lane_copy_part<16>(dst, p, end);
-        }
-        if constexpr (kWords == 2) {
-            if ((a & 7) == 0) return lane_copy_part<8>(dst, p, end);
-        }
-        constexpr int kMost = kWords + (kSize == 2 && kCount > 1 ? 1 : 0);
 #pragma unroll
-        for (int i = 0; i < kMost; i++) {
+        for (int i = 0; i < kWords + (kSize == 2 && kCount > 1 ? 1 : 0); i++) {
             const int left = end - 4 * i;
             lane_copy_part<4>(dst + 4 * i, reinterpret_cast<const char *>(base) + (left > 0 ? 4 * i : 0),
                               left < 0 ? 0 : left < 4 ? left : 4);
         }
     }
 
-    static __device__ __forceinline__ float widen16(uint32_t h) { return Value<S>::widen((uint16_t)h); }
-
-    static __device__ __forceinline__ void read(uint32_t src, int skew, float (&v)[kCount])
+    // A whole step's scales in aligned copies, where every row allows it.
+    static __device__ __forceinline__ bool plain(const S *s, int64_t ld, int64_t expert_ld)
     {
-        const uint4 w4 = lds_v4(src);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        if constexpr (kSize == 4) {
+        constexpr int kAlign = kBytes < 16 ? kBytes : 16;
+        return kBytes >= 4 &&
+               ((reinterpret_cast<uintptr_t>(s) | (ld * kSize) | (expert_ld * kSize)) & (kAlign - 1)) == 0;
+    }
+    static __device__ __forceinline__ void fetch_plain(uint32_t dst, const S *p)
+    {
+        if constexpr (kBytes >= 16) {
 #pragma unroll
-            for (int i = 0; i < kCount; i++) v[i] = __uint_as_float(w[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kCount; i += 2) {
-                const uint32_t pair = skew ? __funnelshift_r(w[i / 2], w[i / 2 + 1], 16) : w[i / 2];
-                v[i] = widen16(pair & 0xffffu);
-                if (i + 1 < kCount) v[i + 1] = widen16(pair >> 16);
-            }
+            for (int i = 0; i < kBytes / 16; i++) lane_copy16(dst + 16 * i, reinterpret_cast<const char *>(p) + 16 * i);
+        } else if constexpr (kBytes >= 4) {
+            lane_copy_part<kBytes>(dst, p, kBytes);
         }
+    }
+
+    // a row's scales as copied, shifted into place where skewed
+    static __device__ __forceinline__ void read(uint32_t src, uint32_t (&w)[kWords])
+    {
+        if constexpr (kWords >= 4) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; i++) {
+                const uint4 v = lds_v4(src + 16 * i);
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        } else if constexpr (kWords == 2) {
+            lds_v2(src, w[0], w[1]);
+        } else {
+            w[0] = lds_u32(src);
+        }
+    }
+    static __device__ __forceinline__ void read_skewed(uint32_t src, int skew, uint32_t (&w)[kWords])
+    {
+        uint32_t low = lds_u32(src);
+#pragma unroll
+        for (int i = 0; i < kWords; i++) {
+            const uint32_t high = lds_u32(src + 4 * i + 4);
+            w[i] = __funnelshift_r(low, high, 16 * skew);
+            low = high;
+        }
+    }
+    static __device__ __forceinline__ float at(const uint32_t (&w)[kWords], int i)
+    {
+        if constexpr (kSize == 4)
+            return __uint_as_float(w[i]);
+        else
+            return Value<S>::widen((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu));
     }
 };
 
 // ---------------------------------------------------------------- kernel
-// A CTA takes items of kWarpRows * kRowWarps weight rows of one expert, over all columns
-// and for every row of x that the expert has, kTiles * 8 rows at a time. Its warps are
+// A CTA takes items of 16 * kRowTiles * kRowWarps weight rows of one expert, over all
+// columns and for every row of x that the expert has, kPassRows at a time. Its warps are
 // kRowWarps in the rows times kColWarps in the columns: a warp walks every kColWarps-th
-// step of 128 columns on its own, through its own ring of asynchronous copies, and the
-// column warps' sums are added in order at the end of an item. The ring runs on over the
-// ends of items, so the memory is never idle in between.
+// step on its own, through its own ring of asynchronous copies, and the column warps' sums
+// are added in order at the end of an item. The ring runs on over the ends of items, so the
+// memory is never idle in between.
+//
+// kPassRows is 8 per column tile of the mma, or 4: the rows then take the even columns of
+// one tile, and half of the sums (the odd columns) need no scaling and no registers.
 struct ExpertRows {
     int expert, lo, hi;
+    int before;  // passes over a row block of the experts before this one
 };
 
-template <class T, class S, int kGroup, int kTiles, int kRowWarps, bool kExperts>
-__global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_constant__ W4Args a)
+// Shared memory for staged rows of x, what two CTAs an SM leave beside their rings; a row is
+// padded to whole steps.
+constexpr int64_t kStagedBytes = 44 * 1024;
+constexpr int kMaxStagedRows = kStagedBytes / 512;
+inline int64_t staged_row_bytes(int64_t k) { return (k + 255) / 256 * 512; }
+
+template <class T_, class S_, int kGroup_, int kPassRows_, int kRowTiles_, int kRowWarps_, int kColWarps_, int kStages_,
+          int kCtas_, bool kStaged_, bool kExperts_>
+struct W4Shape {
+    using T = T_;
+    using S = S_;
+    static constexpr int kGroup = kGroup_, kPassRows = kPassRows_, kRowTiles = kRowTiles_;
+    static constexpr int kRowWarps = kRowWarps_, kColWarps = kColWarps_, kStages = kStages_, kCtas = kCtas_;
+    static constexpr bool kStaged = kStaged_, kExperts = kExperts_;
+    static constexpr bool kEven = kPassRows == 4;
+    static constexpr int kTiles = kEven ? 1 : kPassRows / 8;
+    static constexpr int kWarps = kRowWarps * kColWarps, kBlock = 32 * kWarps;
+    static constexpr int kWarpRows = 16 * kRowTiles, kItemRows = kWarpRows * kRowWarps;
+    static constexpr int kStepCols = 256 / kRowTiles;
+    static constexpr int kScaleSlot = kRowTiles == 1 ? 32 : 16;  // bytes per row and step: up to 8 or 4 FP32 scales
+    static constexpr int kStageBytes = kStepCodeBytes + kWarpRows * kScaleSlot;
+    static constexpr int kSumStride = kItemRows + 4;  // rows of x land in different banks
+    static constexpr size_t kRingBytes = (size_t)kWarps * kStages * kStageBytes;
+    static constexpr int kSumFloats = kColWarps * kPassRows * kSumStride;
+    static constexpr size_t kSumBytes = sizeof(float) * kSumFloats;
+};
+
+template <class Shape>
+__global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(const __grid_constant__ W4Args a)
 {
-    constexpr int kColWarps = kW4Warps / kRowWarps;
-    constexpr int kItemRows = kWarpRows * kRowWarps;
-    constexpr int kPassRows = 8 * kTiles;
-    constexpr int kSumStride = kItemRows + 4;
-    constexpr int kPerScale = kGroup / 32;
-    using Sc = Scales<S, kGroup>;
+    using T = typename Shape::T;
+    using S = typename Shape::S;
     using Bits = typename Value<T>::Bits;
+    constexpr int kGroup = Shape::kGroup, kPassRows = Shape::kPassRows, kTiles = Shape::kTiles;
+    constexpr int kRowTiles = Shape::kRowTiles, kColWarps = Shape::kColWarps, kStages = Shape::kStages;
+    constexpr int kBlock = Shape::kBlock, kWarps = Shape::kWarps, kStageBytes = Shape::kStageBytes;
+    constexpr int kWarpRows = Shape::kWarpRows, kItemRows = Shape::kItemRows, kSumStride = Shape::kSumStride;
+    constexpr int kStepCols = Shape::kStepCols, kStepBytes = kStepCols / 2, kParts = kStepCols / 32;
+    constexpr int kScaleCount = kStepCols / kGroup, kScaleSlot = Shape::kScaleSlot, kPerScale = kGroup / 32;
+    constexpr bool kStaged = Shape::kStaged, kExperts = Shape::kExperts, kEven = Shape::kEven;
+    using Product = typename std::conditional<kStaged, __half, T>::type;  // the mma's operands
+    using Sc = Scales<S, kScaleCount>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ ExpertRows active[kExperts ? kMaxExperts : 1];
-    __shared__ int warp_active[kW4Warps + 1];
+    ExpertRows *const active = reinterpret_cast<ExpertRows *>(smem + Shape::kRingBytes + Shape::kSumBytes);
+    unsigned char *const x_smem = smem + Shape::kRingBytes + Shape::kSumBytes +
+                                  ((sizeof(ExpertRows) * a.n_experts + 15) & ~(size_t)15);
+    __shared__ int warp_active[kWarps], warp_passes[kWarps];
+    __shared__ float x_unscale[kStaged ? kMaxStagedRows : 1];
+    __shared__ uint32_t x_top[kWarps];
 
     pdl_begin();
     dbg_begin();
@@ -194,247 +309,466 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
     const int row_warp = warp / kColWarps, col_warp = warp % kColWarps;
     const int g = lane >> 2, t = lane & 3;  // mma fragment row (or column of C) and quad lane
 
-    // The experts that have rows, in order. Offsets of a wrong plan are clamped.
-    int n_active = 1;
+    // rows of x a pass takes; staged rows are a whole number of passes, or less than one
+    const int pass_cap = kStaged && a.staged_rows < kPassRows ? a.staged_rows : kPassRows;
+    const int chunk_cap = kStaged ? a.staged_rows : INT_MAX;
+
+    // The experts that have rows, in order, and the passes that a row block of each takes.
+    // Offsets of a wrong plan are clamped.
+    int n_active = 1, passes = 1;
     int kept = (int)a.slots;
     if constexpr (kExperts) {
-        n_active = 0;
+        n_active = passes = 0;
         const int slots = (int)a.slots;
         auto offset = [&](int e) {
             const int v = dbg_ok(a.offsets + e, 4, false) ? __ldg(a.offsets + e) : 0;
             return v < 0 ? 0 : v < slots ? v : slots;
         };
         kept = offset(a.n_experts);
-        for (int base = 0; base < a.n_experts; base += kThreads) {
+        for (int base = 0; base < a.n_experts; base += kBlock) {
             const int e = base + threadIdx.x;
             const int lo = e < a.n_experts ? offset(e) : 0, hi = e < a.n_experts ? offset(e + 1) : 0;
             const unsigned has = __ballot_sync(kFull, hi > lo);
-            if (lane == 0) warp_active[warp] = __popc(has);
-            __syncthreads();
-            int at = n_active;
-            for (int w = 0; w < kW4Warps; w++) {
-                at += w < warp ? warp_active[w] : 0;
-                n_active += warp_active[w];
+            const int mine = hi > lo ? (hi - lo - 1) / pass_cap + 1 : 0;
+            int upto = mine;  // passes of this warp's experts up to this one
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(kFull, upto, d);
+                if (lane >= d) upto += up;
             }
-            if (hi > lo) active[at + __popc(has & ((1u << lane) - 1u))] = ExpertRows{e, lo, hi};
+            if (lane == 31) {
+                warp_active[warp] = __popc(has);
+                warp_passes[warp] = upto;
+            }
+            __syncthreads();
+            int at = n_active, before = passes + upto - mine;
+            for (int w = 0; w < kWarps; w++) {
+                at += w < warp ? warp_active[w] : 0;
+                before += w < warp ? warp_passes[w] : 0;
+                n_active += warp_active[w];
+                passes += warp_passes[w];
+            }
+            if (hi > lo) active[at + __popc(has & ((1u << lane) - 1u))] = ExpertRows{e, lo, hi, before};
             __syncthreads();
         }
     } else {
-        if (threadIdx.x == 0) active[0] = ExpertRows{0, 0, (int)a.slots};
+        if (threadIdx.x == 0) active[0] = ExpertRows{0, 0, (int)a.slots, 0};
         __syncthreads();
     }
 
     const int row_blocks = (int)((a.n + kItemRows - 1) / kItemRows);
-    const int64_t items = (int64_t)n_active * row_blocks;
     const int steps = (int)((a.k + kStepCols - 1) / kStepCols);
-    const uint32_t ring = smem_u32(smem) + warp * (kW4Stages * kStageBytes);
-    float *sums = reinterpret_cast<float *>(smem + kW4Warps * kW4Stages * kStageBytes);
-    const S *const scales = static_cast<const S *>(a.s);
-
-    // The copying side of the ring: the next step to fetch.
-    int64_t f_item = blockIdx.x;
-    int f_step = col_warp, f_pass = 0, f_passes = 0, f_slot = 0;
-    const uint8_t *f_q = nullptr;
-    const S *f_s = nullptr;
-    int f_rows = 0;  // weight rows of this warp in the item
-    auto open_item = [&]() {
-        if (f_item < items) {
-            const ExpertRows er = active[f_item / row_blocks];
-            const int64_t r0 = (f_item % row_blocks) * kItemRows + row_warp * kWarpRows;
-            f_q = a.q + er.expert * a.expert_q + r0 * a.ld_q;
-            f_s = scales + er.expert * a.expert_s + r0 * a.ld_s;
-            f_rows = a.n - r0 < kWarpRows ? (int)(a.n - r0) : kWarpRows;
-            f_passes = (er.hi - er.lo + kPassRows - 1) / kPassRows;
+    const int whole_steps = (int)(a.k / kStepCols);
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
+    float *sums = reinterpret_cast<float *>(smem + Shape::kRingBytes);
+    // This CTA's run of items, of equal passes over row blocks for every CTA: an item belongs
+    // to the run that its first pass falls in. CTAs are placed on the SMs in turn, so the runs
+    // of one SM's CTAs follow one another and every SM's share is the same but for one item.
+    const int sms = (int)gridDim.x / a.ctas_per_sm;
+    const int64_t rank = (int64_t)(blockIdx.x % sms) * a.ctas_per_sm + blockIdx.x / sms;
+    auto item_at = [&](int64_t cost) {  // the first item that starts at or past this many passes
+        int lo = 0, hi = n_active;      // the last expert that starts before it
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if ((int64_t)active[mid].before * row_blocks <= cost)
+                lo = mid;
+            else
+                hi = mid;
         }
+        const int each = kExperts ? (active[lo].hi - active[lo].lo - 1) / pass_cap + 1 : 1;
+        const int64_t block = (cost - (int64_t)active[lo].before * row_blocks + each - 1) / each;
+        return lo * row_blocks + (int)(block < row_blocks ? block : row_blocks);
+    };
+    const S *const scales = static_cast<const S *>(a.s);
+    const int64_t costs = n_active > 0 ? (int64_t)passes * row_blocks : 0;
+    const int item_lo = costs > 0 ? item_at(costs * rank / gridDim.x) : 0;
+    const int item_hi = costs > 0 ? item_at(costs * (rank + 1) / gridDim.x) : 0;
+    // 16-bit scales may start in mid-word: in some rows where strides are odd, in every second
+    // step where a step has one
+    const bool skewed = sizeof(S) == 2 && (kScaleCount == 1 || ((a.ld_s | a.expert_s) & 1));
+
+    // The copying side of the ring: the next step to fetch. A lane copies the 16 bytes
+    // f_col of the rows f_row + kLaneRows i, and row `lane`'s scales.
+    constexpr int kPieces = kStepBytes / 16, kLaneRows = 32 / kPieces, kCopies = kWarpRows / kLaneRows;
+    const int f_row = lane / kPieces, f_col = lane % kPieces;
+    int f_left = item_hi - item_lo;  // items to go, from this run's on
+    int f_active = item_lo / row_blocks, f_first = item_lo - f_active * row_blocks;  // the run's expert, first block
+    int f_end = 0, f_block = 0, f_rest = 0;    // the run's last block + 1; the block; rows of x from this chunk on
+    int f_passes = 0, f_rows = 0, f_step = col_warp;
+    int f_plain = 0;  // steps ahead that need no checks: whole steps of an item of whole rows
+    uint32_t f_slot = ring;
+    const uint8_t *f_q = nullptr;  // this lane's 16 bytes of the step
+    const S *f_s = nullptr;        // this lane's first scale of the step
+    const int64_t ld_rows = kLaneRows * a.ld_q;
+    const uint32_t dst_code = code_at<kRowTiles>(f_row, f_col), dst_scale = kStepCodeBytes + lane * kScaleSlot;
+    const int my_steps = steps > col_warp ? (steps - col_warp - 1) / kColWarps + 1 : 0;
+    const int my_plain = Sc::plain(scales, a.ld_s, a.expert_s) && whole_steps > col_warp
+                             ? (whole_steps - col_warp - 1) / kColWarps + 1 : 0;
+    auto chunk_passes = [&](int rest) { return ((rest < chunk_cap ? rest : chunk_cap) + pass_cap - 1) / pass_cap; };
+    auto open_chunk = [&]() {  // the run's first block again
+        const int64_t r0 = (int64_t)f_first * kItemRows + row_warp * kWarpRows, e = active[f_active].expert;
+        f_block = f_first;
+        f_passes = chunk_passes(f_rest);
+        f_q = a.q + e * a.expert_q + (r0 + f_row) * a.ld_q + 16 * f_col + col_warp * kStepBytes;
+        f_s = scales + e * a.expert_s + (r0 + lane) * a.ld_s + col_warp * kScaleCount;
+    };
+    auto open_run = [&]() {
+        f_end = row_blocks - f_first < f_left ? row_blocks : f_first + f_left;
+        f_rest = active[f_active].hi - active[f_active].lo;
+        open_chunk();
+    };
+    auto open_rows = [&]() {  // and the pass over them
+        const int r0 = f_block * kItemRows + row_warp * kWarpRows;
+        f_rows = a.n - r0 < kWarpRows ? (int)(a.n - r0) : kWarpRows;
+        f_step = col_warp;
+        f_plain = f_rows == kWarpRows ? my_plain : 0;
+    };
+    const int64_t back_q = (int64_t)my_steps * kColWarps * kStepBytes;
+    const int64_t back_s = (int64_t)my_steps * kColWarps * kScaleCount;
+    auto advance = [&]() {  // past a pass's last step
+        f_q -= back_q;
+        f_s -= back_s;
+        if (--f_passes == 0) {
+            f_q += kItemRows * a.ld_q;
+            f_s += kItemRows * a.ld_s;
+            f_passes = chunk_passes(f_rest);
+            if (++f_block == f_end) {
+                f_rest -= chunk_cap;
+                if (f_rest > 0) {
+                    open_chunk();
+                } else {
+                    f_left -= f_end - f_first;
+                    if (f_left == 0) return;
+                    f_first = 0;
+                    f_active++;
+                    open_run();
+                }
+            }
+        }
+        open_rows();
     };
     auto fetch = [&]() {
-        if (f_item < items && f_step < steps) {
-            const uint32_t dst = ring + f_slot * kStageBytes;
+        if (f_step >= steps && f_left > 0) advance();
+        if (f_plain > 0) {
+            const uint8_t *q = f_q;
 #pragma unroll
-            for (int i = 0; i < kWarpRows * 4 / 32; i++) {
-                const int r = (i * 32 + lane) >> 2, c = lane & 3;
-                const int64_t byte = (int64_t)f_step * (kStepCols / 2) + 16 * c;
-                const bool in = r < f_rows && byte < a.k / 2;
-                lane_copy_part<16>(dst + code_at(r, c), in ? f_q + r * a.ld_q + byte : a.q, in ? 16 : 0);
-            }
-            const int g0 = f_step * Sc::kCount, left = (int)(a.k / kGroup) - g0;
-            const bool in = lane < f_rows;
-            Sc::fetch(dst + kCodeBytes + lane * kScaleSlot, in ? f_s + lane * a.ld_s + g0 : scales,
-                      in ? (left < Sc::kCount ? left : Sc::kCount) : 0);
+            for (int i = 0; i < kCopies; i++, q += ld_rows) lane_copy16(f_slot + code_row<kRowTiles>(dst_code, i), q);
+            if (kWarpRows == 32 || lane < kWarpRows) Sc::fetch_plain(f_slot + dst_scale, f_s);
+            f_plain--;
             f_step += kColWarps;
-            if (f_step >= steps) {
-                f_step = col_warp;
-                if (++f_pass >= f_passes) {
-                    f_pass = 0;
-                    f_item += gridDim.x;
-                    open_item();
-                }
+            f_q += kColWarps * kStepBytes;
+            f_s += kColWarps * kScaleCount;
+        } else if (f_left > 0 && f_step < steps) {
+            const bool in_cols = f_step * kStepBytes + 16 * f_col < a.k / 2;
+#pragma unroll
+            for (int i = 0; i < kCopies; i++) {
+                const bool in = in_cols && f_row + kLaneRows * i < f_rows;
+                lane_copy_part<16>(f_slot + code_row<kRowTiles>(dst_code, i), in ? f_q + i * ld_rows : a.q,
+                                   in ? 16 : 0);
             }
+            const int left = (int)(a.k / kGroup) - f_step * kScaleCount;
+            const bool in = lane < f_rows;
+            if (kWarpRows == 32 || lane < kWarpRows)
+                Sc::fetch(f_slot + dst_scale, in ? f_s : scales, in ? (left < kScaleCount ? left : kScaleCount) : 0);
+            f_step += kColWarps;
+            f_q += kColWarps * kStepBytes;
+            f_s += kColWarps * kScaleCount;
         }
         lane_copy_commit();
-        f_slot = f_slot + 1 == kW4Stages ? 0 : f_slot + 1;
+        f_slot = f_slot == ring + (kStages - 1) * kStageBytes ? ring : f_slot + kStageBytes;
     };
-    open_item();
-#pragma unroll
-    for (int i = 0; i < kW4Stages - 1; i++) fetch();
+    if (f_left > 0) {
+        open_run();
+        open_rows();
+    }
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; i++) fetch();
 
-    int slot = 0;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const ExpertRows er = active[item / row_blocks];
-        const int64_t r0 = (item % row_blocks) * kItemRows;
-        const int64_t warp_r0 = r0 + row_warp * kWarpRows;
-        // which rows' 16-bit scales start in the upper half of a word
-        int skew[2 * kRowTiles];
-#pragma unroll
-        for (int i = 0; i < 2 * kRowTiles; i++)
-            skew[i] = sizeof(S) == 2 ? (int)((reinterpret_cast<uintptr_t>(scales + er.expert * a.expert_s +
-                                                                          (warp_r0 + g + 8 * i) * a.ld_s) >> 1) & 1) : 0;
-        for (int p0 = er.lo; p0 < er.hi; p0 += kPassRows) {
-            const int pass_rows = er.hi - p0 < kPassRows ? er.hi - p0 : kPassRows;
-            // this lane's rows of x: row g of each tile
-            const T *x[kTiles];
-#pragma unroll
-            for (int m = 0; m < kTiles; m++) {
-                const int p = p0 + 8 * m + g;
-                int64_t row = -1;
-                if (p < er.hi) {
-                    row = p;
-                    if (kExperts && a.order) row = dbg_ok(a.order + p, 4, false) ? __ldg(a.order + p) / a.top_k : -1;
+    // Staged x: rows p0.. of one expert as FP16, each times a power of two that brings its
+    // largest value below 2^15 (FP16 rows as they are), in the pairs that the codes come in.
+    // BF16 values down to 2^-31 of the row's largest stay exact; smaller ones are rounded to
+    // multiples of at most 2^-38 of it, far below what a binary32 sum with it would keep. A single row is shared out over the CTA, more are
+    // taken by a warp each.
+    auto stage_x = [&](const ExpertRows &er, int p0, int rows) {
+        const int padded = steps * kStepCols;
+        const bool split = rows == 1;
+        const int first = 8 * (split ? (int)threadIdx.x : lane), stride = 8 * (split ? kBlock : 32);
+        for (int r = split ? 0 : warp; r < rows; r += split ? 1 : kWarps) {
+            int row = p0 + r;
+            if (kExperts && a.order) row = dbg_ok(a.order + row, 4, false) ? __ldg(a.order + row) / a.top_k : 0;
+            if (row < 0 || row >= a.x_rows) row = 0;  // a wrong plan
+            const T *src = static_cast<const T *>(a.x) + row * a.ld_x;
+            float up = 1.0f, down = 1.0f;
+            if constexpr (!std::is_same<T, __half>::value) {
+                uint32_t top = 0;  // largest magnitudes' bits, of even and of odd values
+#pragma unroll 4
+                for (int c = first; c < a.k; c += stride) {
+                    const uint4 v = ld_keep_v4(src + c);
+                    top = __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu),
+                                   __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
                 }
-                x[m] = row >= 0 && row < a.x_rows ? static_cast<const T *>(a.x) + row * a.ld_x : nullptr;
+                top = __reduce_max_sync(kFull, max(top >> 16, top & 0xffffu));
+                if (split) {
+                    if (lane == 0) x_top[warp] = top;
+                    __syncthreads();
+#pragma unroll
+                    for (int w = 0; w < kWarps; w++) top = max(top, x_top[w]);
+                }
+                const int e = max((int)(top >> 7), 15);  // biased exponent of the largest value
+                up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+                down = __uint_as_float((uint32_t)(e - 14) << 23);
             }
-            float acc[kRowTiles][kTiles][4] = {};
-            for (int step = col_warp; step < steps; step += kColWarps) {
-                // x of the step: with one or two tiles fetched before the wait for the codes,
-                // with more where it is used, because the registers do not hold it
-                constexpr bool kEarly = kTiles <= 2;
-                uint4 xv[kEarly ? 4 : 1][kTiles];
-                auto fetch_x = [&](int j) {
-                    const int64_t col = (int64_t)step * kStepCols + 32 * j + 8 * t;
+            if (first == 0) x_unscale[r] = down;
+#pragma unroll 4
+            for (int c = first; c < padded; c += stride) {
+                uint32_t h[4] = {0, 0, 0, 0};
+                if (c < a.k) {
+                    const uint4 v = ld_keep_v4(src + c);
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int m = 0; m < kTiles; m++) {
-                        uint4 &v = xv[kEarly ? j : 0][m];
-                        v = make_uint4(0, 0, 0, 0);
-                        if (x[m] && col < a.k && dbg_ok(x[m] + col, 16, false))
-                            v = __ldg(reinterpret_cast<const uint4 *>(x[m] + col));
-                    }
-                };
-                if constexpr (kEarly) {
-#pragma unroll
-                    for (int j = 0; j < 4; j++) fetch_x(j);
-                }
-                lane_copy_wait<kW4Stages - 2>();
-                __syncwarp();
-                fetch();
-                const uint32_t src = ring + slot * kStageBytes;
-                slot = slot + 1 == kW4Stages ? 0 : slot + 1;
-                float s[2 * kRowTiles][Sc::kCount];
-#pragma unroll
-                for (int i = 0; i < 2 * kRowTiles; i++) {
-                    // one 16-bit scale a step: its word's half changes from step to step
-                    const int k = sizeof(S) == 2 && Sc::kCount == 1 ? skew[i] ^ (step & 1) : skew[i];
-                    Sc::read(src + kCodeBytes + (g + 8 * i) * kScaleSlot, k, s[i]);
-                }
-                float c[kRowTiles][kTiles][4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    // codes i and i + 4 share a register, so x is paired the same way
-                    if constexpr (!kEarly) fetch_x(j);
-                    uint32_t b[kTiles][4];
-#pragma unroll
-                    for (int m = 0; m < kTiles; m++) {
-                        const uint4 v = xv[kEarly ? j : 0][m];
-                        b[m][0] = __byte_perm(v.x, v.z, 0x5410);
-                        b[m][1] = __byte_perm(v.x, v.z, 0x7632);
-                        b[m][2] = __byte_perm(v.y, v.w, 0x5410);
-                        b[m][3] = __byte_perm(v.y, v.w, 0x7632);
-                    }
-#pragma unroll
-                    for (int r = 0; r < kRowTiles; r++) {
-                        uint32_t lo[4], hi[4];
-                        Codes<T>::widen(lds_u32(src + code_at(16 * r + g, j) + 4 * t), lo);
-                        Codes<T>::widen(lds_u32(src + code_at(16 * r + g + 8, j) + 4 * t), hi);
-                        const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-                        for (int m = 0; m < kTiles; m++) {
-                            if (m > 0 && 8 * m >= pass_rows) continue;
-                            if (j % kPerScale == 0) c[r][m][0] = c[r][m][1] = c[r][m][2] = c[r][m][3] = 0.0f;
-                            Codes<T>::mma(c[r][m], a0, b[m][0], b[m][1]);
-                            Codes<T>::mma(c[r][m], a1, b[m][2], b[m][3]);
-                            if (j % kPerScale == kPerScale - 1) {
-                                const float s0 = s[2 * r][j / kPerScale], s1 = s[2 * r + 1][j / kPerScale];
-                                acc[r][m][0] = __fmaf_rn(s0, c[r][m][0], acc[r][m][0]);
-                                acc[r][m][1] = __fmaf_rn(s0, c[r][m][1], acc[r][m][1]);
-                                acc[r][m][2] = __fmaf_rn(s1, c[r][m][2], acc[r][m][2]);
-                                acc[r][m][3] = __fmaf_rn(s1, c[r][m][3], acc[r][m][3]);
-                            }
+                    for (int i = 0; i < 4; i++) {
+                        if constexpr (std::is_same<T, __half>::value) {
+                            h[i] = u[i];
+                        } else {
+                            const __half2 p = __floats2half2_rn(__fmul_rn(__uint_as_float(u[i] << 16), up),
+                                                                __fmul_rn(__uint_as_float(u[i] & 0xffff0000u), up));
+                            h[i] = *reinterpret_cast<const uint32_t *>(&p);
                         }
                     }
                 }
+                const uint4 paired = make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
+                                                __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632));
+                *reinterpret_cast<uint4 *>(x_smem + (((c >> 5) * chunk_cap + r) * 4 + ((c >> 3) & 3)) * 16) = paired;
             }
-            // column warps' sums: [col warp][row of x][weight row]
-            __syncthreads();
-            float *mine = sums + col_warp * kPassRows * kSumStride + row_warp * kWarpRows;
+        }
+        __syncthreads();
+    };
+    uint32_t slot = ring;
+    int left = item_hi - item_lo;
+    int at = item_lo / row_blocks, first_block = item_lo - at * row_blocks;
+    for (; left > 0; at++, first_block = 0) {
+        const ExpertRows er = active[at];
+        const int end_block = row_blocks - first_block < left ? row_blocks : first_block + left;
+        left -= end_block - first_block;
+        int next_chunk = er.lo;
+        while (next_chunk < er.hi) {
+            const int chunk = next_chunk;
+            next_chunk = er.hi - chunk > chunk_cap ? chunk + chunk_cap : er.hi;
+            if constexpr (kStaged) {
+                __syncthreads();  // the last readers of the rows before
+                stage_x(er, chunk, next_chunk - chunk);
+            }
+            for (int block = first_block; block < end_block; block++) {
+                const int r0 = block * kItemRows;
+                // rows g + 8 i all start in the same half of a word
+                const int row_skew = (int)(er.expert * a.expert_s + (r0 + row_warp * kWarpRows + g) * a.ld_s) & 1;
+                for (int p0 = chunk; p0 < next_chunk; p0 += pass_cap) {
+                    const int pass_rows = next_chunk - p0 < pass_cap ? next_chunk - p0 : pass_cap;
+                    const int in_chunk = kStaged ? p0 - chunk : 0;
+                    // This lane's rows of x, column g of each tile. Columns past the last row repeat
+                    // it: their products are not stored.
+                    const T *x[kTiles];
+                    uint4 xv[kStaged ? 1 : kParts][kTiles];
+                    uint32_t x_src = 0;
+                    if constexpr (kStaged) {
+                        const int r = kEven ? g / 2 : g;
+                        const int last = pass_rows - 1;
+                        const int row = in_chunk + (r < last ? r : last);
+                        x_src = smem_u32(x_smem) + ((col_warp * kParts * chunk_cap + row) * 4 + t) * 16;
+                    }
 #pragma unroll
-            for (int r = 0; r < kRowTiles; r++)
+                    for (int m = 0; m < (kStaged ? 0 : kTiles); m++) {
+                        const int want = p0 + 8 * m + (kEven ? g / 2 : g), p = want < er.hi ? want : er.hi - 1;
+                        int row = p;
+                        if (kExperts && a.order) row = dbg_ok(a.order + p, 4, false) ? __ldg(a.order + p) / a.top_k : 0;
+                        if (row < 0 || row >= a.x_rows) row = 0;  // a wrong plan
+                        x[m] = static_cast<const T *>(a.x) + row * a.ld_x + 8 * t + col_warp * kStepCols;
+                    }
+                    // x of a step is loaded at the end of the step before it
+                    auto load_x = [&](int step) {
+                        if constexpr (kStaged) return;
+                        if (step < whole_steps) {
 #pragma unroll
-                for (int m = 0; m < kTiles; m++)
+                            for (int j = 0; j < kParts; j++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        mine[(8 * m + 2 * t + (i & 1)) * kSumStride + 16 * r + g + 8 * (i >> 1)] = acc[r][m][i];
-            __syncthreads();
-            for (int i = threadIdx.x; i < pass_rows * kItemRows; i += kThreads) {
-                const int m = i / kItemRows, r = i % kItemRows;
-                float v = sums[m * kSumStride + r];
+                                for (int m = 0; m < kTiles; m++) xv[kStaged ? 0 : j][m] = ld_keep_v4(x[m] + 32 * j);
+                        } else if (step < steps) {
 #pragma unroll
-                for (int w = 1; w < kColWarps; w++) v = __fadd_rn(v, sums[(w * kPassRows + m) * kSumStride + r]);
-                T *dst = static_cast<T *>(a.out) + (p0 + m) * a.ld_out + r0 + r;
-                if (r0 + r < a.n && dbg_ok(dst, sizeof(T), true)) *reinterpret_cast<Bits *>(dst) = Value<T>::round(v);
+                            for (int j = 0; j < kParts; j++)
+#pragma unroll
+                                for (int m = 0; m < kTiles; m++)
+                                    xv[kStaged ? 0 : j][m] = step * kStepCols + 32 * j < a.k
+                                                                 ? ld_keep_v4(x[m] + 32 * j) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int m = 0; m < kTiles; m++) x[m] += kColWarps * kStepCols;
+                    };
+                    load_x(col_warp);
+                    float acc[kRowTiles][kTiles][4] = {};  // with even columns only, [0] and [2] are used
+                    float c[kRowTiles][kTiles][4];
+                    for (int step = col_warp; step < steps; step += kColWarps) {
+                        lane_copy_wait<kStages - 2>();
+                        __syncwarp();
+                        fetch();
+                        // piece j of the rows g + 8 r: their lines are all permuted alike
+                        const uint32_t src = slot + code_at<kRowTiles>(g, 0) + 4 * t;
+                        const uint32_t src_s = slot + kStepCodeBytes + g * kScaleSlot;
+                        uint32_t s[2 * kRowTiles][Sc::kWords];
+                        if (skewed) {
+                            const int skew = (row_skew + step * kScaleCount) & 1;
+#pragma unroll
+                            for (int i = 0; i < 2 * kRowTiles; i++)
+                                Sc::read_skewed(src_s + 8 * kScaleSlot * i, skew, s[i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2 * kRowTiles; i++) Sc::read(src_s + 8 * kScaleSlot * i, s[i]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kParts; j++) {
+                            // the A fragments of two mma: rows g and g + 8 alternate
+                            uint32_t codes[kRowTiles][8];
+#pragma unroll
+                            for (int r = 0; r < kRowTiles; r++) {
+                                constexpr int kEightRows = 8 * kStepBytes;
+                                uint32_t lo[4], hi[4];
+                                Codes<Product>::widen(lds_u32((src ^ (16 * j)) + 2 * kEightRows * r), lo);
+                                Codes<Product>::widen(lds_u32((src ^ (16 * j)) + 2 * kEightRows * r + kEightRows), hi);
+#pragma unroll
+                                for (int i = 0; i < 4; i++) {
+                                    codes[r][2 * i] = lo[i];
+                                    codes[r][2 * i + 1] = hi[i];
+                                }
+                            }
+                            // codes i and i + 4 share a register, so x is paired the same way
+                            uint32_t b[kTiles][4];
+#pragma unroll
+                            for (int m = 0; m < kTiles; m++) {
+                                if constexpr (kStaged) {
+                                    const uint4 v = lds_v4(x_src + j * 64 * chunk_cap);
+                                    b[m][0] = v.x, b[m][1] = v.y, b[m][2] = v.z, b[m][3] = v.w;
+                                } else {
+                                    const uint4 v = xv[j][m];
+                                    b[m][0] = __byte_perm(v.x, v.z, 0x5410), b[m][1] = __byte_perm(v.x, v.z, 0x7632);
+                                    b[m][2] = __byte_perm(v.y, v.w, 0x5410), b[m][3] = __byte_perm(v.y, v.w, 0x7632);
+                                }
+                            }
+#pragma unroll
+                            for (int m = 0; m < kTiles; m++)
+#pragma unroll
+                                for (int r = 0; r < kRowTiles; r++)
+                                    if (j % kPerScale == 0)
+                                        Codes<Product>::template mma<true>(c[r][m], codes[r], b[m][0], b[m][1]);
+                                    else
+                                        Codes<Product>::template mma<false>(c[r][m], codes[r], b[m][0], b[m][1]);
+#pragma unroll
+                            for (int m = 0; m < kTiles; m++)
+#pragma unroll
+                                for (int r = 0; r < kRowTiles; r++)
+                                    Codes<Product>::template mma<false>(c[r][m], codes[r] + 4, b[m][2], b[m][3]);
+                            if (j % kPerScale == kPerScale - 1) {
+#pragma unroll
+                                for (int r = 0; r < kRowTiles; r++) {
+                                    const float s0 = Sc::at(s[2 * r], j / kPerScale);
+                                    const float s1 = Sc::at(s[2 * r + 1], j / kPerScale);
+#pragma unroll
+                                    for (int m = 0; m < kTiles; m++)
+#pragma unroll
+                                        for (int i = 0; i < 4; i += kEven ? 2 : 1)
+                                            acc[r][m][i] = __fmaf_rn(i < 2 ? s0 : s1, c[r][m][i], acc[r][m][i]);
+                                }
+                            }
+                        }
+                        if constexpr (kStaged)
+                            x_src += kColWarps * kParts * 64 * chunk_cap;
+                        else
+                            load_x(step + kColWarps);
+                        slot = slot == ring + (kStages - 1) * kStageBytes ? ring : slot + kStageBytes;
+                    }
+                    // column warps' sums: [col warp][row of x][weight row]
+                    __syncthreads();  // the readers of the item before
+                    float *mine = sums + col_warp * kPassRows * kSumStride + row_warp * kWarpRows;
+#pragma unroll
+                    for (int r = 0; r < kRowTiles; r++)
+#pragma unroll
+                        for (int m = 0; m < kTiles; m++)
+#pragma unroll
+                            for (int i = 0; i < 4; i += kEven ? 2 : 1)
+                                mine[(kEven ? t : 8 * m + 2 * t + (i & 1)) * kSumStride + 16 * r + g + 8 * (i >> 1)] =
+                                    acc[r][m][i];
+                    __syncthreads();
+                    for (int i = threadIdx.x; i < pass_rows * kItemRows; i += kBlock) {
+                        const int m = i / kItemRows, r = i % kItemRows;
+                        float v = sums[m * kSumStride + r];
+#pragma unroll
+                        for (int w = 1; w < kColWarps; w++)
+                            v = __fadd_rn(v, sums[(w * kPassRows + m) * kSumStride + r]);
+                        if (kStaged) v = __fmul_rn(v, x_unscale[in_chunk + m]);
+                        T *dst = static_cast<T *>(a.out) + (p0 + m) * a.ld_out + r0 + r;
+                        if (r0 + r < a.n && dbg_ok(dst, sizeof(T), true))
+                            *reinterpret_cast<Bits *>(dst) = Value<T>::round(v);
+                    }
+                }
             }
         }
     }
     lane_copy_wait<0>();
     if constexpr (kExperts) {
         for (int64_t p = kept + blockIdx.x; p < a.slots; p += gridDim.x)
-            for (int64_t c = threadIdx.x; c < a.n; c += kThreads) {
+            for (int64_t c = threadIdx.x; c < a.n; c += kBlock) {
                 T *dst = static_cast<T *>(a.out) + p * a.ld_out + c;
                 if (dbg_ok(dst, sizeof(T), true)) *reinterpret_cast<Bits *>(dst) = 0;
             }
     }
 }
 
-template <class T, class S, int kGroup, int kTiles, int kRowWarps, bool kExperts>
-cudaError_t launch_w4(const W4Args &a, cudaStream_t st)
+template <class Shape>
+cudaError_t launch_w4(W4Args a, cudaStream_t st)
 {
-    constexpr int kColWarps = kW4Warps / kRowWarps;
-    constexpr size_t smem = kW4Warps * kW4Stages * kStageBytes +
-                            sizeof(float) * kColWarps * 8 * kTiles * (kWarpRows * kRowWarps + 4);
-    auto kernel = matvec_w4_kernel<T, S, kGroup, kTiles, kRowWarps, kExperts>;
-    const int64_t blocks = (a.n + kWarpRows * kRowWarps - 1) / (kWarpRows * kRowWarps);
-    const int64_t with_rows = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
+    auto kernel = matvec_w4_kernel<Shape>;
+    const int64_t blocks = (a.n + Shape::kItemRows - 1) / Shape::kItemRows;
+    const int64_t with_rows = !Shape::kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
+    size_t smem = Shape::kRingBytes + Shape::kSumBytes + sizeof(ExpertRows) * a.n_experts;
+    if (Shape::kStaged) smem = (smem + 15) / 16 * 16 + staged_row_bytes(a.k) * a.staged_rows;
     int grid = 0;
-    if (cudaError_t e = grid_for((const void *)kernel, blocks * with_rows * kW4Warps, &grid, smem)) return e;
-    return launch_kernel_smem(kernel, grid, smem, st, a);
+    if (cudaError_t e = grid_for((const void *)kernel, blocks * with_rows * Shape::kWarps, &grid, smem, Shape::kBlock))
+        return e;
+    int sms = 1;
+    if (cudaError_t e = sm_count(&sms)) return e;
+    a.ctas_per_sm = grid % sms == 0 ? grid / sms : 1;
+    return launch_kernel_block(kernel, grid, Shape::kBlock, smem, st, a);
 }
 
-template <class T, class S, int kGroup>
-cudaError_t launch_w4_rows(const W4Args &a, cudaStream_t st)
+template <class T, class S, int kGroup, bool kExperts>
+cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
 {
-    if (a.offsets) {
-        return a.slots <= 4 * (int64_t)a.n_experts ? launch_w4<T, S, kGroup, 1, 1, true>(a, st)
-                                                   : launch_w4<T, S, kGroup, 4, 2, true>(a, st);
+    const int64_t cap = kStagedBytes / staged_row_bytes(a.k);
+    if (rows <= 4 && rows <= cap) {
+        const int64_t most = kExperts ? cap : rows;
+        a.staged_rows = (int)(most < 4 ? most : most / 4 * 4);
+        return launch_w4<W4Shape<T, S, kGroup, 4, 1, 1, 8, 3, 2, true, kExperts>>(a, st);
     }
-    return a.slots <= 8 ? launch_w4<T, S, kGroup, 1, 1, false>(a, st) : launch_w4<T, S, kGroup, 4, 2, false>(a, st);
+    if (rows <= 8) return launch_w4<W4Shape<T, S, kGroup, 8, 2, 1, 8, 3, 2, false, kExperts>>(a, st);
+    const int64_t tiles = (a.n + 31) / 32 * (kExperts ? (a.slots < a.n_experts ? a.slots : a.n_experts) : 1);
+    return tiles >= 480 ? launch_w4<W4Shape<T, S, kGroup, 16, 2, 4, 4, 3, 1, false, kExperts>>(a, st)
+                        : launch_w4<W4Shape<T, S, kGroup, 16, 2, 1, 8, 3, 2, false, kExperts>>(a, st);
+}
+
+template <class T, class S, bool kExperts>
+cudaError_t launch_w4_group(int group, const W4Args &a, cudaStream_t st)
+{
+    // the rows that a matrix is used for; with experts twice the average, for their spread
+    const int64_t rows = kExperts ? (2 * a.slots + a.n_experts - 1) / a.n_experts : a.slots;
+    switch (group) {
+    case 32: return launch_w4_rows<T, S, 32, kExperts>(a, rows, st);
+    case 64: return launch_w4_rows<T, S, 64, kExperts>(a, rows, st);
+    default: return launch_w4_rows<T, S, 128, kExperts>(a, rows, st);
+    }
 }
 
 template <class T, class S>
-cudaError_t launch_w4_group(int group, const W4Args &a, cudaStream_t st)
+cudaError_t launch_w4_kind(int group, const W4Args &a, cudaStream_t st)
 {
-    switch (group) {
-    case 32: return launch_w4_rows<T, S, 32>(a, st);
-    case 64: return launch_w4_rows<T, S, 64>(a, st);
-    default: return launch_w4_rows<T, S, 128>(a, st);
-    }
+    return a.offsets ? launch_w4_group<T, S, true>(group, a, st) : launch_w4_group<T, S, false>(group, a, st);
 }
 
 }  // namespace
@@ -442,10 +776,10 @@ cudaError_t launch_w4_group(int group, const W4Args &a, cudaStream_t st)
 cudaError_t launch_matvec_w4(int x_type, int scale_type, int group, const W4Args &a, cudaStream_t st)
 {
     if (x_type == kBf16)
-        return scale_type == kF32 ? launch_w4_group<__nv_bfloat16, float>(group, a, st)
-                                  : launch_w4_group<__nv_bfloat16, __nv_bfloat16>(group, a, st);
-    return scale_type == kF32 ? launch_w4_group<__half, float>(group, a, st)
-                              : launch_w4_group<__half, __half>(group, a, st);
+        return scale_type == kF32 ? launch_w4_kind<__nv_bfloat16, float>(group, a, st)
+                                  : launch_w4_kind<__nv_bfloat16, __nv_bfloat16>(group, a, st);
+    return scale_type == kF32 ? launch_w4_kind<__half, float>(group, a, st)
+                              : launch_w4_kind<__half, __half>(group, a, st);
 }
 
 cudaError_t read_wait_counters_w4(unsigned long long (&v)[3]) { return read_wait_counters(v); }

@@ -315,6 +315,7 @@ typedef enum { BQ_BF16 = 0, BQ_F16 = 1, BQ_F32 = 2 } bq_row_type;
 #define BQ_MAX_TOP_K 64
 #define BQ_MAX_EXPERTS 1024
 #define BQ_SORT_PARTS 128
+#define BQ_MAX_W4_DIM 16777216 /* most rows and columns of a 4-bit weight matrix */
 
 /* Sorts the slots of a batch by expert, stably: within an expert places go by slot.
  *   ids        [tokens][top_k] int32, or int64 when ids_are_i64 != 0 (read)
@@ -364,9 +365,12 @@ BQ_API bq_status bq_expert_combine_grad(const void *dout, int type, int64_t ld_d
  *   group   32, 64 or 128 columns per scale; k % group == 0
  *   out     [rows][ld_out] of x's type (written)
  * A group's sum of x * code is exact products added in binary32; it is multiplied by the
- * scale and added to the output's sum in binary32. Any number of rows is right; the
+ * scale and added to the output's sum in binary32. BF16 rows may pass through FP16, each
+ * times a power of two: values below 2^-31 of their row's largest then count as the nearest
+ * multiple of 2^-38 of it (at most). Any number of rows is right; the
  * kernels are made for up to 32, and read the weights once for every 32 rows (8 rows up
- * to that number). A wrong group, type or k returns BQ_ERR_SHAPE. */
+ * to that number). A wrong group, type or k returns BQ_ERR_SHAPE;
+ * n and k are at most BQ_MAX_W4_DIM. */
 BQ_API bq_status bq_matvec_w4(const void *x, int type, int64_t rows, int64_t k, int64_t ld_x, const uint8_t *q,
                               int64_t n, int64_t ld_q, const void *scales, int scale_type, int group, int64_t ld_s,
                               void *out, int64_t ld_out, cudaStream_t stream);

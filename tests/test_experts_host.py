@@ -76,6 +76,7 @@ def test_matvec_w4_rejections(bq_lib):
     assert f(type=F32) == SHAPE and f(s_type=F16) == SHAPE and f(type=F16) == SHAPE  # scales of the other 16-bit type
     assert f(group=16) == SHAPE and f(group=96) == SHAPE and f(k=288, ld_x=288, ld_q=144, ld_s=5) == SHAPE
     assert f(k=-64) == SHAPE and f(rows=-1) == SHAPE and f(n=-1) == SHAPE
+    assert f(n=2 ** 24 + 1) == SHAPE and f(rows=2 ** 31) == SHAPE
     assert f(ld_x=248) == SHAPE and f(ld_q=112) == SHAPE and f(ld_s=3) == SHAPE and f(ld_out=31) == SHAPE
     for name in ("x", "q", "s", "out"):
         assert f(**{name: None}) == NULL

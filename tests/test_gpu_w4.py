@@ -54,7 +54,9 @@ def guarded_out(rows, n, dtype, pad=0):
 
 
 # rows, n, k, paddings of x, q, scales, out
-DENSE = [(1, 1, 128, 0, 0, 0, 0), (1, 7168, 1024, 0, 0, 0, 0), (1, 33, 7168, 0, 0, 0, 0), (2, 100, 384, 8, 16, 2, 3),
+DENSE = [(1, 1, 128, 0, 0, 0, 0), (1, 7168, 1024, 0, 0, 0, 0), (3, 96, 7168, 8, 0, 1, 0), (4, 47, 7168, 0, 16, 0, 5),
+         (4, 200, 4096, 0, 0, 0, 0), (5, 33, 768, 0, 0, 0, 0), (16, 15400, 256, 0, 0, 0, 0),
+         (1, 33, 7168, 0, 0, 0, 0), (2, 100, 384, 8, 16, 2, 3),
          (7, 65, 640, 0, 0, 0, 0), (8, 129, 2176, 16, 0, 1, 0), (9, 64, 1152, 0, 32, 3, 1), (16, 300, 896, 0, 0, 0, 0),
          (17, 31, 256, 0, 0, 0, 0), (32, 515, 4224, 0, 0, 0, 0), (33, 50, 1408, 0, 0, 0, 0), (100, 97, 512, 0, 0, 0, 0)]
 
@@ -95,7 +97,7 @@ def test_matvec_with_columns_that_end_inside_a_step(k):
 # tokens, top_k, n_experts, n, k, group
 EXPERTS = [(1, 1, 1, 16, 128, 128), (1, 8, 64, 100, 512, 32), (3, 2, 5, 33, 256, 64), (24, 6, 48, 70, 1024, 64),
            (32, 8, 8, 65, 384, 128), (50, 4, 3, 40, 640, 32), (200, 2, 300, 20, 256, 64), (700, 3, 9, 24, 128, 32),
-           (2, 3, 1024, 16, 128, 64)]
+           (2, 3, 1024, 16, 128, 64), (20, 1, 40, 50, 7168, 32), (3, 6, 20, 2000, 384, 128)]
 
 
 @pytest.mark.parametrize("by_token", [True, False])
@@ -106,6 +108,8 @@ def test_matvec_experts(shape, name, by_token):
     dtype, p, tiny = TYPES[name]
     rng = np.random.default_rng(tokens * 7 + n)
     ids = ids_of(rng, tokens, top_k, n_experts, skew=True)
+    if top_k == 1:
+        ids[::2] = 3  # one expert with far more rows than the average
     offsets, order, _ = plan_of(ids, n_experts)
     slots, kept = tokens * top_k, int(offsets[-1])
     q, s, w = make_weights(rng, (n_experts,), n, k, group, dtype if by_token else torch.float32)
@@ -124,18 +128,43 @@ def test_matvec_experts(shape, name, by_token):
     assert not out[kept:].any() and g.bands_intact()
 
 
-def test_an_infinite_row_leaves_the_others_alone():
+@pytest.mark.parametrize("rows", [4, 5, 12])
+@pytest.mark.parametrize("name", list(TYPES))
+def test_an_infinite_row_leaves_the_others_alone(rows, name):
     rng = np.random.default_rng(3)
-    q, s, _ = make_weights(rng, (), 48, 256, 32, torch.bfloat16)
-    x, _ = make_x(rng, 5, 256, torch.bfloat16)
-    clean = torch.empty((5, 48), dtype=torch.bfloat16, device="cuda")
+    dtype = TYPES[name][0]
+    q, s, w = make_weights(rng, (), 48, 256, 32, dtype)
+    x, _ = make_x(rng, rows, 256, dtype)
+    clean = torch.empty((rows, 48), dtype=dtype, device="cuda")
     w4.matvec_w4(x, q, s, clean)
     x[2, 7], x[3, 9] = float("inf"), float("nan")
     out = torch.empty_like(clean)
     w4.matvec_w4(x, q, s, out)
-    assert not bool(out[2].isfinite().any()) and bool(out[3].isnan().all())
-    for r in (0, 1, 4):
+    code = torch.from_numpy(w[:, 7]).cuda()
+    assert torch.equal(out[2] == float("inf"), code > 0) and torch.equal(out[2] == float("-inf"), code < 0)
+    assert torch.equal(out[2].isnan(), code == 0) and bool(out[3].isnan().all())
+    for r in set(range(rows)) - {2, 3}:
         assert torch.equal(out[r], clean[r])
+
+
+def test_values_far_below_their_rows_largest():
+    # through FP16 a BF16 row's values below 2^-31 of its largest are off by at most 2^-39 of it
+    rng = np.random.default_rng(21)
+    k, n = 1024, 64
+    q, s, w = make_weights(rng, (), n, k, 64, torch.bfloat16)
+    x32 = (rng.standard_normal((3, k)) * 2.0 ** rng.integers(-45, 0, (3, k))).astype(np.float32)
+    x32[:, 100] = [2.0 ** 20, 3.0e38, 2.0 ** -100]
+    x = torch.from_numpy(x32).to(torch.bfloat16).cuda()
+    x64 = x.double().cpu().numpy()
+    for cleared in (False, True):
+        if cleared:
+            q[:, 50] = q[:, 50] & 0xF0  # column 100's codes: the largest value takes no part
+            w[:, 100] = 0.0
+        out = torch.empty((3, n), dtype=torch.bfloat16, device="cuda")
+        w4.matvec_w4(x, q, s, out)
+        terms = np.abs(x64) @ np.abs(w).T
+        terms += 2.0 ** -16 / (64 + 16 + 16) * np.abs(x64).max(1)[:, None] * np.abs(w).sum(1)  # 2^-39 in check's unit
+        check(out, x64 @ w.T, terms, k, 64, 8, 2.0 ** -134)
 
 
 def test_rows_do_not_depend_on_their_company():
