@@ -15,17 +15,26 @@ namespace {
 // ---------------------------------------------------------------- sort
 // A stable counting sort. Every warp owns a run of consecutive slots and a row of
 // counters in shared memory, one per expert. It counts its slots 32 at a time:
-// match_any gives each lane the lanes with the same id, and the lowest of them adds
-// their number, so no counter is ever contended. The counters are then turned into the
+// match_any gives each lane the lanes with the same id, and the lowest of them adds their
+// number, so no counter is ever contended. (A ballot per bit of the id instead took 13.1
+// us for 524288 slots of 64 experts, match_any 11.4.) The counters are then turned into the
 // first place of each (warp, expert), and a second walk over the same slots hands the
 // places out in lane order. Nothing depends on the order in which warps run.
 //
+// Lane w of a warp holds warp w's counter when the counters are summed or scanned over the
+// warps; a row of counters has an odd stride, so that these 32 lie in different banks.
+//
 // Up to kSortOneCta slots one CTA does all of it in one launch. More slots are cut into
-// `parts` runs, one CTA each: a first launch writes each run's counts to the workspace,
-// the second adds up the runs before its own and all runs, and places.
+// `parts` runs, one CTA each: a first launch writes each run's counts to the workspace, the
+// second adds up the runs before its own and all runs, and places. An SM stores at most one
+// of the scattered places per cycle: 12728 slots took 22.4 us in one CTA, 7.8 us in two
+// launches of 13.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int64_t kSortOneCta = 4096;
+constexpr int kFewWarps = 8;  // counters of so few warps are scanned by a thread per expert
+static_assert(kSortWarps == 32, "a lane per warp");
+__host__ __device__ constexpr int count_stride(int n_experts) { return n_experts | 1; }
 
 // The id of slot i, or -1 where the slot is dropped.
 __device__ __forceinline__ int slot_expert(const int32_t *ids, int64_t i, int n_experts)
@@ -60,16 +69,40 @@ __device__ __forceinline__ SlotRun warp_run(int64_t slots, int parts, int part, 
     return SlotRun{lo < slots ? lo : slots, hi < slots ? hi : slots};
 }
 
-// count[w][e] over this CTA's run; the caller synchronizes.
+// The experts of a warp's next kAhead batches of 32 slots, this lane's slot of each: loaded
+// together, so that their latencies overlap.
+constexpr int kAhead = 4;
 template <class Id>
-__device__ __forceinline__ void count_run(const Id *ids, SlotRun run, int n_experts, int *mine, int lane)
+__device__ __forceinline__ void load_experts(const Id *ids, int64_t i0, int64_t hi, int n_experts, int lane,
+                                             int (&e)[kAhead])
 {
-    for (int64_t i0 = run.lo; i0 < run.hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int e = i < run.hi ? slot_expert(ids, i, n_experts) : -1;
-        const unsigned same = __match_any_sync(kFull, e);
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kAhead; k++) {
+        const int64_t i = i0 + 32 * k + lane;
+        e[k] = i < hi ? slot_expert(ids, i, n_experts) : -1;
+    }
+}
+
+// count[w][e] over this CTA's run, e0 its first batches; the caller synchronizes.
+template <class Id>
+__device__ __forceinline__ void count_run(const Id *ids, SlotRun run, int n_experts, const int (&e0)[kAhead], int *mine,
+                                          int lane)
+{
+    int e[kAhead];
+    for (int64_t i0 = run.lo; i0 < run.hi; i0 += 32 * kAhead) {
+        if (i0 == run.lo) {
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) e[k] = e0[k];
+        } else {
+            load_experts(ids, i0, run.hi, n_experts, lane, e);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            if (i0 + 32 * k >= run.hi) break;
+            const unsigned same = __match_any_sync(kFull, e[k]);
+            if (e[k] >= 0 && lane == __ffs(same) - 1) mine[e[k]] += __popc(same);
+            __syncwarp();
+        }
     }
 }
 
@@ -77,21 +110,24 @@ template <class Id>
 __global__ void __launch_bounds__(kSortThreads)
 sort_count_kernel(const Id *__restrict__ ids, int64_t slots, int n_experts, int parts, int32_t *__restrict__ ws)
 {
-    extern __shared__ int count[];  // [kSortWarps][n_experts]
+    extern __shared__ int count[];  // [kSortWarps][count_stride(n_experts)]
     pdl_begin();
     dbg_begin();
     dbg_allow(ids, slots * (int64_t)sizeof(Id), false);
     dbg_allow(ws, 4ll * parts * n_experts, true);
     dbg_ready();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kSortWarps * n_experts; i += kSortThreads) count[i] = 0;
+    const int stride = count_stride(n_experts);
+    const SlotRun run = warp_run(slots, parts, blockIdx.x, warp);
+    int e0[kAhead];
+    load_experts(ids, run.lo, run.hi, n_experts, lane, e0);
+    for (int i = threadIdx.x; i < kSortWarps * stride; i += kSortThreads) count[i] = 0;
     __syncthreads();
-    count_run(ids, warp_run(slots, parts, blockIdx.x, warp), n_experts, count + warp * n_experts, lane);
+    count_run(ids, run, n_experts, e0, count + warp * stride, lane);
     __syncthreads();
-    for (int e = threadIdx.x; e < n_experts; e += kSortThreads) {
-        int sum = 0;
-        for (int w = 0; w < kSortWarps; w++) sum += count[w * n_experts + e];
-        st_i32(ws + (int64_t)blockIdx.x * n_experts + e, sum);
+    for (int e = warp; e < n_experts; e += kSortWarps) {
+        const int sum = __reduce_add_sync(kFull, count[lane * stride + e]);
+        if (lane == 0) st_i32(ws + (int64_t)blockIdx.x * n_experts + e, sum);
     }
 }
 
@@ -100,7 +136,7 @@ __global__ void __launch_bounds__(kSortThreads)
 sort_place_kernel(const Id *__restrict__ ids, int64_t slots, int n_experts, int parts, const int32_t *__restrict__ ws,
                   int32_t *__restrict__ offsets, int32_t *__restrict__ order, int32_t *__restrict__ inverse)
 {
-    extern __shared__ int count[];  // [kSortWarps][n_experts], then total and before [n_experts] each
+    extern __shared__ int count[];  // [kSortWarps][count_stride(n_experts)], then total and before [n_experts]
     __shared__ int warp_sum[32];
     pdl_begin();
     dbg_begin();
@@ -111,12 +147,19 @@ sort_place_kernel(const Id *__restrict__ ids, int64_t slots, int n_experts, int 
     dbg_allow(inverse, 4 * slots, true);
     dbg_ready();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = blockIdx.x;
-    int *total = count + kSortWarps * n_experts, *before = total + n_experts;
-    for (int i = threadIdx.x; i < (kSortWarps + 2) * n_experts; i += kSortThreads) count[i] = 0;
-    __syncthreads();
+    const int stride = count_stride(n_experts);
+    int *total = count + kSortWarps * stride, *before = total + n_experts;
     const SlotRun run = warp_run(slots, parts, part, warp);
-    int *mine = count + warp * n_experts;
-    count_run(ids, run, n_experts, mine, lane);
+    int e0[kAhead];
+    load_experts(ids, run.lo, run.hi, n_experts, lane, e0);
+    // warps past the last slot have nothing to count, and their counters are not used
+    const int64_t batches = (slots + 31) / 32;
+    const int busy = parts == 1 && batches < kSortWarps ? (int)batches : kSortWarps;
+    for (int i = threadIdx.x; i < busy * stride; i += kSortThreads) count[i] = 0;
+    for (int i = threadIdx.x; i < 2 * n_experts; i += kSortThreads) total[i] = 0;
+    __syncthreads();
+    int *mine = count + warp * stride;
+    count_run(ids, run, n_experts, e0, mine, lane);
     // Sums over the runs: thread group g of the expert takes every groups-th run. Integer
     // additions, so their order does not matter.
     if (parts > 1) {
@@ -135,18 +178,31 @@ sort_place_kernel(const Id *__restrict__ ids, int64_t slots, int n_experts, int 
         }
     }
     __syncthreads();
-    // Thread e: the expert's counts over the warps become first places within the run, and
-    // a scan over the experts gives its first place among all.
-    const int e = threadIdx.x;
-    int run_total = 0;
-    if (e < n_experts) {
-        for (int w = 0; w < kSortWarps; w++) {
-            const int v = count[w * n_experts + e];
-            count[w * n_experts + e] = run_total;
-            run_total += v;
+    // An expert's counts over the warps become first places within the run.
+    for (int e = threadIdx.x; busy <= kFewWarps && e < n_experts; e += kSortThreads) {
+        int upto = 0;
+        for (int w = 0; w < busy; w++) {
+            const int v = count[w * stride + e];
+            count[w * stride + e] = upto;
+            upto += v;
         }
+        total[e] = upto;
     }
-    const int all = e < n_experts ? (parts > 1 ? total[e] : run_total) : 0;
+    for (int e = warp; busy > kFewWarps && e < n_experts; e += kSortWarps) {
+        const int v = lane < busy ? count[lane * stride + e] : 0;
+        int upto = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(kFull, upto, d);
+            if (lane >= d) upto += up;
+        }
+        if (lane < busy) count[lane * stride + e] = upto - v;
+        if (parts == 1 && lane == 31) total[e] = upto;
+    }
+    __syncthreads();
+    // Thread e: a scan over the experts gives the expert's first place among all.
+    const int e = threadIdx.x;
+    const int all = e < n_experts ? total[e] : 0;
     int scan = all;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -168,26 +224,31 @@ sort_place_kernel(const Id *__restrict__ ids, int64_t slots, int n_experts, int 
     const int first = scan - all + (warp > 0 ? warp_sum[warp - 1] : 0);
     const int kept = warp_sum[31];
     if (e < n_experts) {
-        for (int w = 0; w < kSortWarps; w++) count[w * n_experts + e] += first + before[e];
+        before[e] += first;
         if (part == 0) {
             st_i32(offsets + e, first);
             if (e == n_experts - 1) st_i32(offsets + n_experts, kept);
         }
     }
     __syncthreads();
-    for (int64_t i0 = run.lo; i0 < run.hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int id = i < run.hi ? slot_expert(ids, i, n_experts) : -1;
-        const unsigned same = __match_any_sync(kFull, id);
-        int place = -1;
-        if (id >= 0) {
-            place = mine[id] + __popc(same & ((1u << lane) - 1u));
-            st_i32(order + place, static_cast<int32_t>(i));
+    for (int64_t i0 = run.lo; i0 < run.hi; i0 += 32 * kAhead) {
+        if (i0 != run.lo) load_experts(ids, i0, run.hi, n_experts, lane, e0);
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+            const int64_t i = i0 + 32 * k + lane;
+            if (i0 + 32 * k >= run.hi) break;
+            const int id = e0[k];
+            const unsigned same = __match_any_sync(kFull, id);
+            int place = -1;
+            if (id >= 0) {
+                place = before[id] + mine[id] + __popc(same & ((1u << lane) - 1u));
+                st_i32(order + place, static_cast<int32_t>(i));
+            }
+            if (i < run.hi) st_i32(inverse + i, place);
+            __syncwarp();
+            if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
+            __syncwarp();
         }
-        if (i < run.hi) st_i32(inverse + i, place);
-        __syncwarp();
-        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
-        __syncwarp();
     }
     // places that no slot takes
     for (int64_t p = kept + (int64_t)part * kSortThreads + threadIdx.x; p < slots; p += (int64_t)parts * kSortThreads)
@@ -203,8 +264,9 @@ cudaError_t launch_sort(const Id *ids, int64_t slots, int n_experts, int32_t *of
         const int64_t need = (slots + kSortThreads - 1) / kSortThreads;
         parts = static_cast<int>(need < kSortParts ? need : kSortParts);
     }
-    const size_t smem_count = sizeof(int) * kSortWarps * n_experts, smem = smem_count + sizeof(int) * 2 * n_experts;
-    const size_t smem_max = sizeof(int) * (kSortWarps + 2) * kMaxExperts;
+    const size_t smem_count = sizeof(int) * kSortWarps * count_stride(n_experts);
+    const size_t smem = smem_count + sizeof(int) * 2 * n_experts;
+    const size_t smem_max = sizeof(int) * (kSortWarps * count_stride(kMaxExperts) + 2 * kMaxExperts);
     int grid = 0;  // not used: grid_for raises the kernels' shared memory limit
     auto place = sort_place_kernel<Id>;
     if (cudaError_t e = grid_for((const void *)place, 1, &grid, smem_max, kSortThreads)) return e;
@@ -246,7 +308,8 @@ __global__ void __launch_bounds__(kThreads)
 gather_kernel(const T *__restrict__ x, int64_t tokens, int64_t hidden, int64_t ld_x, const int32_t *__restrict__ inverse,
               int top_k, const int32_t *__restrict__ offsets, int n_experts, T *__restrict__ out, int64_t ld_out)
 {
-    using P = Piece<T, kWide>;
+    using P = Piece<T>;
+    using C = Cut<T, kWide>;
     pdl_begin();
     const int64_t slots = tokens * top_k;
     dbg_begin();
@@ -255,43 +318,65 @@ gather_kernel(const T *__restrict__ x, int64_t tokens, int64_t hidden, int64_t l
     dbg_allow(offsets, 4ll * (n_experts + 1), false);
     dbg_allow_2d(out, slots, hidden * sizeof(T), ld_out * sizeof(T), true);
     dbg_ready();
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    constexpr int kSegment = 32 * P::N * kGatherPieces;
-    const int64_t segments = (hidden + kSegment - 1) / kSegment;
+    const int lane = threadIdx.x & 31, block_warps = blockDim.x >> 5;
+    const int64_t warp = (int64_t)blockIdx.x * block_warps + (threadIdx.x >> 5);
+    const int64_t warps = (int64_t)gridDim.x * block_warps;
+    constexpr int kSegment = 32 * kGatherPieces;
+    const int64_t pieces = C::pieces(hidden), segments = (pieces + kSegment - 1) / kSegment;
+    const void *x_end = x + (tokens - 1) * ld_x + hidden;
     for (int64_t u = warp; u < tokens * segments; u += warps) {
-        const int64_t t = u / segments, c0 = (u - t * segments) * kSegment + lane * P::N;
-        P v[kGatherPieces];
+        const int64_t t = u / segments, i0 = (u - t * segments) * kSegment + lane;
+        const T *row = x + t * ld_x;
+        typename C::Raw raw[kGatherPieces];
+        if constexpr (kWide) {
 #pragma unroll
-        for (int i = 0; i < kGatherPieces; i++)
-            if (c0 + i * 32 * P::N < hidden) v[i].load(x + t * ld_x + c0 + i * 32 * P::N);
+            for (int i = 0; i < kGatherPieces; i++)
+                if (i0 + 32 * i < pieces) C::fetch(raw[i], row, C::column(row, i0 + 32 * i), x, x_end);
+        }
         for (int j = 0; j < top_k; j++) {
             const int p = slot_place(inverse, t * top_k + j, slots);
             if (p < 0) continue;
-            T *row = out + p * ld_out + c0;
+            T *dst = out + p * ld_out;
+            if constexpr (!kWide) {  // every place has its own alignment; after the first from L1
 #pragma unroll
-            for (int i = 0; i < kGatherPieces; i++)
-                if (c0 + i * 32 * P::N < hidden) v[i].store(row + i * 32 * P::N);
+                for (int i = 0; i < kGatherPieces; i++) {
+                    const int64_t c = C::column(dst, i0 + 32 * i);
+                    if (i0 + 32 * i < pieces && C::inside(c, hidden)) C::fetch(raw[i], row, c, x, x_end);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kGatherPieces; i++) {
+                const int64_t c = C::column(dst, i0 + 32 * i);
+                if (i0 + 32 * i >= pieces || !C::inside(c, hidden)) continue;
+                P v;
+                C::take(v, raw[i], row, c, hidden, x, x_end);
+                C::store(v, dst, c, hidden);
+            }
         }
     }
     const int64_t kept = kept_places(offsets, n_experts, slots);
     P z;
     z.zero();
     for (int64_t u = warp; u < (slots - kept) * segments; u += warps) {
-        const int64_t r = u / segments, c0 = (u - r * segments) * kSegment + lane * P::N;
-        T *row = out + (kept + r) * ld_out + c0;
+        const int64_t r = u / segments, i0 = (u - r * segments) * kSegment + lane;
+        T *dst = out + (kept + r) * ld_out;
 #pragma unroll
-        for (int i = 0; i < kGatherPieces; i++)
-            if (c0 + i * 32 * P::N < hidden) z.store(row + i * 32 * P::N);
+        for (int i = 0; i < kGatherPieces; i++) {
+            const int64_t c = C::column(dst, i0 + 32 * i);
+            if (i0 + 32 * i < pieces && C::inside(c, hidden)) C::store(z, dst, c, hidden);
+        }
     }
 }
 
 // ---------------------------------------------------------------- combine
 // out[t] = sum over j of w[t, j] * y[inverse[t, j]] in binary32, j ascending, dropped
 // slots left out (their weights too), one rounding to T. Without weights it is the plain
-// sum, which is the gather's gradient.
-constexpr int kCombinePieces = 2;
+// sum, which is the gather's gradient. A warp takes a segment of one token's row. Its lanes
+// fetch the token's places and weights together, one each, and the rows of kCombineRows
+// kept slots are loaded before any is added, so that enough loads are in flight.
+template <bool kWide>
+constexpr int kCombinePieces = kWide ? 2 : 1;  // a piece put together holds twice the registers
+constexpr int kCombineRows = 4;
 
 template <class T, bool kWide, bool kWeights>
 __global__ void __launch_bounds__(kThreads)
@@ -299,7 +384,8 @@ combine_kernel(const T *__restrict__ y, int64_t ld_y, const float *__restrict__ 
                const int32_t *__restrict__ inverse, int64_t tokens, int top_k, int64_t hidden, T *__restrict__ out,
                int64_t ld_out)
 {
-    using P = Piece<T, kWide>;
+    using P = Piece<T>;
+    using C = Cut<T, kWide>;
     pdl_begin();
     const int64_t slots = tokens * top_k;
     dbg_begin();
@@ -308,39 +394,68 @@ combine_kernel(const T *__restrict__ y, int64_t ld_y, const float *__restrict__ 
     dbg_allow(inverse, 4 * slots, false);
     dbg_allow_2d(out, tokens, hidden * sizeof(T), ld_out * sizeof(T), true);
     dbg_ready();
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    constexpr int kSegment = 32 * P::N * kCombinePieces;
-    const int64_t segments = (hidden + kSegment - 1) / kSegment;
+    const int lane = threadIdx.x & 31, block_warps = blockDim.x >> 5;
+    const int64_t warp = (int64_t)blockIdx.x * block_warps + (threadIdx.x >> 5);
+    const int64_t warps = (int64_t)gridDim.x * block_warps;
+    constexpr int kPieces = kCombinePieces<kWide>, kSegment = 32 * kPieces;
+    const int64_t pieces = C::pieces(hidden), segments = (pieces + kSegment - 1) / kSegment;
+    const void *y_end = y + (slots - 1) * ld_y + hidden;
     for (int64_t u = warp; u < tokens * segments; u += warps) {
-        const int64_t t = u / segments, c0 = (u - t * segments) * kSegment + lane * P::N;
-        float acc[kCombinePieces][P::N] = {};
-#pragma unroll 4
-        for (int j = 0; j < top_k; j++) {
-            const int p = slot_place(inverse, t * top_k + j, slots);
-            if (p < 0) continue;
-            const float w = kWeights && dbg_ok(weights + t * top_k + j, 4, false) ? __ldg(weights + t * top_k + j) : 1.0f;
-            const T *row = y + p * ld_y + c0;
+        const int64_t t = u / segments, i0 = (u - t * segments) * kSegment + lane;
+        T *dst = out + t * ld_out;
+        int64_t c[kPieces];
+        bool in[kPieces];
 #pragma unroll
-            for (int i = 0; i < kCombinePieces; i++) {
-                if (c0 + i * 32 * P::N < hidden) {
-                    P v;
-                    v.load(row + i * 32 * P::N);
+        for (int k = 0; k < kPieces; k++) {
+            c[k] = C::column(dst, i0 + 32 * k);
+            in[k] = i0 + 32 * k < pieces && C::inside(c[k], hidden);
+        }
+        float acc[kPieces][P::N] = {};
+        for (int j0 = 0; j0 < top_k; j0 += 32) {
+            const int64_t slot = t * top_k + j0 + lane;
+            const int place = j0 + lane < top_k ? slot_place(inverse, slot, slots) : -1;
+            float weight = 1.0f;
+            if (kWeights && place >= 0 && dbg_ok(weights + slot, 4, false)) weight = __ldg(weights + slot);
+            unsigned rest = __ballot_sync(kFull, place >= 0);
+            while (rest != 0) {
+                typename C::Raw raw[kCombineRows][kPieces];
+                const T *rows[kCombineRows];
+                float w[kCombineRows];
+                bool has[kCombineRows];
 #pragma unroll
-                    for (int n = 0; n < P::N; n++)
-                        acc[i][n] = kWeights ? __fmaf_rn(w, v.at(n), acc[i][n]) : __fadd_rn(acc[i][n], v.at(n));
+                for (int i = 0; i < kCombineRows; i++) {
+                    has[i] = rest != 0;
+                    const int j = has[i] ? __ffs(rest) - 1 : 0;
+                    rest &= rest - 1;  // 0 stays 0
+                    w[i] = __shfl_sync(kFull, weight, j);
+                    rows[i] = y + __shfl_sync(kFull, place, j) * ld_y;
+#pragma unroll
+                    for (int k = 0; k < kPieces; k++)
+                        if (has[i] && in[k]) C::fetch(raw[i][k], rows[i], c[k], y, y_end);
+                }
+#pragma unroll
+                for (int i = 0; i < kCombineRows; i++) {
+                    if (!has[i]) break;
+#pragma unroll
+                    for (int k = 0; k < kPieces; k++) {
+                        if (!in[k]) continue;
+                        P v;
+                        C::take(v, raw[i][k], rows[i], c[k], hidden, y, y_end);
+#pragma unroll
+                        for (int n = 0; n < P::N; n++)
+                            acc[k][n] = kWeights ? __fmaf_rn(w[i], v.at(n), acc[k][n]) : __fadd_rn(acc[k][n], v.at(n));
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < kCombinePieces; i++) {
-            if (c0 + i * 32 * P::N < hidden) {
-                P v;
+        for (int k = 0; k < kPieces; k++) {
+            if (!in[k]) continue;
+            P v;
+            v.zero();
 #pragma unroll
-                for (int n = 0; n < P::N; n++) v.set(n, acc[i][n]);
-                v.store(out + t * ld_out + c0 + i * 32 * P::N);
-            }
+            for (int n = 0; n < P::N; n++) v.set(n, acc[k][n]);
+            C::store(v, dst, c[k], hidden);
         }
     }
 }
@@ -360,7 +475,8 @@ combine_grad_kernel(const T *__restrict__ dout, int64_t ld_dout, const T *__rest
                     const int32_t *__restrict__ offsets, int n_experts, int64_t tokens, int top_k, int64_t hidden,
                     T *__restrict__ dy, int64_t ld_dy, float *__restrict__ dweights)
 {
-    using P = Piece<T, kWide>;
+    using P = Piece<T>;
+    using C = Cut<T, kWide>;
     __shared__ float partial[kGradMaxThreads / 32][kGradSlots];
     pdl_begin();
     const int64_t slots = tokens * top_k;
@@ -375,7 +491,8 @@ combine_grad_kernel(const T *__restrict__ dout, int64_t ld_dout, const T *__rest
     dbg_ready();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int groups = (top_k + kGradSlots - 1) / kGradSlots;
-    const int64_t step = (int64_t)blockDim.x * P::N;
+    const int64_t pieces = C::pieces(hidden);
+    const void *d_end = dout + (tokens - 1) * ld_dout + hidden, *y_end = y + (slots - 1) * ld_y + hidden;
     for (int64_t u = blockIdx.x; u < tokens * groups; u += gridDim.x) {
         const int64_t t = u / groups;
         const int j0 = static_cast<int>(u - t * groups) * kGradSlots;
@@ -387,22 +504,34 @@ combine_grad_kernel(const T *__restrict__ dout, int64_t ld_dout, const T *__rest
             place[s] = j0 + s < top_k ? slot_place(inverse, slot, slots) : -1;
             w[s] = place[s] >= 0 && dbg_ok(weights + slot, 4, false) ? __ldg(weights + slot) : 0.0f;
         }
-        for (int64_t c = threadIdx.x * P::N; c < hidden; c += step) {
-            P d, v[kGradSlots];
-            d.load(dout + t * ld_dout + c);
-#pragma unroll
-            for (int s = 0; s < kGradSlots; s++)
-                if (place[s] >= 0) v[s].load(y + place[s] * ld_y + c);
+        const T *d_row = dout + t * ld_dout;
+        for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) {
+            typename C::Raw d_raw[kWide ? 1 : kGradSlots], y_raw[kGradSlots];
+            if constexpr (kWide) C::fetch(d_raw[0], d_row, C::column(d_row, i), dout, d_end);
 #pragma unroll
             for (int s = 0; s < kGradSlots; s++) {
-                if (place[s] < 0) continue;
-                P g;
+                const int64_t c = place[s] >= 0 ? C::column(dy + place[s] * ld_dy, i) : hidden;
+                if (!C::inside(c, hidden)) continue;
+                if constexpr (!kWide) C::fetch(d_raw[s], d_row, c, dout, d_end);
+                C::fetch(y_raw[s], y + place[s] * ld_y, c, y, y_end);
+            }
+#pragma unroll
+            for (int s = 0; s < kGradSlots; s++) {
+                T *dst = dy + place[s] * ld_dy;
+                const int64_t c = place[s] >= 0 ? C::column(dst, i) : hidden;
+                if (!C::inside(c, hidden)) continue;
+                P d, v, g;
+                C::take(d, d_raw[kWide ? 0 : s], d_row, c, hidden, dout, d_end);
+                C::take(v, y_raw[s], y + place[s] * ld_y, c, hidden, y, y_end);
+                C::keep(d, c, hidden);
+                C::keep(v, c, hidden);
+                g.zero();
 #pragma unroll
                 for (int n = 0; n < P::N; n++) {
-                    dot[s] = __fmaf_rn(d.at(n), v[s].at(n), dot[s]);
+                    dot[s] = __fmaf_rn(d.at(n), v.at(n), dot[s]);
                     g.set(n, __fmul_rn(w[s], d.at(n)));
                 }
-                g.store(dy + place[s] * ld_dy + c);
+                C::store(g, dst, c, hidden);
             }
         }
 #pragma unroll
@@ -424,22 +553,35 @@ combine_grad_kernel(const T *__restrict__ dout, int64_t ld_dout, const T *__rest
     P z;
     z.zero();
     for (int64_t p = kept + blockIdx.x; p < slots; p += gridDim.x)
-        for (int64_t c = threadIdx.x * P::N; c < hidden; c += step) z.store(dy + p * ld_dy + c);
+        for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) {
+            T *dst = dy + p * ld_dy;
+            const int64_t c = C::column(dst, i);
+            if (C::inside(c, hidden)) C::store(z, dst, c, hidden);
+        }
 }
 
-// Warps that the grid of a row kernel needs, for grid_for.
-int64_t row_units(int64_t rows, int64_t hidden, int per_segment) { return rows * ((hidden + per_segment - 1) / per_segment); }
+// Launches a kernel of warp units. Few units go out in small CTAs, so that they spread over
+// all SMs: 16 tokens' combine of 7168 columns in 28 CTAs of 8 warps took 5.0 us.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_units(void (*kernel)(KArgs...), int64_t units, cudaStream_t st, Args... args)
+{
+    int sms = 1, grid = 0;
+    if (cudaError_t e = sm_count(&sms)) return e;
+    const int64_t per_sm = (units + sms - 1) / sms;
+    const int block = per_sm >= 8 ? 256 : per_sm >= 4 ? 128 : per_sm >= 2 ? 64 : 32;
+    if (cudaError_t e = grid_for((const void *)kernel, units, &grid, 0, block)) return e;
+    return launch_kernel_block(kernel, grid, block, 0, st, args...);
+}
+
+int64_t row_units(int64_t rows, int64_t pieces, int per_segment) { return rows * ((pieces + per_segment - 1) / per_segment); }
 
 template <class T, bool kWide>
 cudaError_t launch_gather_t(const RowArgs &a, const void *x, int64_t ld_x, const int32_t *offsets, int n_experts,
                             void *out, int64_t ld_out, cudaStream_t st)
 {
-    auto kernel = gather_kernel<T, kWide>;
-    int grid = 0;
-    const int64_t units = row_units(a.tokens * a.top_k, a.hidden, 32 * Piece<T, kWide>::N * kGatherPieces);
-    if (cudaError_t e = grid_for((const void *)kernel, units, &grid)) return e;
-    return launch_kernel(kernel, grid, st, static_cast<const T *>(x), a.tokens, a.hidden, ld_x, a.inverse, a.top_k,
-                         offsets, n_experts, static_cast<T *>(out), ld_out);
+    const int64_t units = row_units(a.tokens, Cut<T, kWide>::pieces(a.hidden), 32 * kGatherPieces);
+    return launch_units(gather_kernel<T, kWide>, units, st, static_cast<const T *>(x), a.tokens, a.hidden, ld_x,
+                        a.inverse, a.top_k, offsets, n_experts, static_cast<T *>(out), ld_out);
 }
 
 template <class T, bool kWide>
@@ -447,11 +589,9 @@ cudaError_t launch_combine_t(const RowArgs &a, const void *y, int64_t ld_y, cons
                              int64_t ld_out, cudaStream_t st)
 {
     auto kernel = weights ? combine_kernel<T, kWide, true> : combine_kernel<T, kWide, false>;
-    int grid = 0;
-    const int64_t units = row_units(a.tokens, a.hidden, 32 * Piece<T, kWide>::N * kCombinePieces);
-    if (cudaError_t e = grid_for((const void *)kernel, units, &grid)) return e;
-    return launch_kernel(kernel, grid, st, static_cast<const T *>(y), ld_y, weights, a.inverse, a.tokens, a.top_k,
-                         a.hidden, static_cast<T *>(out), ld_out);
+    const int64_t units = row_units(a.tokens, Cut<T, kWide>::pieces(a.hidden), 32 * kCombinePieces<kWide>);
+    return launch_units(kernel, units, st, static_cast<const T *>(y), ld_y, weights, a.inverse, a.tokens, a.top_k,
+                        a.hidden, static_cast<T *>(out), ld_out);
 }
 
 template <class T, bool kWide>
@@ -460,7 +600,7 @@ cudaError_t launch_combine_grad_t(const RowArgs &a, const void *dout, int64_t ld
                                   float *dweights, cudaStream_t st)
 {
     auto kernel = combine_grad_kernel<T, kWide>;
-    const int64_t pieces = (a.hidden + Piece<T, kWide>::N - 1) / Piece<T, kWide>::N;
+    const int64_t pieces = Cut<T, kWide>::pieces(a.hidden);
     const int64_t want = (pieces + 31) / 32 * 32;  // without columns one warp writes the zeros of dw
     const int block = static_cast<int>(want < 32 ? 32 : want < kGradMaxThreads ? want : kGradMaxThreads);
     const int64_t units = a.tokens * ((a.top_k + kGradSlots - 1) / kGradSlots);

@@ -150,13 +150,6 @@ __device__ __forceinline__ uint32_t code_row(uint32_t at, int i)
     return (kRowTiles == 1 ? at ^ (64 * (i & 1)) : at) + 512 * i;
 }
 
-// 16 bytes that other warps will read too: through L1.
-__device__ __forceinline__ uint4 ld_keep_v4(const void *p)
-{
-    if (!dbg_ok(p, 16, false)) return make_uint4(0, 0, 0, 0);
-    return __ldg(static_cast<const uint4 *>(p));
-}
-
 // ---------------------------------------------------------------- scales
 // A row's kCount scales of one step, copied as the 4-byte words that hold them: 16-bit
 // scales of rows with odd strides may start in the upper half of their first word.

@@ -39,13 +39,20 @@ def empty_plan(tokens: int, top_k: int, n_experts: int, device="cuda") -> Plan:
     return Plan(ints(n_experts + 1), ints(tokens * top_k), ints(tokens, top_k), ints(SORT_PARTS, n_experts))
 
 
-def _here(call: str, **tensors) -> None:
-    """Every tensor lives on the current CUDA device, where the library launches."""
+def _here(call: str, names: str, *tensors) -> int:
+    """The current CUDA device, where the library launches: every tensor must live there."""
     cur = torch.cuda.current_device()
-    for name, t in tensors.items():
+    for i, t in enumerate(tensors):
         if t is not None and t.get_device() != cur:
             where = t.device if t.is_cuda else "the CPU"
-            raise ValueError(f"{call}: {name} is on {where}, but the current CUDA device is cuda:{cur}")
+            raise ValueError(f"{call}: {names.split()[i]} is on {where}, but the current CUDA device is cuda:{cur}")
+    return cur
+
+
+def _on(stream, device: int) -> int:
+    """The stream's handle; without one, the current stream's, which a decode step's many short
+    calls read directly: a torch.cuda.Stream object would cost a third of such a call."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _flat(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
@@ -83,7 +90,7 @@ def sort(ids: torch.Tensor, n_experts: int, offsets: torch.Tensor, order: torch.
         raise ValueError("sort: ids must be [tokens, top_k]")
     tokens, top_k = ids.shape
     wide = ids.dtype == torch.int64
-    _here("sort", ids=ids, offsets=offsets, order=order, inverse=inverse, workspace=workspace)
+    dev = _here("sort", "ids offsets order inverse workspace", ids, offsets, order, inverse, workspace)
     if (offsets.numel(), order.numel()) != (n_experts + 1, tokens * top_k) or inverse.shape != ids.shape:
         raise ValueError("sort: offsets must have n_experts + 1, order and inverse tokens * top_k values")
     if workspace.numel() < SORT_PARTS * n_experts:
@@ -91,7 +98,7 @@ def sort(ids: torch.Tensor, n_experts: int, offsets: torch.Tensor, order: torch.
     check("bq_expert_sort", load().bq_expert_sort(
         _flat(ids, torch.int64 if wide else torch.int32, "ids"), wide, tokens, top_k, n_experts,
         _flat(offsets, torch.int32, "offsets"), _flat(order, torch.int32, "order"),
-        _flat(inverse, torch.int32, "inverse"), _flat(workspace, torch.int32, "workspace"), _stream(stream)))
+        _flat(inverse, torch.int32, "inverse"), _flat(workspace, torch.int32, "workspace"), _on(stream, dev)))
 
 
 def _plan_shape(inverse: torch.Tensor, call: str):
@@ -103,21 +110,21 @@ def _plan_shape(inverse: torch.Tensor, call: str):
 def gather(x: torch.Tensor, inverse: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """Token rows x [tokens, hidden] -> out [tokens * top_k, hidden] by place, zeros past the
     kept places (bq_expert_gather)."""
-    _here("gather", x=x, inverse=inverse, offsets=offsets, out=out)
+    dev = _here("gather", "x inverse offsets out", x, inverse, offsets, out)
     tokens, top_k = _plan_shape(inverse, "gather")
     kind, hidden = _row_type(x, "x"), x.shape[-1]
     xp, ld_x = _rows(x, tokens, hidden, x.dtype, "x")
     op, ld_out = _rows(out, tokens * top_k, hidden, x.dtype, "out")
     check("bq_expert_gather", load().bq_expert_gather(
         xp, kind, tokens, hidden, ld_x, _flat(inverse, torch.int32, "inverse"), top_k,
-        _flat(offsets, torch.int32, "offsets"), offsets.numel() - 1, op, ld_out, _stream(stream)))
+        _flat(offsets, torch.int32, "offsets"), offsets.numel() - 1, op, ld_out, _on(stream, dev)))
 
 
 def combine(y: torch.Tensor, weights: Optional[torch.Tensor], inverse: torch.Tensor, out: torch.Tensor,
             stream=None) -> None:
     """Expert rows y [tokens * top_k, hidden] -> out [tokens, hidden], row t the sum over j of
     weights[t, j] (float32; None: 1) times t's j-th expert row (bq_expert_combine)."""
-    _here("combine", y=y, weights=weights, inverse=inverse, out=out)
+    dev = _here("combine", "y weights inverse out", y, weights, inverse, out)
     tokens, top_k = _plan_shape(inverse, "combine")
     kind, hidden = _row_type(y, "y"), y.shape[-1]
     yp, ld_y = _rows(y, tokens * top_k, hidden, y.dtype, "y")
@@ -126,7 +133,7 @@ def combine(y: torch.Tensor, weights: Optional[torch.Tensor], inverse: torch.Ten
         raise ValueError("combine: weights must be [tokens, top_k]")
     check("bq_expert_combine", load().bq_expert_combine(
         yp, kind, ld_y, _flat(weights, torch.float32, "weights") if weights is not None else None,
-        _flat(inverse, torch.int32, "inverse"), tokens, top_k, hidden, op, ld_out, _stream(stream)))
+        _flat(inverse, torch.int32, "inverse"), tokens, top_k, hidden, op, ld_out, _on(stream, dev)))
 
 
 def gather_grad(dout: torch.Tensor, inverse: torch.Tensor, dx: torch.Tensor, stream=None) -> None:
@@ -138,8 +145,8 @@ def combine_grad(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor, inv
                  offsets: torch.Tensor, dy: torch.Tensor, dweights: torch.Tensor, stream=None) -> None:
     """The gradients of ``combine``, in one pass: dy [tokens * top_k, hidden] by place (zeros
     past the kept places) and dweights [tokens, top_k] (bq_expert_combine_grad)."""
-    _here("combine_grad", dout=dout, y=y, weights=weights, inverse=inverse, offsets=offsets, dy=dy,
-          dweights=dweights)
+    dev = _here("combine_grad", "dout y weights inverse offsets dy dweights", dout, y, weights, inverse, offsets, dy,
+                dweights)
     tokens, top_k = _plan_shape(inverse, "combine_grad")
     kind, hidden = _row_type(dout, "dout"), dout.shape[-1]
     dp, ld_d = _rows(dout, tokens, hidden, dout.dtype, "dout")
@@ -150,4 +157,4 @@ def combine_grad(dout: torch.Tensor, y: torch.Tensor, weights: torch.Tensor, inv
     check("bq_expert_combine_grad", load().bq_expert_combine_grad(
         dp, kind, ld_d, yp, ld_y, _flat(weights, torch.float32, "weights"), _flat(inverse, torch.int32, "inverse"),
         _flat(offsets, torch.int32, "offsets"), offsets.numel() - 1, tokens, top_k, hidden, gp, ld_g,
-        _flat(dweights, torch.float32, "dweights"), _stream(stream)))
+        _flat(dweights, torch.float32, "dweights"), _on(stream, dev)))

@@ -12,8 +12,7 @@ from typing import Optional
 import torch
 
 from ._lib import check, load
-from .codec import _stream
-from .experts import _flat, _here, _row_type, _rows
+from .experts import _flat, _here, _on, _row_type, _rows
 
 
 def _weights(call: str, q: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, dims: int):
@@ -41,7 +40,7 @@ def _weights(call: str, q: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, 
 def matvec_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """x [rows, k] times the weights [n, k] transposed -> out [rows, n] of x's type
     (bq_matvec_w4). Any number of rows; made for up to 32."""
-    _here("matvec_w4", x=x, q=q, scales=scales, out=out)
+    dev = _here("matvec_w4", "x q scales out", x, q, scales, out)
     n, k, group, s_kind = _weights("matvec_w4", q, scales, x, 2)
     rows = x.shape[0]
     xp, ld_x = _rows(x, rows, k, x.dtype, "x")
@@ -49,7 +48,7 @@ def matvec_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, out: torch
     one = n <= 1
     check("bq_matvec_w4", load().bq_matvec_w4(
         xp, _row_type(x, "x"), rows, k, ld_x, q.data_ptr(), n, k // 2 if one else q.stride(0), scales.data_ptr(),
-        s_kind, group, k // group if one else scales.stride(0), op, ld_out, _stream(stream)))
+        s_kind, group, k // group if one else scales.stride(0), op, ld_out, _on(stream, dev)))
 
 
 def matvec_w4_experts(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
@@ -58,7 +57,7 @@ def matvec_w4_experts(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, of
     [slots, n], zeros past the kept places (bq_matvec_w4_experts). With ``order`` (of
     ``experts.sort``) place p takes row order[p] // top_k of x, the tokens' rows; without it
     x [slots, k] is already by place."""
-    _here("matvec_w4_experts", x=x, q=q, scales=scales, offsets=offsets, out=out, order=order)
+    dev = _here("matvec_w4_experts", "x q scales offsets out order", x, q, scales, offsets, out, order)
     n, k, group, s_kind = _weights("matvec_w4_experts", q, scales, x, 3)
     n_experts = q.shape[0]
     slots, x_rows = out.shape[0], x.shape[0]
@@ -73,4 +72,4 @@ def matvec_w4_experts(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, of
         xp, _row_type(x, "x"), x_rows, k, ld_x, q.data_ptr(), n, k // 2 if one else q.stride(1), q.stride(0),
         scales.data_ptr(), s_kind, group, k // group if one else scales.stride(1), scales.stride(0),
         _flat(offsets, torch.int32, "offsets"), n_experts, _flat(order, torch.int32, "order") if order is not None
-        else None, top_k, slots, op, ld_out, _stream(stream)))
+        else None, top_k, slots, op, ld_out, _on(stream, dev)))
