@@ -49,6 +49,7 @@ _PROTOS = {
     "bq_expert_combine": ([_P, _INT, _I64, _P, _P, _I64, _INT, _I64, _P, _I64, _P], _INT),
     "bq_expert_combine_grad": ([_P, _INT, _I64, _P, _I64, _P, _P, _P, _INT, _I64, _INT, _I64, _P, _I64, _P, _P],
                                _INT),
+    "bq_quant_w4": ([_P, _INT, _I64, _I64, _I64, _INT, _P, _I64, _P, _INT, _I64, _P], _INT),
     "bq_matvec_w4": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _P, _INT, _INT, _I64, _P, _I64, _P], _INT),
     "bq_matvec_w4_experts": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _INT, _INT, _I64, _I64, _P, _INT,
                               _P, _INT, _I64, _P, _I64, _P], _INT),

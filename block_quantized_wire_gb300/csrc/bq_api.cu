@@ -592,6 +592,22 @@ bq_status matvec_w4(int type, int scale_type, int group, bqk::W4Args &a, cudaStr
 
 extern "C" {
 
+bq_status bq_quant_w4(const void *x, int type, int64_t n, int64_t k, int64_t ld_x, int group, uint8_t *q, int64_t ld_q,
+                      void *scales, int scale_type, int64_t ld_s, cudaStream_t stream)
+{
+    if (!row_type(type) || !row_type(scale_type) || (group != 32 && group != 64 && group != 128)) return BQ_ERR_SHAPE;
+    if (n < 0 || n > BQ_MAX_W4_DIM || k < 0 || k > BQ_MAX_W4_DIM || k % group) return BQ_ERR_SHAPE;
+    if (n == 0 || k == 0) return BQ_OK;
+    if (ld_x < k || ld_q < k / 2 || ld_s < k / group) return BQ_ERR_SHAPE;
+    if (!x || !q || !scales) return BQ_ERR_NULL;
+    const int size = bqk::row_type_bytes(type), s_size = bqk::row_type_bytes(scale_type);
+    if (!aligned(x, 16) || ld_x * size % 16 || !aligned(q, 16) || ld_q % 16 || !aligned(scales, 4)) return BQ_ERR_ALIGN;
+    const Range ins[] = {rows_span(x, type, n, k, ld_x)};
+    const Range outs[] = {span2d(q, n, k / 2, ld_q), span2d(scales, n, s_size * (k / group), s_size * ld_s)};
+    if (any_alias(outs, 2, ins, 1)) return BQ_ERR_ALIAS;
+    return from_cuda(bqk::launch_quant_w4(type, scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, stream));
+}
+
 bq_status bq_matvec_w4(const void *x, int type, int64_t rows, int64_t k, int64_t ld_x, const uint8_t *q, int64_t n,
                        int64_t ld_q, const void *scales, int scale_type, int group, int64_t ld_s, void *out,
                        int64_t ld_out, cudaStream_t stream)

@@ -109,6 +109,8 @@ struct W4Args {
     int n_experts, top_k;
     int staged_rows, ctas_per_sm;  // filled by the launcher
 };
+cudaError_t launch_quant_w4(int type, int scale_type, int group, const void *x, int64_t n, int64_t k, int64_t ld_x,
+                            uint8_t *q, int64_t ld_q, void *scales, int64_t ld_s, cudaStream_t st);
 cudaError_t launch_matvec_w4(int x_type, int scale_type, int group, const W4Args &a, cudaStream_t st);
 
 // Programmatic dependent launch: every codec kernel is launched with programmatic

@@ -764,7 +764,97 @@ cudaError_t launch_w4_kind(int group, const W4Args &a, cudaStream_t st)
     return a.offsets ? launch_w4_group<T, S, true>(group, a, st) : launch_w4_group<T, S, false>(group, a, st);
 }
 
+// ---------------------------------------------------------------- quantize
+// Per group: s = amax / 7 in binary32, rounded to the scale's type; code = the integer
+// nearest to x / s (ties to even), within [-7, 7]; a group whose scale is 0 has codes 0.
+// Weights are quantized once when a model is loaded: a lane takes eight columns, a group's
+// lanes find its amax by shuffles.
+template <class T, class S, int kGroup>
+__global__ void __launch_bounds__(kThreads)
+quant_w4_kernel(const T *__restrict__ x, int64_t n, int64_t k, int64_t ld_x, uint8_t *__restrict__ q, int64_t ld_q,
+                S *__restrict__ scales, int64_t ld_s)
+{
+    pdl_begin();
+    dbg_begin();
+    dbg_allow_2d(x, n, k * sizeof(T), ld_x * sizeof(T), false);
+    dbg_allow_2d(q, n, k / 2, ld_q, true);
+    dbg_allow_2d(scales, n, k / kGroup * sizeof(S), ld_s * sizeof(S), true);
+    dbg_ready();
+    using P = Piece<T>;
+    const int64_t per_row = k / 8, units = n * per_row;
+    const int64_t first = (int64_t)blockIdx.x * kThreads + (threadIdx.x & ~31u);
+    for (int64_t w0 = first; w0 < units; w0 += (int64_t)gridDim.x * kThreads) {
+        const int64_t u = w0 + (threadIdx.x & 31);
+        const bool in = u < units;
+        const int64_t row = in ? u / per_row : 0, c = in ? (u - row * per_row) * 8 : 0;
+        float v[8] = {};
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < 8; i += P::N) {
+                P piece;
+                piece.put(ld_stream_v4(x + row * ld_x + c + i));
+#pragma unroll
+                for (int j = 0; j < P::N; j++) v[i + j] = piece.at(j);
+            }
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+        for (int d = 1; d < kGroup / 8; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, d));
+        const auto bits = Value<S>::round(__fdiv_rn(amax, 7.0f));
+        const float s = Value<S>::widen(bits);
+        uint32_t word = 0;
+        if (s > 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float code = fminf(fmaxf(rintf(__fdiv_rn(v[i], s)), -7.0f), 7.0f);
+                word |= ((uint32_t)(int)code & 15u) << (4 * i);
+            }
+        }
+        if (in) {
+            st_u32(q + row * ld_q + c / 2, word);
+            S *dst = scales + row * ld_s + c / kGroup;
+            if (c % kGroup == 0 && dbg_ok(dst, sizeof(S), true))
+                *reinterpret_cast<typename Value<S>::Bits *>(dst) = bits;
+        }
+    }
+}
+
+template <class T, class S, int kGroup>
+cudaError_t launch_quant(const void *x, int64_t n, int64_t k, int64_t ld_x, uint8_t *q, int64_t ld_q, void *scales,
+                         int64_t ld_s, cudaStream_t st)
+{
+    auto kernel = quant_w4_kernel<T, S, kGroup>;
+    int grid = 0;
+    if (cudaError_t e = grid_for((const void *)kernel, (n * (k / 8) + 31) / 32, &grid)) return e;
+    return launch_kernel(kernel, grid, st, static_cast<const T *>(x), n, k, ld_x, q, ld_q, static_cast<S *>(scales), ld_s);
+}
+
+template <class T, class S, typename... Args>
+cudaError_t launch_quant_group(int group, Args... args)
+{
+    return group == 32 ? launch_quant<T, S, 32>(args...) : group == 64 ? launch_quant<T, S, 64>(args...)
+                                                                       : launch_quant<T, S, 128>(args...);
+}
+
+template <class T, typename... Args>
+cudaError_t launch_quant_scale(int scale_type, Args... args)
+{
+    return scale_type == kBf16  ? launch_quant_group<T, __nv_bfloat16>(args...)
+           : scale_type == kF16 ? launch_quant_group<T, __half>(args...)
+                                : launch_quant_group<T, float>(args...);
+}
+
 }  // namespace
+
+cudaError_t launch_quant_w4(int type, int scale_type, int group, const void *x, int64_t n, int64_t k, int64_t ld_x,
+                            uint8_t *q, int64_t ld_q, void *scales, int64_t ld_s, cudaStream_t st)
+{
+    return type == kBf16  ? launch_quant_scale<__nv_bfloat16>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st)
+           : type == kF16 ? launch_quant_scale<__half>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st)
+                          : launch_quant_scale<float>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st);
+}
 
 cudaError_t launch_matvec_w4(int x_type, int scale_type, int group, const W4Args &a, cudaStream_t st)
 {

@@ -37,6 +37,34 @@ def _weights(call: str, q: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, 
     return n, k, group, _row_type(scales, "scales")
 
 
+def empty_w4(n: int, k: int, group: int, scale_dtype=torch.bfloat16, device="cuda", lead=()):
+    """(q, scales) of a weight matrix [n, k], or of several with the leading dimensions `lead`."""
+    return (torch.empty((*lead, n, k // 2), dtype=torch.uint8, device=device),
+            torch.empty((*lead, n, k // group), dtype=scale_dtype, device=device))
+
+
+def quant_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """Weights x [n, k] or [n_experts, n, k] (bfloat16, float16 or float32) -> codes q and group
+    scales: amax / 7 per group, the nearest code (bq_quant_w4). Leading dimensions must be
+    contiguous with the rows."""
+    dev = _here("quant_w4", "x q scales", x, q, scales)
+    if q.dtype != torch.uint8:
+        raise TypeError(f"quant_w4: q must be uint8, got {q.dtype}")
+    if x.dim() < 2 or q.shape != (*x.shape[:-1], x.shape[-1] // 2) or scales.shape[:-1] != x.shape[:-1]:
+        raise ValueError("quant_w4: q must be [..., n, k / 2] and scales [..., n, k / group]")
+    k, groups = x.shape[-1], scales.shape[-1]
+    group = k // groups if groups else 32
+    if group not in (32, 64, 128) or groups * group != k:
+        raise ValueError(f"quant_w4: {k} columns with {groups} scales a row: a scale covers 32, 64 or 128 columns")
+    n = x.numel() // k if k else 0
+    flat = [t.view(n, t.shape[-1]) if n else t for t in (x, q, scales)]
+    xp, ld_x = _rows(flat[0], n, k, x.dtype, "x") if n else (None, k)
+    qp, ld_q = _rows(flat[1], n, k // 2, torch.uint8, "q") if n else (None, k)
+    sp, ld_s = _rows(flat[2], n, groups, scales.dtype, "scales") if n else (None, k)
+    check("bq_quant_w4", load().bq_quant_w4(xp, _row_type(x, "x"), n, k, ld_x, group, qp, ld_q, sp,
+                                            _row_type(scales, "scales"), ld_s, _on(stream, dev)))
+
+
 def matvec_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """x [rows, k] times the weights [n, k] transposed -> out [rows, n] of x's type
     (bq_matvec_w4). Any number of rows; made for up to 32."""

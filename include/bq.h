@@ -356,6 +356,17 @@ BQ_API bq_status bq_expert_combine_grad(const void *dout, int type, int64_t ld_d
                                         int n_experts, int64_t tokens, int top_k, int64_t hidden, void *dy,
                                         int64_t ld_dy, float *dweights, cudaStream_t stream);
 
+/* Weights -> 4-bit codes with group scales, as the products below read them: per group of
+ * `group` (32, 64 or 128) columns s = scale_type_rne(fl(amax / 7)), code = the integer
+ * nearest to fl(x / s), ties to even, within [-7, 7]; a group with s == 0 has codes 0.
+ * Bit-exact; non-finite weights are not specified.
+ *   x [n][ld_x] of type (read); q [n][ld_q] bytes, scales [n][ld_s] of scale_type (written)
+ *   16-byte aligned x and q with rows a multiple of 16 bytes apart, scales 4-byte aligned;
+ *   k % group == 0. Several experts' matrices of equal n are one matrix of n_experts * n
+ *   rows. */
+BQ_API bq_status bq_quant_w4(const void *x, int type, int64_t n, int64_t k, int64_t ld_x, int group, uint8_t *q,
+                             int64_t ld_q, void *scales, int scale_type, int64_t ld_s, cudaStream_t stream);
+
 /* A few rows times a 4-bit weight matrix with group scales:
  *   out[m][i] = sum over c of x[m][c] * code[i][c] * scale[i][c / group].
  *   x       [rows][ld_x] BF16 or FP16 (read); 16-byte aligned, ld_x % 8 == 0

@@ -68,6 +68,19 @@ def test_combine_grad_rejections(bq_lib):
     assert f(dw=A + 2 * M) == ALIAS and f(dy=A + 6 * M + 158) == ALIAS
 
 
+def test_quant_w4_rejections(bq_lib):
+    def f(x=A, type=BF16, n=32, k=256, ld_x=256, group=64, q=A + M, ld_q=128, s=A + 2 * M, s_type=F32, ld_s=4):
+        return bq_lib.bq_quant_w4(x, type, n, k, ld_x, group, q, ld_q, s, s_type, ld_s, None)
+    assert f(n=0, x=None) == OK and f(k=0, q=None) == OK
+    assert f(type=5) == SHAPE and f(s_type=-1) == SHAPE and f(group=48) == SHAPE and f(k=288, ld_x=288) == SHAPE
+    assert f(n=-1) == SHAPE and f(ld_x=255) == SHAPE and f(ld_q=127) == SHAPE and f(ld_s=3) == SHAPE
+    for name in ("x", "q", "s"):
+        assert f(**{name: None}) == NULL
+    assert f(x=A + 8) == ALIGN and f(ld_x=260) == ALIGN and f(q=A + M + 4) == ALIGN and f(ld_q=136) == ALIGN
+    assert f(s=A + 2 * M + 2) == ALIGN
+    assert f(q=A + 16) == ALIAS and f(s=A + M + 4092) == ALIAS and f(s=A) == ALIAS
+
+
 def test_matvec_w4_rejections(bq_lib):
     def f(x=A, type=BF16, rows=4, k=256, ld_x=256, q=A + M, n=32, ld_q=128, s=A + 2 * M, s_type=BF16, group=64, ld_s=4,
           out=A + 3 * M, ld_out=32):
