@@ -22,6 +22,8 @@ namespace {
 // columns. One tile makes items small and leaves registers for more warps; two tiles share
 // each fragment of x between them.
 constexpr int kStepCodeBytes = 2048;
+constexpr int kW4Warps = kThreads / 32;
+constexpr int kW4Stages = 3;  // steps of a warp's ring
 
 // ---------------------------------------------------------------- codes to numbers
 // Eight codes of a word -> four pairs of exact integers, pair i = codes (i, i + 4). The
@@ -224,12 +226,11 @@ struct Scales {
 };
 
 // ---------------------------------------------------------------- kernel
-// A CTA takes items of 16 * kRowTiles * kRowWarps weight rows of one expert, over all
-// columns and for every row of x that the expert has, kPassRows at a time. Its warps are
-// kRowWarps in the rows times kColWarps in the columns: a warp walks every kColWarps-th
-// step on its own, through its own ring of asynchronous copies, and the column warps' sums
-// are added in order at the end of an item. The ring runs on over the ends of items, so the
-// memory is never idle in between.
+// A CTA takes items of 16 * kRowTiles weight rows of one expert, over all columns and for
+// every row of x that the expert has, kPassRows at a time. A warp walks every eighth step on
+// its own, through its own ring of asynchronous copies, and the warps' sums are added in
+// order at the end of an item. The ring runs on over the ends of items, so the memory is
+// never idle in between.
 //
 // kPassRows is 8 per column tile of the mma, or 4: the rows then take the even columns of
 // one tile, and half of the sums (the odd columns) need no scaling and no registers.
@@ -244,37 +245,32 @@ constexpr int64_t kStagedBytes = 44 * 1024;
 constexpr int kMaxStagedRows = kStagedBytes / 512;
 inline int64_t staged_row_bytes(int64_t k) { return (k + 255) / 256 * 512; }
 
-template <class T_, class S_, int kGroup_, int kPassRows_, int kRowTiles_, int kRowWarps_, int kColWarps_, int kStages_,
-          int kCtas_, bool kStaged_, bool kExperts_>
+template <class T_, class S_, int kGroup_, int kPassRows_, int kRowTiles_, bool kStaged_, bool kExperts_>
 struct W4Shape {
     using T = T_;
     using S = S_;
     static constexpr int kGroup = kGroup_, kPassRows = kPassRows_, kRowTiles = kRowTiles_;
-    static constexpr int kRowWarps = kRowWarps_, kColWarps = kColWarps_, kStages = kStages_, kCtas = kCtas_;
     static constexpr bool kStaged = kStaged_, kExperts = kExperts_;
     static constexpr bool kEven = kPassRows == 4;
     static constexpr int kTiles = kEven ? 1 : kPassRows / 8;
-    static constexpr int kWarps = kRowWarps * kColWarps, kBlock = 32 * kWarps;
-    static constexpr int kWarpRows = 16 * kRowTiles, kItemRows = kWarpRows * kRowWarps;
+    static constexpr int kItemRows = 16 * kRowTiles;
     static constexpr int kStepCols = 256 / kRowTiles;
-    static constexpr int kScaleSlot = kRowTiles == 1 ? 32 : 16;  // bytes per row and step: up to 8 or 4 FP32 scales
-    static constexpr int kStageBytes = kStepCodeBytes + kWarpRows * kScaleSlot;
+    static constexpr int kScaleSlot = kStepCols / kGroup * (int)sizeof(S) <= 8 ? 16 : kRowTiles == 1 ? 32 : 16;
+    static constexpr int kStageBytes = kStepCodeBytes + kItemRows * kScaleSlot;
     static constexpr int kSumStride = kItemRows + 4;  // rows of x land in different banks
-    static constexpr size_t kRingBytes = (size_t)kWarps * kStages * kStageBytes;
-    static constexpr int kSumFloats = kColWarps * kPassRows * kSumStride;
-    static constexpr size_t kSumBytes = sizeof(float) * kSumFloats;
+    static constexpr size_t kRingBytes = (size_t)kW4Warps * kW4Stages * kStageBytes;
+    static constexpr size_t kSumBytes = sizeof(float) * kW4Warps * kPassRows * kSumStride;
 };
 
 template <class Shape>
-__global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(const __grid_constant__ W4Args a)
+__global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_constant__ W4Args a)
 {
     using T = typename Shape::T;
     using S = typename Shape::S;
     using Bits = typename Value<T>::Bits;
     constexpr int kGroup = Shape::kGroup, kPassRows = Shape::kPassRows, kTiles = Shape::kTiles;
-    constexpr int kRowTiles = Shape::kRowTiles, kColWarps = Shape::kColWarps, kStages = Shape::kStages;
-    constexpr int kBlock = Shape::kBlock, kWarps = Shape::kWarps, kStageBytes = Shape::kStageBytes;
-    constexpr int kWarpRows = Shape::kWarpRows, kItemRows = Shape::kItemRows, kSumStride = Shape::kSumStride;
+    constexpr int kRowTiles = Shape::kRowTiles, kStages = kW4Stages, kStageBytes = Shape::kStageBytes;
+    constexpr int kItemRows = Shape::kItemRows, kSumStride = Shape::kSumStride;
     constexpr int kStepCols = Shape::kStepCols, kStepBytes = kStepCols / 2, kParts = kStepCols / 32;
     constexpr int kScaleCount = kStepCols / kGroup, kScaleSlot = Shape::kScaleSlot, kPerScale = kGroup / 32;
     constexpr bool kStaged = Shape::kStaged, kExperts = Shape::kExperts, kEven = Shape::kEven;
@@ -284,9 +280,9 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
     ExpertRows *const active = reinterpret_cast<ExpertRows *>(smem + Shape::kRingBytes + Shape::kSumBytes);
     unsigned char *const x_smem = smem + Shape::kRingBytes + Shape::kSumBytes +
                                   ((sizeof(ExpertRows) * a.n_experts + 15) & ~(size_t)15);
-    __shared__ int warp_active[kWarps], warp_passes[kWarps];
+    __shared__ int warp_active[kW4Warps], warp_passes[kW4Warps];
     __shared__ float x_unscale[kStaged ? kMaxStagedRows : 1];
-    __shared__ uint32_t x_top[kWarps];
+    __shared__ uint32_t x_top[kW4Warps];
 
     pdl_begin();
     dbg_begin();
@@ -299,7 +295,6 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
     dbg_ready();
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row_warp = warp / kColWarps, col_warp = warp % kColWarps;
     const int g = lane >> 2, t = lane & 3;  // mma fragment row (or column of C) and quad lane
 
     // rows of x a pass takes; staged rows are a whole number of passes, or less than one
@@ -318,7 +313,7 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
             return v < 0 ? 0 : v < slots ? v : slots;
         };
         kept = offset(a.n_experts);
-        for (int base = 0; base < a.n_experts; base += kBlock) {
+        for (int base = 0; base < a.n_experts; base += kThreads) {
             const int e = base + threadIdx.x;
             const int lo = e < a.n_experts ? offset(e) : 0, hi = e < a.n_experts ? offset(e + 1) : 0;
             const unsigned has = __ballot_sync(kFull, hi > lo);
@@ -335,7 +330,7 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
             }
             __syncthreads();
             int at = n_active, before = passes + upto - mine;
-            for (int w = 0; w < kWarps; w++) {
+            for (int w = 0; w < kW4Warps; w++) {
                 at += w < warp ? warp_active[w] : 0;
                 before += w < warp ? warp_passes[w] : 0;
                 n_active += warp_active[w];
@@ -382,28 +377,28 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
 
     // The copying side of the ring: the next step to fetch. A lane copies the 16 bytes
     // f_col of the rows f_row + kLaneRows i, and row `lane`'s scales.
-    constexpr int kPieces = kStepBytes / 16, kLaneRows = 32 / kPieces, kCopies = kWarpRows / kLaneRows;
+    constexpr int kPieces = kStepBytes / 16, kLaneRows = 32 / kPieces, kCopies = kItemRows / kLaneRows;
     const int f_row = lane / kPieces, f_col = lane % kPieces;
     int f_left = item_hi - item_lo;  // items to go, from this run's on
     int f_active = item_lo / row_blocks, f_first = item_lo - f_active * row_blocks;  // the run's expert, first block
     int f_end = 0, f_block = 0, f_rest = 0;    // the run's last block + 1; the block; rows of x from this chunk on
-    int f_passes = 0, f_rows = 0, f_step = col_warp;
+    int f_passes = 0, f_rows = 0, f_step = warp;
     int f_plain = 0;  // steps ahead that need no checks: whole steps of an item of whole rows
     uint32_t f_slot = ring;
     const uint8_t *f_q = nullptr;  // this lane's 16 bytes of the step
     const S *f_s = nullptr;        // this lane's first scale of the step
     const int64_t ld_rows = kLaneRows * a.ld_q;
     const uint32_t dst_code = code_at<kRowTiles>(f_row, f_col), dst_scale = kStepCodeBytes + lane * kScaleSlot;
-    const int my_steps = steps > col_warp ? (steps - col_warp - 1) / kColWarps + 1 : 0;
-    const int my_plain = Sc::plain(scales, a.ld_s, a.expert_s) && whole_steps > col_warp
-                             ? (whole_steps - col_warp - 1) / kColWarps + 1 : 0;
+    const int my_steps = steps > warp ? (steps - warp - 1) / kW4Warps + 1 : 0;
+    const int my_plain = Sc::plain(scales, a.ld_s, a.expert_s) && whole_steps > warp
+                             ? (whole_steps - warp - 1) / kW4Warps + 1 : 0;
     auto chunk_passes = [&](int rest) { return ((rest < chunk_cap ? rest : chunk_cap) + pass_cap - 1) / pass_cap; };
     auto open_chunk = [&]() {  // the run's first block again
-        const int64_t r0 = (int64_t)f_first * kItemRows + row_warp * kWarpRows, e = active[f_active].expert;
+        const int64_t r0 = (int64_t)f_first * kItemRows, e = active[f_active].expert;
         f_block = f_first;
         f_passes = chunk_passes(f_rest);
-        f_q = a.q + e * a.expert_q + (r0 + f_row) * a.ld_q + 16 * f_col + col_warp * kStepBytes;
-        f_s = scales + e * a.expert_s + (r0 + lane) * a.ld_s + col_warp * kScaleCount;
+        f_q = a.q + e * a.expert_q + (r0 + f_row) * a.ld_q + 16 * f_col + warp * kStepBytes;
+        f_s = scales + e * a.expert_s + (r0 + lane) * a.ld_s + warp * kScaleCount;
     };
     auto open_run = [&]() {
         f_end = row_blocks - f_first < f_left ? row_blocks : f_first + f_left;
@@ -411,13 +406,13 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
         open_chunk();
     };
     auto open_rows = [&]() {  // and the pass over them
-        const int r0 = f_block * kItemRows + row_warp * kWarpRows;
-        f_rows = a.n - r0 < kWarpRows ? (int)(a.n - r0) : kWarpRows;
-        f_step = col_warp;
-        f_plain = f_rows == kWarpRows ? my_plain : 0;
+        const int r0 = f_block * kItemRows;
+        f_rows = a.n - r0 < kItemRows ? (int)(a.n - r0) : kItemRows;
+        f_step = warp;
+        f_plain = f_rows == kItemRows ? my_plain : 0;
     };
-    const int64_t back_q = (int64_t)my_steps * kColWarps * kStepBytes;
-    const int64_t back_s = (int64_t)my_steps * kColWarps * kScaleCount;
+    const int64_t back_q = (int64_t)my_steps * kW4Warps * kStepBytes;
+    const int64_t back_s = (int64_t)my_steps * kW4Warps * kScaleCount;
     auto advance = [&]() {  // past a pass's last step
         f_q -= back_q;
         f_s -= back_s;
@@ -446,11 +441,11 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
             const uint8_t *q = f_q;
 #pragma unroll
             for (int i = 0; i < kCopies; i++, q += ld_rows) lane_copy16(f_slot + code_row<kRowTiles>(dst_code, i), q);
-            if (kWarpRows == 32 || lane < kWarpRows) Sc::fetch_plain(f_slot + dst_scale, f_s);
+            if (kItemRows == 32 || lane < kItemRows) Sc::fetch_plain(f_slot + dst_scale, f_s);
             f_plain--;
-            f_step += kColWarps;
-            f_q += kColWarps * kStepBytes;
-            f_s += kColWarps * kScaleCount;
+            f_step += kW4Warps;
+            f_q += kW4Warps * kStepBytes;
+            f_s += kW4Warps * kScaleCount;
         } else if (f_left > 0 && f_step < steps) {
             const bool in_cols = f_step * kStepBytes + 16 * f_col < a.k / 2;
 #pragma unroll
@@ -461,11 +456,11 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
             }
             const int left = (int)(a.k / kGroup) - f_step * kScaleCount;
             const bool in = lane < f_rows;
-            if (kWarpRows == 32 || lane < kWarpRows)
+            if (kItemRows == 32 || lane < kItemRows)
                 Sc::fetch(f_slot + dst_scale, in ? f_s : scales, in ? (left < kScaleCount ? left : kScaleCount) : 0);
-            f_step += kColWarps;
-            f_q += kColWarps * kStepBytes;
-            f_s += kColWarps * kScaleCount;
+            f_step += kW4Warps;
+            f_q += kW4Warps * kStepBytes;
+            f_s += kW4Warps * kScaleCount;
         }
         lane_copy_commit();
         f_slot = f_slot == ring + (kStages - 1) * kStageBytes ? ring : f_slot + kStageBytes;
@@ -485,8 +480,8 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
     auto stage_x = [&](const ExpertRows &er, int p0, int rows) {
         const int padded = steps * kStepCols;
         const bool split = rows == 1;
-        const int first = 8 * (split ? (int)threadIdx.x : lane), stride = 8 * (split ? kBlock : 32);
-        for (int r = split ? 0 : warp; r < rows; r += split ? 1 : kWarps) {
+        const int first = 8 * (split ? (int)threadIdx.x : lane), stride = 8 * (split ? kThreads : 32);
+        for (int r = split ? 0 : warp; r < rows; r += split ? 1 : kW4Warps) {
             int row = p0 + r;
             if (kExperts && a.order) row = dbg_ok(a.order + row, 4, false) ? __ldg(a.order + row) / a.top_k : 0;
             if (row < 0 || row >= a.x_rows) row = 0;  // a wrong plan
@@ -505,7 +500,7 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
                     if (lane == 0) x_top[warp] = top;
                     __syncthreads();
 #pragma unroll
-                    for (int w = 0; w < kWarps; w++) top = max(top, x_top[w]);
+                    for (int w = 0; w < kW4Warps; w++) top = max(top, x_top[w]);
                 }
                 const int e = max((int)(top >> 7), 15);  // biased exponent of the largest value
                 up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
@@ -548,13 +543,13 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
             const int chunk = next_chunk;
             next_chunk = er.hi - chunk > chunk_cap ? chunk + chunk_cap : er.hi;
             if constexpr (kStaged) {
-                __syncthreads();  // the last readers of the rows before
+                __syncthreads();  // the readers of the rows before
                 stage_x(er, chunk, next_chunk - chunk);
             }
             for (int block = first_block; block < end_block; block++) {
                 const int r0 = block * kItemRows;
                 // rows g + 8 i all start in the same half of a word
-                const int row_skew = (int)(er.expert * a.expert_s + (r0 + row_warp * kWarpRows + g) * a.ld_s) & 1;
+                const int row_skew = (int)(er.expert * a.expert_s + (r0 + g) * a.ld_s) & 1;
                 for (int p0 = chunk; p0 < next_chunk; p0 += pass_cap) {
                     const int pass_rows = next_chunk - p0 < pass_cap ? next_chunk - p0 : pass_cap;
                     const int in_chunk = kStaged ? p0 - chunk : 0;
@@ -567,7 +562,7 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
                         const int r = kEven ? g / 2 : g;
                         const int last = pass_rows - 1;
                         const int row = in_chunk + (r < last ? r : last);
-                        x_src = smem_u32(x_smem) + ((col_warp * kParts * chunk_cap + row) * 4 + t) * 16;
+                        x_src = smem_u32(x_smem) + ((warp * kParts * chunk_cap + row) * 4 + t) * 16;
                     }
 #pragma unroll
                     for (int m = 0; m < (kStaged ? 0 : kTiles); m++) {
@@ -575,7 +570,7 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
                         int row = p;
                         if (kExperts && a.order) row = dbg_ok(a.order + p, 4, false) ? __ldg(a.order + p) / a.top_k : 0;
                         if (row < 0 || row >= a.x_rows) row = 0;  // a wrong plan
-                        x[m] = static_cast<const T *>(a.x) + row * a.ld_x + 8 * t + col_warp * kStepCols;
+                        x[m] = static_cast<const T *>(a.x) + row * a.ld_x + 8 * t + warp * kStepCols;
                     }
                     // x of a step is loaded at the end of the step before it
                     auto load_x = [&](int step) {
@@ -594,12 +589,12 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
                                                                  ? ld_keep_v4(x[m] + 32 * j) : make_uint4(0, 0, 0, 0);
                         }
 #pragma unroll
-                        for (int m = 0; m < kTiles; m++) x[m] += kColWarps * kStepCols;
+                        for (int m = 0; m < kTiles; m++) x[m] += kW4Warps * kStepCols;
                     };
-                    load_x(col_warp);
+                    load_x(warp);
                     float acc[kRowTiles][kTiles][4] = {};  // with even columns only, [0] and [2] are used
                     float c[kRowTiles][kTiles][4];
-                    for (int step = col_warp; step < steps; step += kColWarps) {
+                    for (int step = warp; step < steps; step += kW4Warps) {
                         lane_copy_wait<kStages - 2>();
                         __syncwarp();
                         fetch();
@@ -672,14 +667,14 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
                             }
                         }
                         if constexpr (kStaged)
-                            x_src += kColWarps * kParts * 64 * chunk_cap;
+                            x_src += kW4Warps * kParts * 64 * chunk_cap;
                         else
-                            load_x(step + kColWarps);
+                            load_x(step + kW4Warps);
                         slot = slot == ring + (kStages - 1) * kStageBytes ? ring : slot + kStageBytes;
                     }
-                    // column warps' sums: [col warp][row of x][weight row]
+                    // the warps' sums: [warp][row of x][weight row]
                     __syncthreads();  // the readers of the item before
-                    float *mine = sums + col_warp * kPassRows * kSumStride + row_warp * kWarpRows;
+                    float *mine = sums + warp * kPassRows * kSumStride;
 #pragma unroll
                     for (int r = 0; r < kRowTiles; r++)
 #pragma unroll
@@ -689,16 +684,16 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
                                 mine[(kEven ? t : 8 * m + 2 * t + (i & 1)) * kSumStride + 16 * r + g + 8 * (i >> 1)] =
                                     acc[r][m][i];
                     __syncthreads();
-                    for (int i = threadIdx.x; i < pass_rows * kItemRows; i += kBlock) {
+                    for (int i = threadIdx.x; i < pass_rows * kItemRows; i += kThreads) {
                         const int m = i / kItemRows, r = i % kItemRows;
-                        float v = sums[m * kSumStride + r];
+                        if (r0 + r >= a.n) continue;
+                        const float *of = sums + m * kSumStride + r;
+                        float v = of[0];
 #pragma unroll
-                        for (int w = 1; w < kColWarps; w++)
-                            v = __fadd_rn(v, sums[(w * kPassRows + m) * kSumStride + r]);
+                        for (int w = 1; w < kW4Warps; w++) v = __fadd_rn(v, of[w * kPassRows * kSumStride]);
                         if (kStaged) v = __fmul_rn(v, x_unscale[in_chunk + m]);
                         T *dst = static_cast<T *>(a.out) + (p0 + m) * a.ld_out + r0 + r;
-                        if (r0 + r < a.n && dbg_ok(dst, sizeof(T), true))
-                            *reinterpret_cast<Bits *>(dst) = Value<T>::round(v);
+                        if (dbg_ok(dst, sizeof(T), true)) *reinterpret_cast<Bits *>(dst) = Value<T>::round(v);
                     }
                 }
             }
@@ -707,7 +702,7 @@ __global__ void __launch_bounds__(Shape::kBlock, Shape::kCtas) matvec_w4_kernel(
     lane_copy_wait<0>();
     if constexpr (kExperts) {
         for (int64_t p = kept + blockIdx.x; p < a.slots; p += gridDim.x)
-            for (int64_t c = threadIdx.x; c < a.n; c += kBlock) {
+            for (int64_t c = threadIdx.x; c < a.n; c += kThreads) {
                 T *dst = static_cast<T *>(a.out) + p * a.ld_out + c;
                 if (dbg_ok(dst, sizeof(T), true)) *reinterpret_cast<Bits *>(dst) = 0;
             }
@@ -723,12 +718,12 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st)
     size_t smem = Shape::kRingBytes + Shape::kSumBytes + sizeof(ExpertRows) * a.n_experts;
     if (Shape::kStaged) smem = (smem + 15) / 16 * 16 + staged_row_bytes(a.k) * a.staged_rows;
     int grid = 0;
-    if (cudaError_t e = grid_for((const void *)kernel, blocks * with_rows * Shape::kWarps, &grid, smem, Shape::kBlock))
+    if (cudaError_t e = grid_for((const void *)kernel, blocks * with_rows * kW4Warps, &grid, smem, kThreads))
         return e;
     int sms = 1;
     if (cudaError_t e = sm_count(&sms)) return e;
     a.ctas_per_sm = grid % sms == 0 ? grid / sms : 1;
-    return launch_kernel_block(kernel, grid, Shape::kBlock, smem, st, a);
+    return launch_kernel_block(kernel, grid, kThreads, smem, st, a);
 }
 
 template <class T, class S, int kGroup, bool kExperts>
@@ -738,12 +733,10 @@ cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
     if (rows <= 4 && rows <= cap) {
         const int64_t most = kExperts ? cap : rows;
         a.staged_rows = (int)(most < 4 ? most : most / 4 * 4);
-        return launch_w4<W4Shape<T, S, kGroup, 4, 1, 1, 8, 3, 2, true, kExperts>>(a, st);
+        return launch_w4<W4Shape<T, S, kGroup, 4, 1, true, kExperts>>(a, st);
     }
-    if (rows <= 8) return launch_w4<W4Shape<T, S, kGroup, 8, 2, 1, 8, 3, 2, false, kExperts>>(a, st);
-    const int64_t tiles = (a.n + 31) / 32 * (kExperts ? (a.slots < a.n_experts ? a.slots : a.n_experts) : 1);
-    return tiles >= 480 ? launch_w4<W4Shape<T, S, kGroup, 16, 2, 4, 4, 3, 1, false, kExperts>>(a, st)
-                        : launch_w4<W4Shape<T, S, kGroup, 16, 2, 1, 8, 3, 2, false, kExperts>>(a, st);
+    return rows <= 8 ? launch_w4<W4Shape<T, S, kGroup, 8, 2, false, kExperts>>(a, st)
+                     : launch_w4<W4Shape<T, S, kGroup, 16, 2, false, kExperts>>(a, st);
 }
 
 template <class T, class S, bool kExperts>
