@@ -14,12 +14,13 @@ namespace {
 
 // ---------------------------------------------------------------- sort
 // A stable counting sort. Every warp owns a run of consecutive slots and a row of
-// counters in shared memory, one per expert. It counts its slots 32 at a time:
-// match_any gives each lane the lanes with the same id, and the lowest of them adds their
-// number, so no counter is ever contended. (A ballot per bit of the id instead took 13.1
-// us for 524288 slots of 64 experts, match_any 11.4.) The counters are then turned into the
-// first place of each (warp, expert), and a second walk over the same slots hands the
-// places out in lane order. Nothing depends on the order in which warps run.
+// counters in shared memory, one per expert. It counts its slots with shared-memory
+// additions, whose order does not matter. The counters are then turned into the first place
+// of each (warp, expert), and a second walk over the same slots, 32 at a time, hands the
+// places out in lane order: match_any gives each lane the lanes with the same id. Nothing
+// depends on the order in which warps run. match_any is the slow part, an SM finishes one
+// every 49 cycles: with it in the counting too, 524288 slots of 64 experts took 11.4 us, and
+// with a ballot per bit of the id in its place 13.1 us.
 //
 // Lane w of a warp holds warp w's counter when the counters are summed or scanned over the
 // warps; a row of counters has an odd stride, so that these 32 lie in different banks.
@@ -99,9 +100,7 @@ __device__ __forceinline__ void count_run(const Id *ids, SlotRun run, int n_expe
 #pragma unroll
         for (int k = 0; k < kAhead; k++) {
             if (i0 + 32 * k >= run.hi) break;
-            const unsigned same = __match_any_sync(kFull, e[k]);
-            if (e[k] >= 0 && lane == __ffs(same) - 1) mine[e[k]] += __popc(same);
-            __syncwarp();
+            if (e[k] >= 0) atomicAdd(&mine[e[k]], 1);
         }
     }
 }
@@ -297,11 +296,32 @@ __device__ __forceinline__ int64_t kept_places(const int32_t *offsets, int n_exp
     return kept < 0 ? 0 : kept < slots ? kept : slots;
 }
 
+// The warp units of a row kernel: unit u = t * per_token + v is segment v of token t's row. A
+// walker steps from one of a warp's units to its next without a division.
+struct Units {
+    int64_t t, tokens, dt;
+    int v, per_token, dv;
+    __device__ __forceinline__ Units(int64_t tokens_, int per_token_) : tokens(tokens_), per_token(per_token_)
+    {
+        const int64_t block_warps = blockDim.x >> 5, warps = gridDim.x * block_warps;
+        const int64_t u = blockIdx.x * block_warps + (threadIdx.x >> 5);
+        t = u / per_token, v = (int)(u - t * per_token);
+        dt = warps / per_token, dv = (int)(warps - dt * per_token);
+    }
+    __device__ __forceinline__ bool more() const { return t < tokens; }
+    __device__ __forceinline__ void step()
+    {
+        t += dt, v += dv;
+        if (v >= per_token) v -= per_token, t++;
+    }
+};
+
 // ---------------------------------------------------------------- gather
 // out[inverse[t, j]] = x[t]: a warp holds a segment of one token's row in registers and
 // stores it to each of the token's places, so every row of x is read once. Rows past the
 // kept places are zeros.
 constexpr int kGatherPieces = 4;
+constexpr int kGatherRows = 4;
 
 template <class T, bool kWide>
 __global__ void __launch_bounds__(kThreads)
@@ -318,52 +338,65 @@ gather_kernel(const T *__restrict__ x, int64_t tokens, int64_t hidden, int64_t l
     dbg_allow(offsets, 4ll * (n_experts + 1), false);
     dbg_allow_2d(out, slots, hidden * sizeof(T), ld_out * sizeof(T), true);
     dbg_ready();
-    const int lane = threadIdx.x & 31, block_warps = blockDim.x >> 5;
-    const int64_t warp = (int64_t)blockIdx.x * block_warps + (threadIdx.x >> 5);
-    const int64_t warps = (int64_t)gridDim.x * block_warps;
+    const int lane = threadIdx.x & 31;
     constexpr int kSegment = 32 * kGatherPieces;
     const int64_t pieces = C::pieces(hidden), segments = (pieces + kSegment - 1) / kSegment;
     const void *x_end = x + (tokens - 1) * ld_x + hidden;
-    for (int64_t u = warp; u < tokens * segments; u += warps) {
-        const int64_t t = u / segments, i0 = (u - t * segments) * kSegment + lane;
+    auto places = [&](int64_t t, int j0) {  // lane j: the place of slot j0 + j
+        return j0 + lane < top_k ? slot_place(inverse, t * top_k + j0 + lane, slots) : -1;
+    };
+    for (Units u(tokens, (int)segments); u.more(); u.step()) {
+        const int64_t t = u.t;
         const T *row = x + t * ld_x;
+        const int64_t i0 = (int64_t)u.v * kSegment + lane;
         typename C::Raw raw[kGatherPieces];
         if constexpr (kWide) {
 #pragma unroll
             for (int i = 0; i < kGatherPieces; i++)
                 if (i0 + 32 * i < pieces) C::fetch(raw[i], row, C::column(row, i0 + 32 * i), x, x_end);
         }
-        for (int j = 0; j < top_k; j++) {
-            const int p = slot_place(inverse, t * top_k + j, slots);
-            if (p < 0) continue;
-            T *dst = out + p * ld_out;
-            if constexpr (!kWide) {  // every place has its own alignment; after the first from L1
+        for (int j0 = 0; j0 < top_k; j0 += 32) {
+            const int place = places(t, j0);
+            for (unsigned rest = __ballot_sync(kFull, place >= 0); rest != 0;) {
+                T *dst[kGatherRows];
+                bool has[kGatherRows];
 #pragma unroll
-                for (int i = 0; i < kGatherPieces; i++) {
-                    const int64_t c = C::column(dst, i0 + 32 * i);
-                    if (i0 + 32 * i < pieces && C::inside(c, hidden)) C::fetch(raw[i], row, c, x, x_end);
+                for (int r = 0; r < kGatherRows; r++) {
+                    has[r] = rest != 0;
+                    dst[r] = out + __shfl_sync(kFull, place, has[r] ? __ffs(rest) - 1 : 0) * ld_out;
+                    rest &= rest - 1;  // 0 stays 0
                 }
-            }
 #pragma unroll
-            for (int i = 0; i < kGatherPieces; i++) {
-                const int64_t c = C::column(dst, i0 + 32 * i);
-                if (i0 + 32 * i >= pieces || !C::inside(c, hidden)) continue;
-                P v;
-                C::take(v, raw[i], row, c, hidden, x, x_end);
-                C::store(v, dst, c, hidden);
+                for (int r = 0; r < kGatherRows; r++) {
+                    if (!has[r]) break;
+                    if constexpr (!kWide) {  // every place has its own alignment; after the first from L1
+#pragma unroll
+                        for (int i = 0; i < kGatherPieces; i++) {
+                            const int64_t c = C::column(dst[r], i0 + 32 * i);
+                            if (i0 + 32 * i < pieces && C::inside(c, hidden)) C::fetch(raw[i], row, c, x, x_end);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kGatherPieces; i++) {
+                        const int64_t c = C::column(dst[r], i0 + 32 * i);
+                        if (i0 + 32 * i >= pieces || !C::inside(c, hidden)) continue;
+                        P v;
+                        C::take(v, raw[i], row, c, hidden, x, x_end);
+                        C::store(v, dst[r], c, hidden);
+                    }
+                }
             }
         }
     }
     const int64_t kept = kept_places(offsets, n_experts, slots);
     P z;
     z.zero();
-    for (int64_t u = warp; u < (slots - kept) * segments; u += warps) {
-        const int64_t r = u / segments, i0 = (u - r * segments) * kSegment + lane;
-        T *dst = out + (kept + r) * ld_out;
+    for (Units w(slots - kept, (int)segments); w.more(); w.step()) {
+        T *dst = out + (kept + w.t) * ld_out;
 #pragma unroll
         for (int i = 0; i < kGatherPieces; i++) {
-            const int64_t c = C::column(dst, i0 + 32 * i);
-            if (i0 + 32 * i < pieces && C::inside(c, hidden)) C::store(z, dst, c, hidden);
+            const int64_t at = (int64_t)w.v * kSegment + lane + 32 * i, c = C::column(dst, at);
+            if (at < pieces && C::inside(c, hidden)) C::store(z, dst, c, hidden);
         }
     }
 }
@@ -394,14 +427,12 @@ combine_kernel(const T *__restrict__ y, int64_t ld_y, const float *__restrict__ 
     dbg_allow(inverse, 4 * slots, false);
     dbg_allow_2d(out, tokens, hidden * sizeof(T), ld_out * sizeof(T), true);
     dbg_ready();
-    const int lane = threadIdx.x & 31, block_warps = blockDim.x >> 5;
-    const int64_t warp = (int64_t)blockIdx.x * block_warps + (threadIdx.x >> 5);
-    const int64_t warps = (int64_t)gridDim.x * block_warps;
+    const int lane = threadIdx.x & 31;
     constexpr int kPieces = kCombinePieces<kWide>, kSegment = 32 * kPieces;
     const int64_t pieces = C::pieces(hidden), segments = (pieces + kSegment - 1) / kSegment;
     const void *y_end = y + (slots - 1) * ld_y + hidden;
-    for (int64_t u = warp; u < tokens * segments; u += warps) {
-        const int64_t t = u / segments, i0 = (u - t * segments) * kSegment + lane;
+    for (Units u(tokens, (int)segments); u.more(); u.step()) {
+        const int64_t t = u.t, i0 = (int64_t)u.v * kSegment + lane;
         T *dst = out + t * ld_out;
         int64_t c[kPieces];
         bool in[kPieces];
@@ -452,9 +483,7 @@ combine_kernel(const T *__restrict__ y, int64_t ld_y, const float *__restrict__ 
         for (int k = 0; k < kPieces; k++) {
             if (!in[k]) continue;
             P v;
-            v.zero();
-#pragma unroll
-            for (int n = 0; n < P::N; n++) v.set(n, acc[k][n]);
+            v.round(acc[k]);
             C::store(v, dst, c[k], hidden);
         }
     }
@@ -502,7 +531,7 @@ combine_grad_kernel(const T *__restrict__ dout, int64_t ld_dout, const T *__rest
         for (int s = 0; s < kGradSlots; s++) {
             const int64_t slot = t * top_k + j0 + s;
             place[s] = j0 + s < top_k ? slot_place(inverse, slot, slots) : -1;
-            w[s] = place[s] >= 0 && dbg_ok(weights + slot, 4, false) ? __ldg(weights + slot) : 0.0f;
+            w[s] = j0 + s < top_k && dbg_ok(weights + slot, 4, false) ? __ldg(weights + slot) : 0.0f;
         }
         const T *d_row = dout + t * ld_dout;
         for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) {
@@ -525,12 +554,13 @@ combine_grad_kernel(const T *__restrict__ dout, int64_t ld_dout, const T *__rest
                 C::take(v, y_raw[s], y + place[s] * ld_y, c, hidden, y, y_end);
                 C::keep(d, c, hidden);
                 C::keep(v, c, hidden);
-                g.zero();
+                float scaled[P::N];
 #pragma unroll
                 for (int n = 0; n < P::N; n++) {
                     dot[s] = __fmaf_rn(d.at(n), v.at(n), dot[s]);
-                    g.set(n, __fmul_rn(w[s], d.at(n)));
+                    scaled[n] = __fmul_rn(w[s], d.at(n));
                 }
+                g.round(scaled);
                 C::store(g, dst, c, hidden);
             }
         }
@@ -601,10 +631,24 @@ cudaError_t launch_combine_grad_t(const RowArgs &a, const void *dout, int64_t ld
 {
     auto kernel = combine_grad_kernel<T, kWide>;
     const int64_t pieces = Cut<T, kWide>::pieces(a.hidden);
-    const int64_t want = (pieces + 31) / 32 * 32;  // without columns one warp writes the zeros of dw
-    const int block = static_cast<int>(want < 32 ? 32 : want < kGradMaxThreads ? want : kGradMaxThreads);
     const int64_t units = a.tokens * ((a.top_k + kGradSlots - 1) / kGradSlots);
-    int grid = 0;
+    int sms = 1, grid = 0;
+    if (cudaError_t e = sm_count(&sms)) return e;
+    // Few units go out in few rounds over the row, else the CTA is the largest whose rounds (four,
+    // or as many as it takes) are fullest: 257 pieces take 3 rounds of 96 threads (12.6 us for
+    // 3000 tokens of 1028 FP32 columns; 14.5 us with 160 threads, 16.0 us with 256).
+    const int64_t least = (pieces + kGradMaxThreads - 1) / kGradMaxThreads;
+    const int64_t most = units < (int64_t)16 * sms || least > 4 ? least : 4;
+    int block = 32;  // without columns one warp writes the zeros of dw
+    double fullest = 0.0;
+    for (int threads = kGradMaxThreads; threads >= 32; threads -= 32) {
+        const int64_t rounds = (pieces + threads - 1) / threads;
+        const double full = (double)pieces / (double)(rounds * threads);
+        if (rounds <= most && full > fullest) {
+            fullest = full;
+            block = threads;
+        }
+    }
     if (cudaError_t e = grid_for((const void *)kernel, units * (block / 32), &grid, 0, block)) return e;
     return launch_kernel_block(kernel, grid, block, 0, st, static_cast<const T *>(dout), ld_dout,
                                static_cast<const T *>(y), ld_y, weights, a.inverse, offsets, n_experts, a.tokens,

@@ -11,12 +11,18 @@ template <>
 struct Value<__nv_bfloat16> {
     static __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
     static __device__ __forceinline__ uint16_t round(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+    static __device__ __forceinline__ uint32_t round2(float lo, float hi) { return f32x2_to_bf16x2(make_float2(lo, hi)); }
     using Bits = uint16_t;
 };
 template <>
 struct Value<__half> {
     static __device__ __forceinline__ float widen(uint16_t b) { return __half2float(__ushort_as_half(b)); }
     static __device__ __forceinline__ uint16_t round(float v) { return __half_as_ushort(__float2half_rn(v)); }
+    static __device__ __forceinline__ uint32_t round2(float lo, float hi)
+    {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
     using Bits = uint16_t;
 };
 template <>
@@ -54,7 +60,16 @@ struct Piece {
             w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | ((uint32_t)b << 16) : (w[i / 2] & 0xffff0000u) | b;
     }
     __device__ __forceinline__ float at(int i) const { return Value<T>::widen(bits(i)); }
-    __device__ __forceinline__ void set(int i, float v) { set_bits(i, Value<T>::round(v)); }
+    __device__ __forceinline__ void round(const float (&v)[N])
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; i++) w[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 2; i++) w[i] = Value<T>::round2(v[2 * i], v[2 * i + 1]);
+        }
+    }
     __device__ __forceinline__ void put(const uint4 v) { w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w; }
 };
 
@@ -62,9 +77,9 @@ struct Piece {
 // pieces (kWide), piece i is the columns [N i, N i + N). Else the pieces are the 16-byte
 // words of the row that is written: its first and last may stick out of the row, and a row
 // that is read lies at some other alignment to them, so a piece of it is put together from
-// the two aligned words that hold it. Rows are never read one value at a time but at the
-// ends of rows and of the buffer: 10551 tokens' gather gradient of 919 BF16 columns took
-// 24.0 us so.
+// the two aligned words that hold it. Only the ends of the buffer are read value by value:
+// 10551 tokens' gather gradient of 919 BF16 columns took 24.0 us with whole rows so, 15.1 us
+// in words.
 template <class T, bool kWide>
 struct Cut {
     using P = Piece<T>;
@@ -118,24 +133,29 @@ struct Cut {
             for (int i = 0; i < 5; i++) r[i] = skew & 4 ? s[i + 1] : s[i];
 #pragma unroll
             for (int i = 0; i < 4; i++) v.w[i] = __funnelshift_r(r[i], r[i + 1], 8 * (skew & 2));
-        } else {  // at the buffer's ends
-            v.zero();
-#pragma unroll 1
-            for (int i = 0; i < N; i++)
-                if (c + i >= 0 && c + i < hidden && dbg_ok(row + c + i, sizeof(T), false)) {
-                    const typename P::Bits b = __ldg(reinterpret_cast<const typename P::Bits *>(row + c + i));
-#pragma unroll
-                    for (int k = 0; k < N; k++)
-                        if (k == i) v.set_bits(k, b);
-                }
+        } else {
+            v.put(at_end(row + c, -c, hidden - c));
         }
+    }
+    // a piece at the buffer's ends, value by value: those with lo <= i < hi
+    static __device__ __noinline__ uint4 at_end(const T *p, int64_t lo, int64_t hi)
+    {
+        P v;
+        v.zero();
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (i >= lo && i < hi && dbg_ok(p + i, sizeof(T), false))
+                v.set_bits(i, __ldg(reinterpret_cast<const typename P::Bits *>(p + i)));
+        return make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
     }
     static __device__ __forceinline__ void keep(P &v, int64_t c, int64_t hidden)
     {
-        if (kWide || (c >= 0 && c + N <= hidden)) return;
+        if constexpr (!kWide) {
+            if (c >= 0 && c + N <= hidden) return;
 #pragma unroll
-        for (int i = 0; i < N; i++)
-            if (c + i < 0 || c + i >= hidden) v.set_bits(i, 0);
+            for (int i = 0; i < N; i++)
+                if (c + i < 0 || c + i >= hidden) v.set_bits(i, 0);
+        }
     }
     static __device__ __forceinline__ void store(const P &v, T *row, int64_t c, int64_t hidden)
     {
