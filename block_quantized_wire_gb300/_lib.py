@@ -92,6 +92,9 @@ def _open(path: str):
 def load():
     """Load libbq.so once; raise if it is not built or does not load."""
     global _lib
+    lib = _lib
+    if lib is not None:
+        return lib
     with _lock:
         if _lib is None:
             _lib = _open(library_path())

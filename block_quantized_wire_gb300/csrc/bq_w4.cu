@@ -28,7 +28,7 @@ constexpr int kW4Stages = 3;  // steps of a warp's ring
 // ---------------------------------------------------------------- codes to numbers
 // Eight codes of a word -> four pairs of exact integers, pair i = codes (i, i + 4). The
 // four bits, their sign bit flipped (which adds 8), become the low mantissa bits of a
-// power of two whose ulp is 1, and one exact subtraction removes the power and the 8.
+// power of two whose ulp is 1, and one exact operation removes the power and the 8.
 template <class T>
 struct Codes;
 
@@ -40,14 +40,19 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t 
     return r;
 }
 
+// BF16 codes come out times 2^-12, so that no group's binary32 sum overflows where its
+// product with the scale would not (128 codes of 8 times the largest BF16 value are 2^138);
+// the sums of all groups are brought up again at the end. Both are exact, but for products
+// below 2^-149.
 template <>
 struct Codes<__nv_bfloat16> {
+    static constexpr float kUp = 4096.0f;
     static __device__ __forceinline__ void widen(uint32_t w, uint32_t (&v)[4])
     {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const uint32_t h = and_xor(w >> (4 * i), 0x000f000fu, 0x43084308u);  // 128 + 8 + c
-            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(h), "r"(0x43084308u));
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(h), "r"(0x39803980u), "r"(0xbd08bd08u));
         }
     }
     // c = a * b, or c += a * b
@@ -69,6 +74,7 @@ struct Codes<__nv_bfloat16> {
 
 template <>
 struct Codes<__half> {
+    static constexpr float kUp = 1.0f;
     static __device__ __forceinline__ void widen(uint32_t w, uint32_t (&v)[4])
     {
         // The mantissa holds both codes of a byte: 1024 + 8 + c from the low one, 1024 + 16 (8 +
@@ -243,6 +249,7 @@ struct ExpertRows {
 // padded to whole steps.
 constexpr int64_t kStagedBytes = 44 * 1024;
 constexpr int kMaxStagedRows = kStagedBytes / 512;
+constexpr int64_t kStagedItems = 1216;  // 16-row items that make staging pay: four for each of 304 CTAs
 inline int64_t staged_row_bytes(int64_t k) { return (k + 255) / 256 * 512; }
 
 template <class T_, class S_, int kGroup_, int kPassRows_, int kRowTiles_, bool kStaged_, bool kExperts_>
@@ -692,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
 #pragma unroll
                         for (int w = 1; w < kW4Warps; w++) v = __fadd_rn(v, of[w * kPassRows * kSumStride]);
                         if (kStaged) v = __fmul_rn(v, x_unscale[in_chunk + m]);
+                        if (Codes<Product>::kUp != 1.0f) v = __fmul_rn(v, Codes<Product>::kUp);
                         T *dst = static_cast<T *>(a.out) + (p0 + m) * a.ld_out + r0 + r;
                         if (dbg_ok(dst, sizeof(T), true)) *reinterpret_cast<Bits *>(dst) = Value<T>::round(v);
                     }
@@ -729,14 +737,19 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st)
 template <class T, class S, int kGroup, bool kExperts>
 cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
 {
+    // Staging pays where one row goes over many long weight rows, so that few CTAs stage it
+    // and each uses it for long: one token's eight experts of 4096 x 7168 took 30.4 us staged
+    // and W4E1 us directly, ten tokens' experts of 3358 x 2944 21.6 us staged and 17.0 us
+    // directly, one row times 2932 x 7808 8.4 and 7.3 us.
+    const int64_t used = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
     const int64_t cap = kStagedBytes / staged_row_bytes(a.k);
-    if (rows <= 4 && rows <= cap) {
-        const int64_t most = kExperts ? cap : rows;
-        a.staged_rows = (int)(most < 4 ? most : most / 4 * 4);
+    if (rows == 1 && a.k >= 4096 && cap >= 1 && used * (a.n / 16) >= kStagedItems) {
+        a.staged_rows = (int)(!kExperts ? 1 : cap < 4 ? cap : cap / 4 * 4);
         return launch_w4<W4Shape<T, S, kGroup, 4, 1, true, kExperts>>(a, st);
     }
-    return rows <= 8 ? launch_w4<W4Shape<T, S, kGroup, 8, 2, false, kExperts>>(a, st)
-                     : launch_w4<W4Shape<T, S, kGroup, 16, 2, false, kExperts>>(a, st);
+    return rows <= 4   ? launch_w4<W4Shape<T, S, kGroup, 4, 2, false, kExperts>>(a, st)
+           : rows <= 8 ? launch_w4<W4Shape<T, S, kGroup, 8, 2, false, kExperts>>(a, st)
+                       : launch_w4<W4Shape<T, S, kGroup, 16, 2, false, kExperts>>(a, st);
 }
 
 template <class T, class S, bool kExperts>

@@ -56,7 +56,7 @@ def _on(stream, device: int) -> int:
 
 
 def _flat(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
@@ -72,12 +72,13 @@ def _row_type(t: torch.Tensor, name: str) -> int:
 
 def _rows(t: torch.Tensor, rows: int, cols: int, dtype: torch.dtype, name: str):
     """(pointer, leading dimension) of a row-major [rows, cols] view."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
+        raise ValueError(f"{name}: expected shape ({rows}, {cols}), got {tuple(shape)}")
     ld, unit = t.stride()
-    if cols > 1 and unit != 1:
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name}: expected unit column stride")
     return t.data_ptr(), ld if rows > 1 else cols
 

@@ -12,29 +12,36 @@ from typing import Optional
 import torch
 
 from ._lib import check, load
-from .experts import _flat, _here, _on, _row_type, _rows
+from .experts import ROW_TYPES, _flat, _here, _on, _row_type, _rows
+
+
+GROUPS = (32, 64, 128)
 
 
 def _weights(call: str, q: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, dims: int):
-    """(n, k, group, scale type) of a weight matrix; the checks that need the tensors."""
-    if q.dtype != torch.uint8:
+    """(n, k, group, x type, scale type, row strides of q and scales) of a weight matrix; the
+    checks that need the tensors."""
+    x_type, s_type, q_shape, s_shape, x_shape = x.dtype, scales.dtype, q.shape, scales.shape, x.shape
+    if q.dtype is not torch.uint8:
         raise TypeError(f"{call}: q must be uint8, got {q.dtype}")
-    if q.dim() != dims or scales.shape[:-1] != q.shape[:-1]:
+    if len(q_shape) != dims or q_shape[:-1] != s_shape[:-1]:
         raise ValueError(f"{call}: q and scales must have {dims} dimensions, alike but the last")
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"{call}: x must be bfloat16 or float16, got {x.dtype}")
-    if scales.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"{call}: scales must be {x.dtype} or float32, got {scales.dtype}")
-    n, k = q.shape[-2], 2 * q.shape[-1]
-    groups = scales.shape[-1]
-    if x.dim() != 2 or x.shape[1] != k:
+    if x_type is not torch.bfloat16 and x_type is not torch.float16:
+        raise TypeError(f"{call}: x must be bfloat16 or float16, got {x_type}")
+    if s_type is not x_type and s_type is not torch.float32:
+        raise TypeError(f"{call}: scales must be {x_type} or float32, got {s_type}")
+    n, half, groups = q_shape[-2], q_shape[-1], s_shape[-1]
+    k = 2 * half
+    if len(x_shape) != 2 or x_shape[1] != k:
         raise ValueError(f"{call}: x must be [rows, {k}]")
     group = k // groups if groups else 32
-    if group not in (32, 64, 128) or groups * group != k:
+    if group not in GROUPS or groups * group != k:
         raise ValueError(f"{call}: {k} columns with {groups} scales a row: a scale covers 32, 64 or 128 columns")
-    if (q.shape[-1] > 1 and q.stride(-1) != 1) or (groups > 1 and scales.stride(-1) != 1):
+    q_stride, s_stride = q.stride(), scales.stride()
+    if (q_stride[-1] != 1 and half > 1) or (s_stride[-1] != 1 and groups > 1):
         raise ValueError(f"{call}: q and scales must have unit column stride")
-    return n, k, group, _row_type(scales, "scales")
+    ld_q, ld_s = (q_stride[-2], s_stride[-2]) if n > 1 else (half, groups)
+    return n, k, group, ROW_TYPES[x_type], ROW_TYPES[s_type], ld_q, ld_s
 
 
 def empty_w4(n: int, k: int, group: int, scale_dtype=torch.bfloat16, device="cuda", lead=()):
@@ -54,7 +61,7 @@ def quant_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None
         raise ValueError("quant_w4: q must be [..., n, k / 2] and scales [..., n, k / group]")
     k, groups = x.shape[-1], scales.shape[-1]
     group = k // groups if groups else 32
-    if group not in (32, 64, 128) or groups * group != k:
+    if group not in GROUPS or groups * group != k:
         raise ValueError(f"quant_w4: {k} columns with {groups} scales a row: a scale covers 32, 64 or 128 columns")
     n = x.numel() // k if k else 0
     flat = [t.view(n, t.shape[-1]) if n else t for t in (x, q, scales)]
@@ -69,14 +76,12 @@ def matvec_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, out: torch
     """x [rows, k] times the weights [n, k] transposed -> out [rows, n] of x's type
     (bq_matvec_w4). Any number of rows; made for up to 32."""
     dev = _here("matvec_w4", "x q scales out", x, q, scales, out)
-    n, k, group, s_kind = _weights("matvec_w4", q, scales, x, 2)
+    n, k, group, kind, s_kind, ld_q, ld_s = _weights("matvec_w4", q, scales, x, 2)
     rows = x.shape[0]
     xp, ld_x = _rows(x, rows, k, x.dtype, "x")
     op, ld_out = _rows(out, rows, n, x.dtype, "out")
-    one = n <= 1
-    check("bq_matvec_w4", load().bq_matvec_w4(
-        xp, _row_type(x, "x"), rows, k, ld_x, q.data_ptr(), n, k // 2 if one else q.stride(0), scales.data_ptr(),
-        s_kind, group, k // group if one else scales.stride(0), op, ld_out, _on(stream, dev)))
+    check("bq_matvec_w4", load().bq_matvec_w4(xp, kind, rows, k, ld_x, q.data_ptr(), n, ld_q, scales.data_ptr(),
+                                              s_kind, group, ld_s, op, ld_out, _on(stream, dev)))
 
 
 def matvec_w4_experts(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, offsets: torch.Tensor,
@@ -86,7 +91,7 @@ def matvec_w4_experts(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, of
     ``experts.sort``) place p takes row order[p] // top_k of x, the tokens' rows; without it
     x [slots, k] is already by place."""
     dev = _here("matvec_w4_experts", "x q scales offsets out order", x, q, scales, offsets, out, order)
-    n, k, group, s_kind = _weights("matvec_w4_experts", q, scales, x, 3)
+    n, k, group, kind, s_kind, ld_q, ld_s = _weights("matvec_w4_experts", q, scales, x, 3)
     n_experts = q.shape[0]
     slots, x_rows = out.shape[0], x.shape[0]
     if offsets.numel() != n_experts + 1:
@@ -95,9 +100,8 @@ def matvec_w4_experts(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, of
         raise ValueError("matvec_w4_experts: order must have one value for each row of out")
     xp, ld_x = _rows(x, x_rows, k, x.dtype, "x")
     op, ld_out = _rows(out, slots, n, x.dtype, "out")
-    one = n <= 1
     check("bq_matvec_w4_experts", load().bq_matvec_w4_experts(
-        xp, _row_type(x, "x"), x_rows, k, ld_x, q.data_ptr(), n, k // 2 if one else q.stride(1), q.stride(0),
-        scales.data_ptr(), s_kind, group, k // group if one else scales.stride(1), scales.stride(0),
-        _flat(offsets, torch.int32, "offsets"), n_experts, _flat(order, torch.int32, "order") if order is not None
-        else None, top_k, slots, op, ld_out, _on(stream, dev)))
+        xp, kind, x_rows, k, ld_x, q.data_ptr(), n, ld_q, q.stride(0), scales.data_ptr(), s_kind, group, ld_s,
+        scales.stride(0), _flat(offsets, torch.int32, "offsets"), n_experts,
+        _flat(order, torch.int32, "order") if order is not None else None, top_k, slots, op, ld_out,
+        _on(stream, dev)))

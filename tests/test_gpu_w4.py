@@ -167,6 +167,81 @@ def test_values_far_below_their_rows_largest():
         check(out, x64 @ w.T, terms, k, 64, 8, 2.0 ** -134)
 
 
+def staged_case(name, s_dtype, lead, n, k, group, seed):
+    """Weights large enough for the kernel that keeps rows of x in shared memory, drawn on the
+    GPU, and a function that gives an expert's weights in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    code = torch.randint(-8, 8, (*lead, n, k), generator=g, device="cuda", dtype=torch.int8)
+    q = ((code[..., 0::2] & 15) | ((code[..., 1::2] & 15) << 4)).view(torch.uint8)
+    s = (torch.randn((*lead, n, k // group), generator=g, device="cuda") * 0.02).to(s_dtype)
+
+    def weights(*at):
+        return code[at].double() * s[at].double().repeat_interleave(group, dim=-1)
+    return g, q, s, weights
+
+
+@pytest.mark.parametrize("wide_range", [False, True])
+@pytest.mark.parametrize("name,wide_scales,k,group", [("bf16", False, 4096, 32), ("bf16", True, 4160, 64),
+                                                      ("f16", False, 4352, 128), ("f16", True, 7200, 32)])
+def test_one_row_times_many(name, wide_scales, k, group, wide_range):
+    dtype, p, tiny = TYPES[name]
+    n = 19500
+    g, q, s, weights = staged_case(name, torch.float32 if wide_scales else dtype, (), n, k, group, k)
+    x = torch.randn((1, k), generator=g, device="cuda")
+    if wide_range and name == "bf16":
+        x *= 2.0 ** torch.randint(-45, 0, (1, k), generator=g, device="cuda")
+        x[0, 100] = 2.0 ** 30
+    x = x.to(dtype)
+    out, guard = guarded_out(1, n, dtype)
+    w4.matvec_w4(x, q, s, out)
+    w, x64 = weights(), x.double()
+    want, terms = x64 @ w.T, x64.abs() @ w.abs().T
+    if name == "bf16":  # through FP16: 2^-39 of the largest for each value, in check's unit
+        terms += 2.0 ** -16 / (group + k // group + 16) * x64.abs().max() * w.abs().sum(1)
+    check(out, want.cpu().numpy(), terms.cpu().numpy(), k, group, p, tiny)
+    assert guard.bands_intact()
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("k", [4096, 7168])
+def test_experts_with_one_row_on_average(name, k):
+    # 12 tokens over 24 experts of 1650 rows: the kernel expects one row an expert, and one
+    # expert has nine, more than its shared memory holds at once
+    dtype, p, tiny = TYPES[name]
+    group, n, n_experts = 64, 1650, 24
+    g, q, s, weights = staged_case(name, dtype, (n_experts,), n, k, group, 3)
+    ids = np.array([[3]] * 5 + [[0]] + [[3]] * 4 + [[23], [40]])
+    offsets, order, _ = plan_of(ids, n_experts)
+    x = torch.randn((12, k), generator=g, device="cuda").to(dtype)
+    out, guard = guarded_out(12, n, dtype)
+    w4.matvec_w4_experts(x, q, s, torch.from_numpy(offsets).cuda(), out, order=torch.from_numpy(order).cuda(), top_k=1)
+    want, terms = torch.zeros((12, n), dtype=torch.float64), torch.zeros((12, n), dtype=torch.float64)
+    for e in (0, 3, 23):
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        rows, w = x[torch.from_numpy(order[at]).cuda().long()].double(), weights(e)
+        want[at], terms[at] = (rows @ w.T).cpu(), (rows.abs() @ w.abs().T).cpu()
+        if name == "bf16":
+            few = 2.0 ** -16 / (group + k // group + 16) * rows.abs().max() * w.abs().sum(1)
+            terms[at] += few.cpu()
+    check(out, want.numpy(), terms.numpy(), k, group, p, tiny)
+    assert not out[11].any() and guard.bands_intact()
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+def test_a_row_of_infinities_times_many(name):
+    dtype = TYPES[name][0]
+    g, q, s, weights = staged_case(name, dtype, (), 19500, 4096, 32, 8)
+    x = torch.randn((1, 4096), generator=g, device="cuda").to(dtype)
+    x[0, 7] = float("inf")
+    out = torch.empty((1, 19500), dtype=dtype, device="cuda")
+    w4.matvec_w4(x, q, s, out)
+    w = weights()[:, 7]
+    assert torch.equal(out[0] == float("inf"), w > 0) and torch.equal(out[0] == float("-inf"), w < 0)
+    x[0, 7] = float("nan")
+    w4.matvec_w4(x, q, s, out)
+    assert bool(out.isnan().all())
+
+
 def test_rows_do_not_depend_on_their_company():
     # row 0 alone, with 7 and with 31 others, and repeated calls: the same bits wherever the
     # same kernel runs, and within one launch wherever the row stands
@@ -233,5 +308,7 @@ def test_the_debug_build_declines_no_access(bq_lib):
         for shape in EXPERTS:
             test_matvec_experts(shape, "bf16", True)
             test_matvec_experts(shape, "f16", False)
+        test_one_row_times_many("bf16", True, 4160, 64, False)
+        test_experts_with_one_row_on_average("f16", 7168)
         torch.cuda.synchronize()
         assert codec.take_index_errors() == 0
