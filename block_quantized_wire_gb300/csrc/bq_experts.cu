@@ -272,7 +272,8 @@ cudaError_t launch_sort(const Id *ids, int64_t slots, int n_experts, int32_t *of
     if (parts > 1) {
         auto count = sort_count_kernel<Id>;
         if (cudaError_t e = grid_for((const void *)count, 1, &grid, smem_max, kSortThreads)) return e;
-        if (cudaError_t e = launch_kernel_block(count, parts, kSortThreads, smem_count, st, ids, slots, n_experts, parts, ws))
+        if (cudaError_t e =
+                launch_kernel_block(count, parts, kSortThreads, smem_count, st, ids, slots, n_experts, parts, ws))
             return e;
     }
     return launch_kernel_block(place, parts, kSortThreads, smem, st, ids, slots, n_experts, parts, ws, offsets, order,
@@ -319,14 +320,17 @@ struct Units {
 // ---------------------------------------------------------------- gather
 // out[inverse[t, j]] = x[t]: a warp holds a segment of one token's row in registers and
 // stores it to each of the token's places, so every row of x is read once. Rows past the
-// kept places are zeros.
+// kept places are zeros. Bound by the stores: 16384 rows of 7168 BF16 values to 131072 places
+// (2.1 GB, 8 of 9 parts written) take 349 us, 6.06 TB/s, where the GPU writes at 6.55 TB/s
+// without reading.
 constexpr int kGatherPieces = 4;
 constexpr int kGatherRows = 4;
 
 template <class T, bool kWide>
 __global__ void __launch_bounds__(kThreads)
-gather_kernel(const T *__restrict__ x, int64_t tokens, int64_t hidden, int64_t ld_x, const int32_t *__restrict__ inverse,
-              int top_k, const int32_t *__restrict__ offsets, int n_experts, T *__restrict__ out, int64_t ld_out)
+gather_kernel(const T *__restrict__ x, int64_t tokens, int64_t hidden, int64_t ld_x,
+              const int32_t *__restrict__ inverse, int top_k, const int32_t *__restrict__ offsets, int n_experts,
+              T *__restrict__ out, int64_t ld_out)
 {
     using P = Piece<T>;
     using C = Cut<T, kWide>;
@@ -406,7 +410,9 @@ gather_kernel(const T *__restrict__ x, int64_t tokens, int64_t hidden, int64_t l
 // slots left out (their weights too), one rounding to T. Without weights it is the plain
 // sum, which is the gather's gradient. A warp takes a segment of one token's row. Its lanes
 // fetch the token's places and weights together, one each, and the rows of kCombineRows
-// kept slots are loaded before any is added, so that enough loads are in flight.
+// kept slots are loaded before any is added, so that enough loads are in flight. Bound by the
+// memory: 65536 rows of 7168 BF16 values summed into 16384 take 176 us, 6.7 TB/s (254 us with
+// one row loaded after the other).
 template <bool kWide>
 constexpr int kCombinePieces = kWide ? 2 : 1;  // a piece put together holds twice the registers
 constexpr int kCombineRows = 4;
@@ -493,7 +499,8 @@ combine_kernel(const T *__restrict__ y, int64_t ld_y, const float *__restrict__ 
 // dy[inverse[t, j]] = w[t, j] * dout[t] and dw[t, j] = <dout[t], y[inverse[t, j]]>, in
 // one pass over dout and y. A CTA takes up to kGradSlots slots of one token; its threads
 // walk the row together, each keeping one partial dot product per slot, and the partial
-// products are added up in a fixed tree at the end. dw of a dropped slot is 0.
+// products are added up in a fixed tree at the end. dw of a dropped slot is 0. Bound by the
+// memory: 65536 rows of 4096 BF16 values (1.14 GB) take 176 us, 6.5 TB/s.
 constexpr int kGradSlots = 4;
 constexpr int kGradMaxThreads = 256;
 
@@ -603,7 +610,10 @@ cudaError_t launch_units(void (*kernel)(KArgs...), int64_t units, cudaStream_t s
     return launch_kernel_block(kernel, grid, block, 0, st, args...);
 }
 
-int64_t row_units(int64_t rows, int64_t pieces, int per_segment) { return rows * ((pieces + per_segment - 1) / per_segment); }
+int64_t row_units(int64_t rows, int64_t pieces, int per_segment)
+{
+    return rows * ((pieces + per_segment - 1) / per_segment);
+}
 
 template <class T, bool kWide>
 cudaError_t launch_gather_t(const RowArgs &a, const void *x, int64_t ld_x, const int32_t *offsets, int n_experts,
@@ -668,8 +678,9 @@ cudaError_t launch_combine_grad_t(const RowArgs &a, const void *dout, int64_t ld
 cudaError_t launch_expert_sort(const void *ids, bool ids_are_i64, int64_t slots, int n_experts, int32_t *offsets,
                                int32_t *order, int32_t *inverse, int32_t *ws, cudaStream_t st)
 {
-    return ids_are_i64 ? launch_sort(static_cast<const int64_t *>(ids), slots, n_experts, offsets, order, inverse, ws, st)
-                       : launch_sort(static_cast<const int32_t *>(ids), slots, n_experts, offsets, order, inverse, ws, st);
+    if (ids_are_i64)
+        return launch_sort(static_cast<const int64_t *>(ids), slots, n_experts, offsets, order, inverse, ws, st);
+    return launch_sort(static_cast<const int32_t *>(ids), slots, n_experts, offsets, order, inverse, ws, st);
 }
 
 cudaError_t launch_expert_gather(int type, const RowArgs &a, const void *x, int64_t ld_x, const int32_t *offsets,

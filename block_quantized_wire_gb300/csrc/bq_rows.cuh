@@ -11,7 +11,10 @@ template <>
 struct Value<__nv_bfloat16> {
     static __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
     static __device__ __forceinline__ uint16_t round(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
-    static __device__ __forceinline__ uint32_t round2(float lo, float hi) { return f32x2_to_bf16x2(make_float2(lo, hi)); }
+    static __device__ __forceinline__ uint32_t round2(float lo, float hi)
+    {
+        return f32x2_to_bf16x2(make_float2(lo, hi));
+    }
     using Bits = uint16_t;
 };
 template <>

@@ -3,13 +3,22 @@
 // byte i) and s one scale per `group` columns of a weight row.
 //
 // With few rows the weights are read once and used for little: at M rows 4 M operations
-// per byte, so the bound is the memory's rate up to about 16 rows. What has to be kept
-// off the critical path is turning codes into numbers. One warp instruction per code
-// would already be more than an SM issues at that rate, so the products run on the
-// tensor cores: a code becomes an exact BF16 (FP16) integer in half an instruction, the
-// 16 x 16 tiles of weights are the A operand of mma.m16n8k16, up to 8 rows of x are B,
-// and the binary32 sums of a group are multiplied by its scale outside the mma. Sums are
-// binary32 throughout; the output is rounded once.
+// per byte, so the memory would be the bound up to about 16 rows. What keeps the kernel from
+// it is turning codes into numbers. One warp instruction per code would already be more than
+// an SM issues at that rate, so the products run on the tensor cores: a code becomes an
+// exact BF16 (FP16) integer in less than half an instruction, the 16 x 16 tiles of weights
+// are the A operand of mma.m16n8k16, up to 8 rows of x are B, and the binary32 sums of a
+// group are multiplied by its scale outside the mma. Sums are binary32 throughout; the
+// output is rounded once. (The tcgen05 products take no A operand of 4-bit integers and add
+// all of a tile's groups into one accumulator; here each group needs its own sum.)
+//
+// What it measures: of one token's eight experts of 4096 x 7168 with groups of 32 (132 MB,
+// 19.5 us at the copy rate) the copies alone take 24.5 us, the arithmetic alone 23.7 us, both
+// together 31 us. 2 KB of codes cost a warp 345 to 390 instructions, about half of them on the
+// integer units, which run one warp instruction in two cycles; and a mma m16n8k16 takes eight.
+// Tried without gain: three CTAs an SM at 80 registers, rings of 2 to 4 steps, codes loaded a
+// part ahead, a group's scaling one group late, the mma of one part between the widening of
+// the next, shifts as high products (slower: four cycles each), x shared by a ring of its own.
 #include <climits>
 #include <type_traits>
 
@@ -180,21 +189,42 @@ struct Scales {
         }
     }
 
-    // A whole step's scales in aligned copies, where every row allows it.
-    static __device__ __forceinline__ bool plain(const S *s, int64_t ld, int64_t expert_ld)
+    // A whole step's scales without checks. align is that of pointers and strides, at most 16
+    // bytes, 0 where words do not line up: a step is plain where it allows the largest copies.
+    // (Choosing the copies by it in every step cost 3 %.) A single 16-bit scale comes with the
+    // one it shares a word with, which must exist: rows of an even number of scales.
+    static constexpr int kAlign = kBytes < 4 ? 4 : kBytes < 16 ? kBytes : 16;
+    static __device__ __forceinline__ int align_of(const S *s, int64_t groups, int64_t ld, int64_t expert_ld)
     {
-        constexpr int kAlign = kBytes < 16 ? kBytes : 16;
-        return kBytes >= 4 &&
-               ((reinterpret_cast<uintptr_t>(s) | (ld * kSize) | (expert_ld * kSize)) & (kAlign - 1)) == 0;
+        const uint64_t strides = (uint64_t)(ld * kSize) | (uint64_t)(expert_ld * kSize);
+        const uint64_t bits = reinterpret_cast<uintptr_t>(s) | strides | 16;
+        const int align = (int)(bits & (0 - bits));
+        return align < 4 || (kBytes < 4 && groups % 2 != 0) ? 0 : align;
+    }
+    template <int kCopy>
+    static __device__ __forceinline__ void copies(uint32_t dst, const S *p)
+    {
+#pragma unroll
+        for (int i = 0; i < kBytes / kCopy; i++) {
+            if constexpr (kCopy == 16)
+                lane_copy16(dst + 16 * i, reinterpret_cast<const char *>(p) + 16 * i);
+            else
+                lane_copy_part<kCopy>(dst + kCopy * i, reinterpret_cast<const char *>(p) + kCopy * i, kCopy);
+        }
     }
     static __device__ __forceinline__ void fetch_plain(uint32_t dst, const S *p)
     {
-        if constexpr (kBytes >= 16) {
-#pragma unroll
-            for (int i = 0; i < kBytes / 16; i++) lane_copy16(dst + 16 * i, reinterpret_cast<const char *>(p) + 16 * i);
-        } else if constexpr (kBytes >= 4) {
-            lane_copy_part<kBytes>(dst, p, kBytes);
-        }
+        if constexpr (kBytes < 4)
+            lane_copy_part<4>(dst, reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3), 4);
+        else
+            copies<kAlign>(dst, p);
+    }
+    static __device__ __forceinline__ void fetch_words(uint32_t dst, const S *p, int align)
+    {
+        if (kBytes >= 8 && align == 8)
+            copies<(kBytes < 8 ? 4 : 8)>(dst, p);
+        else
+            copies<4>(dst, p);
     }
 
     // a row's scales as copied, shifted into place where skewed
@@ -397,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
     const int64_t ld_rows = kLaneRows * a.ld_q;
     const uint32_t dst_code = code_at<kRowTiles>(f_row, f_col), dst_scale = kStepCodeBytes + lane * kScaleSlot;
     const int my_steps = steps > warp ? (steps - warp - 1) / kW4Warps + 1 : 0;
-    const int my_plain = Sc::plain(scales, a.ld_s, a.expert_s) && whole_steps > warp
+    const int align_s = Sc::align_of(scales, a.k / kGroup, a.ld_s, a.expert_s);
+    const int my_plain = align_s >= Sc::kAlign && whole_steps > warp
                              ? (whole_steps - warp - 1) / kW4Warps + 1 : 0;
     auto chunk_passes = [&](int rest) { return ((rest < chunk_cap ? rest : chunk_cap) + pass_cap - 1) / pass_cap; };
     auto open_chunk = [&]() {  // the run's first block again
@@ -463,8 +494,12 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
             }
             const int left = (int)(a.k / kGroup) - f_step * kScaleCount;
             const bool in = lane < f_rows;
-            if (kItemRows == 32 || lane < kItemRows)
-                Sc::fetch(f_slot + dst_scale, in ? f_s : scales, in ? (left < kScaleCount ? left : kScaleCount) : 0);
+            if (kItemRows == 32 || lane < kItemRows) {
+                if (align_s > 0 && in && left >= kScaleCount && Sc::kBytes >= 4)
+                    Sc::fetch_words(f_slot + dst_scale, f_s, align_s);
+                else
+                    Sc::fetch(f_slot + dst_scale, in ? f_s : scales, !in ? 0 : left < kScaleCount ? left : kScaleCount);
+            }
             f_step += kW4Warps;
             f_q += kW4Warps * kStepBytes;
             f_s += kW4Warps * kScaleCount;
@@ -482,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
     // Staged x: rows p0.. of one expert as FP16, each times a power of two that brings its
     // largest value below 2^15 (FP16 rows as they are), in the pairs that the codes come in.
     // BF16 values down to 2^-31 of the row's largest stay exact; smaller ones are rounded to
-    // multiples of at most 2^-38 of it, far below what a binary32 sum with it would keep. A single row is shared out over the CTA, more are
-    // taken by a warp each.
+    // multiples of at most 2^-38 of it, far below what a binary32 sum with it would keep. A
+    // single row is shared out over the CTA, more are taken by a warp each.
     auto stage_x = [&](const ExpertRows &er, int p0, int rows) {
         const int padded = steps * kStepCols;
         const bool split = rows == 1;
@@ -739,7 +774,7 @@ cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
 {
     // Staging pays where one row goes over many long weight rows, so that few CTAs stage it
     // and each uses it for long: one token's eight experts of 4096 x 7168 took 30.4 us staged
-    // and W4E1 us directly, ten tokens' experts of 3358 x 2944 21.6 us staged and 17.0 us
+    // and 36.1 us directly, ten tokens' experts of 3358 x 2944 21.6 us staged and 17.0 us
     // directly, one row times 2932 x 7808 8.4 and 7.3 us.
     const int64_t used = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
     const int64_t cap = kStagedBytes / staged_row_bytes(a.k);
@@ -747,9 +782,21 @@ cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
         a.staged_rows = (int)(!kExperts ? 1 : cap < 4 ? cap : cap / 4 * 4);
         return launch_w4<W4Shape<T, S, kGroup, 4, 1, true, kExperts>>(a, st);
     }
-    return rows <= 4   ? launch_w4<W4Shape<T, S, kGroup, 4, 2, false, kExperts>>(a, st)
-           : rows <= 8 ? launch_w4<W4Shape<T, S, kGroup, 8, 2, false, kExperts>>(a, st)
-                       : launch_w4<W4Shape<T, S, kGroup, 16, 2, false, kExperts>>(a, st);
+    // One 16-row tile a warp makes twice the items of half the steps, each step a little dearer:
+    // taken where rounds of the two CTAs an SM, times the steps of a warp and one for the
+    // item's end, come out fewer.
+    int sms = 1;
+    if (cudaError_t e = sm_count(&sms)) return e;
+    const int64_t rounds1 = (used * ((a.n + 15) / 16) - 1) / (2 * sms) + 1, steps1 = (a.k + 2047) / 2048;
+    const int64_t rounds2 = (used * ((a.n + 31) / 32) - 1) / (2 * sms) + 1, steps2 = (a.k + 1023) / 1024;
+    const bool one = 11 * rounds1 * (steps1 + 1) < 10 * rounds2 * (steps2 + 1);
+    if (rows <= 4)
+        return one ? launch_w4<W4Shape<T, S, kGroup, 4, 1, false, kExperts>>(a, st)
+                   : launch_w4<W4Shape<T, S, kGroup, 4, 2, false, kExperts>>(a, st);
+    if (rows <= 8)
+        return one ? launch_w4<W4Shape<T, S, kGroup, 8, 1, false, kExperts>>(a, st)
+                   : launch_w4<W4Shape<T, S, kGroup, 8, 2, false, kExperts>>(a, st);
+    return launch_w4<W4Shape<T, S, kGroup, 16, 2, false, kExperts>>(a, st);
 }
 
 template <class T, class S, bool kExperts>
@@ -834,7 +881,8 @@ cudaError_t launch_quant(const void *x, int64_t n, int64_t k, int64_t ld_x, uint
     auto kernel = quant_w4_kernel<T, S, kGroup>;
     int grid = 0;
     if (cudaError_t e = grid_for((const void *)kernel, (n * (k / 8) + 31) / 32, &grid)) return e;
-    return launch_kernel(kernel, grid, st, static_cast<const T *>(x), n, k, ld_x, q, ld_q, static_cast<S *>(scales), ld_s);
+    return launch_kernel(kernel, grid, st, static_cast<const T *>(x), n, k, ld_x, q, ld_q, static_cast<S *>(scales),
+                         ld_s);
 }
 
 template <class T, class S, typename... Args>
@@ -857,9 +905,11 @@ cudaError_t launch_quant_scale(int scale_type, Args... args)
 cudaError_t launch_quant_w4(int type, int scale_type, int group, const void *x, int64_t n, int64_t k, int64_t ld_x,
                             uint8_t *q, int64_t ld_q, void *scales, int64_t ld_s, cudaStream_t st)
 {
-    return type == kBf16  ? launch_quant_scale<__nv_bfloat16>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st)
-           : type == kF16 ? launch_quant_scale<__half>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st)
-                          : launch_quant_scale<float>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st);
+    switch (type) {
+    case kBf16: return launch_quant_scale<__nv_bfloat16>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st);
+    case kF16: return launch_quant_scale<__half>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st);
+    default: return launch_quant_scale<float>(scale_type, group, x, n, k, ld_x, q, ld_q, scales, ld_s, st);
+    }
 }
 
 cudaError_t launch_matvec_w4(int x_type, int scale_type, int group, const W4Args &a, cudaStream_t st)
