@@ -103,15 +103,21 @@ cudaError_t grid_for(const void *kernel, int64_t nchunk, int *grid, size_t smem,
                 occ = g_occ[i].ctas_per_sm;
     }
     if (occ == 0) {
-        if (smem > 48 * 1024) {
+        // The kernel's shared memory limit is that of its largest entry: a call with less must
+        // not lower it for those that found theirs before. A full table starts anew.
+        std::lock_guard<std::mutex> lock(g_occ_mu);
+        if (g_occ_n == kMaxKernels) g_occ_n = 0;
+        size_t limit = 48 * 1024;
+        for (int i = 0; i < g_occ_n; i++)
+            if (g_occ[i].kernel == kernel && g_occ[i].device == dev && g_occ[i].smem > limit) limit = g_occ[i].smem;
+        if (smem > limit) {
             if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      static_cast<int>(smem)))
                 return e;
         }
         if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, block, smem)) return e;
         if (occ < 1) occ = 1;
-        std::lock_guard<std::mutex> lock(g_occ_mu);
-        if (g_occ_n < kMaxKernels) g_occ[g_occ_n++] = OccEntry{kernel, smem, block, dev, occ};
+        g_occ[g_occ_n++] = OccEntry{kernel, smem, block, dev, occ};
     }
     const int64_t warps_per_cta = block / 32;
     const int64_t need = (nchunk + warps_per_cta - 1) / warps_per_cta;

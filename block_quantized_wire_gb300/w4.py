@@ -74,7 +74,7 @@ def quant_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None
 
 def matvec_w4(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, out: torch.Tensor, stream=None) -> None:
     """x [rows, k] times the weights [n, k] transposed -> out [rows, n] of x's type
-    (bq_matvec_w4). Any number of rows; made for up to 32."""
+    (bq_matvec_w4). Any number of rows; made for up to 16, and 16 at a time."""
     dev = _here("matvec_w4", "x q scales out", x, q, scales, out)
     n, k, group, kind, s_kind, ld_q, ld_s = _weights("matvec_w4", q, scales, x, 2)
     rows = x.shape[0]

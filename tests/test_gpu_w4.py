@@ -260,6 +260,21 @@ def test_rows_do_not_depend_on_their_company():
     assert torch.equal(outs[0][0], outs[0][5]) and torch.equal(one[0], outs[0][0])
 
 
+def test_calls_with_more_and_less_shared_memory_in_turn():
+    # the kernel's shared memory grows with the number of experts: a call with few experts must
+    # not take the limit away from the one with many
+    rng = np.random.default_rng(31)
+    for n_experts in (900, 3, 900, 40, 900, 3):
+        q = torch.full((n_experts, 32, 64), 0x11, dtype=torch.uint8, device="cuda")
+        s = torch.ones((n_experts, 32, 2), dtype=torch.bfloat16, device="cuda")
+        x = torch.from_numpy(rng.integers(0, 2, (1, 128)).astype(np.float32)).to(torch.bfloat16).cuda()
+        offsets = torch.ones(n_experts + 1, dtype=torch.int32, device="cuda")
+        offsets[0] = 0
+        out = torch.empty((1, 32), dtype=torch.bfloat16, device="cuda")
+        w4.matvec_w4_experts(x, q, s, offsets, out)
+        assert bool((out == x.sum()).all())
+
+
 def test_no_rows_no_columns_and_an_empty_sum():
     e = torch.empty
     q, s = e((8, 64), dtype=torch.uint8, device="cuda"), torch.ones((8, 1), dtype=torch.bfloat16, device="cuda")
