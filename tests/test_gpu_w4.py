@@ -227,6 +227,44 @@ def test_experts_with_one_row_on_average(name, k):
     assert not out[11].any() and guard.bands_intact()
 
 
+@pytest.mark.parametrize("rows", [1, 4, 6])
+@pytest.mark.parametrize("name,wide_scales,k,group", [("bf16", False, 4160, 64), ("bf16", True, 4192, 32),
+                                                      ("f16", False, 4224, 128), ("f16", True, 4160, 64)])
+def test_many_items_of_several_steps(name, wide_scales, k, group, rows):
+    # so many weight rows that a warp takes two row tiles, and several steps of each item; an odd
+    # number of scales a row, and columns that end inside a step
+    dtype, p, tiny = TYPES[name]
+    n = 7210
+    g, q, s, weights = staged_case(name, torch.float32 if wide_scales else dtype, (), n, k, group, k + rows)
+    x = torch.randn((rows, k), generator=g, device="cuda").to(dtype)
+    out, guard = guarded_out(rows, n, dtype)
+    w4.matvec_w4(x, q, s, out)
+    w, x64 = weights(), x.double()
+    check(out, (x64 @ w.T).cpu().numpy(), (x64.abs() @ w.abs().T).cpu().numpy(), k, group, p, tiny)
+    assert guard.bands_intact()
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+def test_experts_with_many_items_of_several_steps(name):
+    dtype, p, tiny = TYPES[name]
+    group, n, k, n_experts = 64, 2410, 4160, 8
+    g, q, s, weights = staged_case(name, dtype, (n_experts,), n, k, group, 5)
+    rng = np.random.default_rng(5)
+    ids = ids_of(rng, 16, 2, n_experts, skew=True)
+    offsets, order, _ = plan_of(ids, n_experts)
+    x = torch.randn((16, k), generator=g, device="cuda").to(dtype)
+    out, guard = guarded_out(32, n, dtype)
+    w4.matvec_w4_experts(x, q, s, torch.from_numpy(offsets).cuda(), out, order=torch.from_numpy(order).cuda(), top_k=2)
+    want, terms = torch.zeros((32, n), dtype=torch.float64), torch.zeros((32, n), dtype=torch.float64)
+    for e in range(n_experts):
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        if at.start < at.stop:
+            rows, w = x[torch.from_numpy(order[at] // 2).cuda().long()].double(), weights(e)
+            want[at], terms[at] = (rows @ w.T).cpu(), (rows.abs() @ w.abs().T).cpu()
+    check(out, want.numpy(), terms.numpy(), k, group, p, tiny)
+    assert not out[int(offsets[-1]):].any() and guard.bands_intact()
+
+
 @pytest.mark.parametrize("name", list(TYPES))
 def test_a_row_of_infinities_times_many(name):
     dtype = TYPES[name][0]
@@ -325,5 +363,8 @@ def test_the_debug_build_declines_no_access(bq_lib):
             test_matvec_experts(shape, "f16", False)
         test_one_row_times_many("bf16", True, 4160, 64, False)
         test_experts_with_one_row_on_average("f16", 7168)
+        test_many_items_of_several_steps("bf16", False, 4160, 64, 6)
+        test_many_items_of_several_steps("f16", True, 4160, 64, 4)
+        test_experts_with_many_items_of_several_steps("bf16")
         torch.cuda.synchronize()
         assert codec.take_index_errors() == 0
