@@ -90,14 +90,18 @@ struct Cut {
 
     static __host__ __device__ __forceinline__ int64_t pieces(int64_t hidden)
     {
+        if (hidden == 0) return 0;  // a row without columns has no words, wherever it starts
         return kWide ? hidden / N : (hidden + 2 * N - 2) / N;
     }
     // first column of piece i of the row written at `row`; it may be negative
-    static __device__ __forceinline__ int64_t column(const T *row, int64_t i)
+    static __host__ __device__ __forceinline__ int64_t column(const T *row, int64_t i)
     {
         return kWide ? N * i : N * i - (int64_t)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     }
-    static __device__ __forceinline__ bool inside(int64_t c, int64_t hidden) { return c < hidden && (kWide || c > -N); }
+    static __host__ __device__ __forceinline__ bool inside(int64_t c, int64_t hidden)
+    {
+        return c < hidden && (kWide || c > -N);
+    }
 
     // Columns [c, c + N) of a row of the buffer [lo, hi), in two steps: fetch() starts the
     // loads, of several pieces one after the other, and take() puts the piece together. Where
@@ -106,10 +110,11 @@ struct Cut {
     struct Raw {
         uint4 x, y;
     };
-    static __device__ __forceinline__ bool windowed(const T *p, const void *lo, const void *hi)
+    static __host__ __device__ __forceinline__ bool windowed(const T *p, const void *lo, const void *hi)
     {
         const uintptr_t a = reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15;
-        return a >= reinterpret_cast<uintptr_t>(lo) && a + 32 <= reinterpret_cast<uintptr_t>(hi);
+        const uintptr_t end = reinterpret_cast<uintptr_t>(hi);
+        return a >= reinterpret_cast<uintptr_t>(lo) && end >= 32 && a <= end - 32;  // a + 32 could wrap
     }
     static __device__ __forceinline__ void fetch(Raw &raw, const T *row, int64_t c, const void *lo, const void *hi)
     {

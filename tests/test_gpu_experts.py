@@ -383,3 +383,21 @@ def test_the_debug_build_declines_no_access(bq_lib):
                 test_combine_grad_against_the_formula(name, shape)
         torch.cuda.synchronize()
         assert codec.take_index_errors() == 0
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("tokens,top_k,spare", [(17, 4, 0), (64, 8, 0), (64, 3, 5), (2000, 8, 0)])
+def test_combine_grad_of_many_slots_without_columns(name, tokens, top_k, spare):
+    # no columns: dweights are zeros, and nothing is read or written through the rows, whose
+    # tensors have null pointers (or, with spare columns beside them, rows `spare` values apart)
+    dtype = TYPES[name][0]
+    ids = ids_of(np.random.default_rng(tokens), tokens, top_k, 5)
+    offsets, order, inverse = device_plan(ids, 5)
+    dout = torch.ones((tokens, spare), dtype=dtype, device="cuda")[:, :0]
+    y = torch.ones((tokens * top_k, spare), dtype=dtype, device="cuda")[:, :0]
+    around = torch.full((tokens * top_k, spare), 3.0, dtype=dtype, device="cuda")
+    gw = Guarded(4 * tokens * top_k)
+    dw = gw.view(torch.float32, (tokens, top_k))
+    experts.combine_grad(dout, y, torch.full((tokens, top_k), float("nan"), device="cuda"), inverse, offsets,
+                         around[:, :0], dw)
+    assert not dw.any() and gw.bands_intact() and bool((around == 3.0).all())
