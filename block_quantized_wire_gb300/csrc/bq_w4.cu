@@ -777,7 +777,7 @@ cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
     // and 36.1 us directly, ten tokens' experts of 3358 x 2944 21.6 us staged and 17.0 us
     // directly, one row times 2932 x 7808 8.4 and 7.3 us.
     const int64_t used = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
-    const int64_t cap = kStagedBytes / staged_row_bytes(a.k);
+    const int64_t cap = a.k > 0 ? kStagedBytes / staged_row_bytes(a.k) : 0;
     if (rows == 1 && a.k >= 4096 && cap >= 1 && used * (a.n / 16) >= kStagedItems) {
         a.staged_rows = (int)(!kExperts ? 1 : cap < 4 ? cap : cap / 4 * 4);
         return launch_w4<W4Shape<T, S, kGroup, 4, 1, true, kExperts>>(a, st);

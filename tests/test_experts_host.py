@@ -1,9 +1,13 @@
 """The expert-layer calls without a GPU: the C ABI's refusals (before any CUDA call; the
 fake pointers are never dereferenced) and the binding's checks of tensors."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
-from block_quantized_wire_gb300 import experts, w4
+from block_quantized_wire_gb300 import build, experts, w4
 
 OK, NULL, SHAPE, ALIGN, ALIAS = range(5)
 A = 0x7F0000000000  # a 256-byte-aligned fake device address
@@ -198,3 +202,19 @@ def test_the_binding_checks_weights(on_device):
         w4.matvec_w4_experts(x, qe, se, offsets[:5], out)
     with pytest.raises(ValueError, match="order must have"):
         w4.matvec_w4_experts(x, qe, se, offsets, out, order=z(2, dtype=torch.int32))
+
+
+def test_a_product_over_no_columns_reaches_the_launch(bq_lib):
+    # in a process of its own that sees no GPU: the call passes every check and fails at the launch
+    calls = """
+import sys
+from block_quantized_wire_gb300 import _lib
+lib, A, M = _lib.load(), 0x7F0000000000, 0x1000000
+for rows in (1, 3, 40):
+    assert lib.bq_matvec_w4(None, 0, rows, 0, 0, None, 24000, 0, None, 0, 32, 0, A, 24000, None) == 5
+    assert lib.bq_matvec_w4_experts(None, 0, rows, 0, 0, None, 24000, 0, 0, None, 0, 32, 0, 0, A + M, 8, None, 1, rows,
+                                    A + 2 * M, 24000, None) == 5
+"""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, "-c", calls], capture_output=True, text=True, env=env, cwd=build.ROOT)
+    assert r.returncode == 0, (r.returncode, r.stderr)
