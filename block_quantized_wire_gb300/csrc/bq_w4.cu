@@ -8,19 +8,18 @@
 // an SM issues at that rate, so the products run on the tensor cores: a code becomes an
 // exact BF16 (FP16) integer in less than half an instruction, the 16 x 16 tiles of weights
 // are the A operand of mma.m16n8k16, up to 8 rows of x are B, and the binary32 sums of a
-// group are multiplied by its scale outside the mma. Sums are binary32 throughout; the
-// output is rounded once. (The tcgen05 products take no A operand of 4-bit integers and add
+// group are multiplied by its scale outside the mma. Sums are binary32 throughout (the mma
+// may truncate where a binary32 addition would round); the output is rounded once. (The tcgen05 products take no A operand of 4-bit integers and add
 // all of a tile's groups into one accumulator; here each group needs its own sum.)
 //
 // What it measures: of one token's eight experts of 4096 x 7168 with groups of 32 (132 MB,
 // 19.5 us at the copy rate) the copies alone take 24.5 us, the arithmetic alone 23.7 us, both
-// together 31 us. 2 KB of codes cost a warp 345 to 390 instructions, about half of them on the
+// together 32 us. 2 KB of codes cost a warp 345 to 390 instructions, about half of them on the
 // integer units, which run one warp instruction in two cycles; and a mma m16n8k16 takes eight.
 // Tried without gain: three CTAs an SM at 80 registers, rings of 2 to 4 steps, codes loaded a
 // part ahead, a group's scaling one group late, the mma of one part between the widening of
 // the next, shifts as high products (slower: four cycles each), x shared by a ring of its own.
 #include <climits>
-#include <type_traits>
 
 #include "bq_rows.cuh"
 
@@ -278,7 +277,6 @@ struct ExpertRows {
 // Shared memory for staged rows of x, what two CTAs an SM leave beside their rings; a row is
 // padded to whole steps.
 constexpr int64_t kStagedBytes = 44 * 1024;
-constexpr int kMaxStagedRows = kStagedBytes / 512;
 constexpr int64_t kStagedItems = 1216;  // 16-row items that make staging pay: four for each of 304 CTAs
 inline int64_t staged_row_bytes(int64_t k) { return (k + 255) / 256 * 512; }
 
@@ -311,15 +309,12 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
     constexpr int kStepCols = Shape::kStepCols, kStepBytes = kStepCols / 2, kParts = kStepCols / 32;
     constexpr int kScaleCount = kStepCols / kGroup, kScaleSlot = Shape::kScaleSlot, kPerScale = kGroup / 32;
     constexpr bool kStaged = Shape::kStaged, kExperts = Shape::kExperts, kEven = Shape::kEven;
-    using Product = typename std::conditional<kStaged, __half, T>::type;  // the mma's operands
     using Sc = Scales<S, kScaleCount>;
     extern __shared__ __align__(128) unsigned char smem[];
     ExpertRows *const active = reinterpret_cast<ExpertRows *>(smem + Shape::kRingBytes + Shape::kSumBytes);
     unsigned char *const x_smem = smem + Shape::kRingBytes + Shape::kSumBytes +
                                   ((sizeof(ExpertRows) * a.n_experts + 15) & ~(size_t)15);
     __shared__ int warp_active[kW4Warps], warp_passes[kW4Warps];
-    __shared__ float x_unscale[kStaged ? kMaxStagedRows : 1];
-    __shared__ uint32_t x_top[kW4Warps];
 
     pdl_begin();
     dbg_begin();
@@ -514,12 +509,9 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; i++) fetch();
 
-    // Staged x: rows p0.. of one expert as FP16, each times a power of two that brings its
-    // largest value below 2^15 (FP16 rows as they are), in the pairs that the codes come in.
-    // BF16 values down to 2^-31 of the row's largest stay exact; smaller ones are rounded to
-    // multiples of at most 2^-38 of it, far below what a binary32 sum with it would keep. A
-    // single row is shared out over the CTA, more are taken by a warp each.
-    auto stage_x = [&](const ExpertRows &er, int p0, int rows) {
+    // Staged x: rows p0.. of one expert, in the pairs that the codes come in, zeros up to a
+    // whole step. A single row is shared out over the CTA, more are taken by a warp each.
+    auto stage_x = [&](int p0, int rows) {
         const int padded = steps * kStepCols;
         const bool split = rows == 1;
         const int first = 8 * (split ? (int)threadIdx.x : lane), stride = 8 * (split ? kThreads : 32);
@@ -528,46 +520,11 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
             if (kExperts && a.order) row = dbg_ok(a.order + row, 4, false) ? __ldg(a.order + row) / a.top_k : 0;
             if (row < 0 || row >= a.x_rows) row = 0;  // a wrong plan
             const T *src = static_cast<const T *>(a.x) + row * a.ld_x;
-            float up = 1.0f, down = 1.0f;
-            if constexpr (!std::is_same<T, __half>::value) {
-                uint32_t top = 0;  // largest magnitudes' bits, of even and of odd values
-#pragma unroll 4
-                for (int c = first; c < a.k; c += stride) {
-                    const uint4 v = ld_keep_v4(src + c);
-                    top = __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu),
-                                   __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-                }
-                top = __reduce_max_sync(kFull, max(top >> 16, top & 0xffffu));
-                if (split) {
-                    if (lane == 0) x_top[warp] = top;
-                    __syncthreads();
-#pragma unroll
-                    for (int w = 0; w < kW4Warps; w++) top = max(top, x_top[w]);
-                }
-                const int e = max((int)(top >> 7), 15);  // biased exponent of the largest value
-                up = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
-                down = __uint_as_float((uint32_t)(e - 14) << 23);
-            }
-            if (first == 0) x_unscale[r] = down;
 #pragma unroll 4
             for (int c = first; c < padded; c += stride) {
-                uint32_t h[4] = {0, 0, 0, 0};
-                if (c < a.k) {
-                    const uint4 v = ld_keep_v4(src + c);
-                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        if constexpr (std::is_same<T, __half>::value) {
-                            h[i] = u[i];
-                        } else {
-                            const __half2 p = __floats2half2_rn(__fmul_rn(__uint_as_float(u[i] << 16), up),
-                                                                __fmul_rn(__uint_as_float(u[i] & 0xffff0000u), up));
-                            h[i] = *reinterpret_cast<const uint32_t *>(&p);
-                        }
-                    }
-                }
-                const uint4 paired = make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
-                                                __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632));
+                const uint4 v = c < a.k ? ld_keep_v4(src + c) : make_uint4(0, 0, 0, 0);
+                const uint4 paired = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 *reinterpret_cast<uint4 *>(x_smem + (((c >> 5) * chunk_cap + r) * 4 + ((c >> 3) & 3)) * 16) = paired;
             }
         }
@@ -586,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
             next_chunk = er.hi - chunk > chunk_cap ? chunk + chunk_cap : er.hi;
             if constexpr (kStaged) {
                 __syncthreads();  // the readers of the rows before
-                stage_x(er, chunk, next_chunk - chunk);
+                stage_x(chunk, next_chunk - chunk);
             }
             for (int block = first_block; block < end_block; block++) {
                 const int r0 = block * kItemRows;
@@ -661,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
                             for (int r = 0; r < kRowTiles; r++) {
                                 constexpr int kEightRows = 8 * kStepBytes;
                                 uint32_t lo[4], hi[4];
-                                Codes<Product>::widen(lds_u32((src ^ (16 * j)) + 2 * kEightRows * r), lo);
-                                Codes<Product>::widen(lds_u32((src ^ (16 * j)) + 2 * kEightRows * r + kEightRows), hi);
+                                Codes<T>::widen(lds_u32((src ^ (16 * j)) + 2 * kEightRows * r), lo);
+                                Codes<T>::widen(lds_u32((src ^ (16 * j)) + 2 * kEightRows * r + kEightRows), hi);
 #pragma unroll
                                 for (int i = 0; i < 4; i++) {
                                     codes[r][2 * i] = lo[i];
@@ -687,14 +644,14 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
 #pragma unroll
                                 for (int r = 0; r < kRowTiles; r++)
                                     if (j % kPerScale == 0)
-                                        Codes<Product>::template mma<true>(c[r][m], codes[r], b[m][0], b[m][1]);
+                                        Codes<T>::template mma<true>(c[r][m], codes[r], b[m][0], b[m][1]);
                                     else
-                                        Codes<Product>::template mma<false>(c[r][m], codes[r], b[m][0], b[m][1]);
+                                        Codes<T>::template mma<false>(c[r][m], codes[r], b[m][0], b[m][1]);
 #pragma unroll
                             for (int m = 0; m < kTiles; m++)
 #pragma unroll
                                 for (int r = 0; r < kRowTiles; r++)
-                                    Codes<Product>::template mma<false>(c[r][m], codes[r] + 4, b[m][2], b[m][3]);
+                                    Codes<T>::template mma<false>(c[r][m], codes[r] + 4, b[m][2], b[m][3]);
                             if (j % kPerScale == kPerScale - 1) {
 #pragma unroll
                                 for (int r = 0; r < kRowTiles; r++) {
@@ -733,8 +690,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
                         float v = of[0];
 #pragma unroll
                         for (int w = 1; w < kW4Warps; w++) v = __fadd_rn(v, of[w * kPassRows * kSumStride]);
-                        if (kStaged) v = __fmul_rn(v, x_unscale[in_chunk + m]);
-                        if (Codes<Product>::kUp != 1.0f) v = __fmul_rn(v, Codes<Product>::kUp);
+                        if (Codes<T>::kUp != 1.0f) v = __fmul_rn(v, Codes<T>::kUp);
                         T *dst = static_cast<T *>(a.out) + (p0 + m) * a.ld_out + r0 + r;
                         if (dbg_ok(dst, sizeof(T), true)) *reinterpret_cast<Bits *>(dst) = Value<T>::round(v);
                     }
@@ -773,9 +729,9 @@ template <class T, class S, int kGroup, bool kExperts>
 cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
 {
     // Staging pays where one row goes over many long weight rows, so that few CTAs stage it
-    // and each uses it for long: one token's eight experts of 4096 x 7168 took 30.4 us staged
-    // and 36.1 us directly, ten tokens' experts of 3358 x 2944 21.6 us staged and 17.0 us
-    // directly, one row times 2932 x 7808 8.4 and 7.3 us.
+    // and each uses it for long: one token's eight experts of 4096 x 7168 take 32.1 us staged
+    // and 36.3 us directly, one row times 32000 x 8192 33.5 and 39.9 us; one token's eight experts
+    // of 2432 x 4096 14.9 and 14.6 us.
     const int64_t used = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
     const int64_t cap = a.k > 0 ? kStagedBytes / staged_row_bytes(a.k) : 0;
     if (rows == 1 && a.k >= 4096 && cap >= 1 && used * (a.n / 16) >= kStagedItems) {

@@ -375,12 +375,12 @@ BQ_API bq_status bq_quant_w4(const void *x, int type, int64_t n, int64_t k, int6
  *   scales  [n][ld_s] of scale_type (read): the type of x, or FP32; 4-byte aligned
  *   group   32, 64 or 128 columns per scale; k % group == 0
  *   out     [rows][ld_out] of x's type (written)
- * A group's sum of x * code is exact products added in binary32; it is multiplied by the
- * scale and added to the output's sum in binary32. BF16 rows may pass through FP16, each
- * times a power of two: values below 2^-31 of their row's largest then count as the nearest
- * multiple of 2^-38 of it (at most). Any number of rows is right; the kernels are made for
- * up to 16, and read the weights once for every 16 rows. A wrong group, type or k returns
- * BQ_ERR_SHAPE; n and k are at most BQ_MAX_W4_DIM. */
+ * The products x * code are exact; a group's are added in binary32 by the tensor cores, which
+ * may truncate where a binary32 addition would round. The sum is multiplied by the scale and
+ * added to the output's sum in binary32, and does not overflow where that product does not.
+ * Any number of rows is right; the kernels are made for up to 16, and read the weights once
+ * for every 16 rows. A wrong group, type or k returns BQ_ERR_SHAPE; n and k are at most
+ * BQ_MAX_W4_DIM. */
 BQ_API bq_status bq_matvec_w4(const void *x, int type, int64_t rows, int64_t k, int64_t ld_x, const uint8_t *q,
                               int64_t n, int64_t ld_q, const void *scales, int scale_type, int group, int64_t ld_s,
                               void *out, int64_t ld_out, cudaStream_t stream);

@@ -368,3 +368,72 @@ def test_the_debug_build_declines_no_access(bq_lib):
         test_experts_with_many_items_of_several_steps("bf16")
         torch.cuda.synchronize()
         assert codec.take_index_errors() == 0
+
+
+# Rows kept in shared memory (one row on average, many long weight rows). Their values and
+# sums have the range and precision of rows read directly: products are exact, so check's own
+# bound holds without an allowance.
+STAGED = [("bf16", False, 4096, 32), ("bf16", True, 4160, 64), ("bf16", False, 7168, 128), ("f16", True, 4096, 32)]
+
+
+@pytest.mark.parametrize("name,wide_scales,k,group", STAGED)
+def test_one_row_whose_largest_value_takes_no_part(name, wide_scales, k, group):
+    dtype, p, tiny = TYPES[name]
+    n = 19500
+    g, q, s, weights = staged_case(name, torch.float32 if wide_scales else dtype, (), n, k, group, k + 1)
+    q[:, 50] &= 0xF0  # column 100's codes
+    w = weights()
+    w[:, 100] = 0.0
+    x = torch.randn((1, k), generator=g, device="cuda") * 2.0 ** torch.randint(-12, 0, (1, k), generator=g, device="cuda")
+    x[0, 100] = 2.0 ** 14
+    x = x.to(dtype)
+    if name == "bf16":
+        x *= 2.0 ** -40
+        x[0, 100] = 2.0 ** 30
+    out, guard = guarded_out(1, n, dtype)
+    w4.matvec_w4(x, q, s, out)
+    x64 = x.double()
+    check(out, (x64 @ w.T).cpu().numpy(), (x64.abs() @ w.abs().T).cpu().numpy(), k, group, p, tiny)
+    assert guard.bands_intact()
+
+
+@pytest.mark.parametrize("group", [32, 128])
+def test_an_experts_row_whose_largest_value_takes_no_part(group):
+    dtype, p, tiny = TYPES["bf16"]
+    n, k, n_experts = 3000, 4096, 24
+    g, q, s, weights = staged_case("bf16", dtype, (n_experts,), n, k, group, 13)
+    s[..., 100 // group] = 0.0  # the scales of the largest value's group
+    ids = np.array([[3], [0], [3], [23], [3], [3], [3]])
+    offsets, order, _ = plan_of(ids, n_experts)
+    x = torch.randn((7, k), generator=g, device="cuda").to(dtype) * 2.0 ** -45
+    x[:, 100] = 3.0e38
+    out, guard = guarded_out(7, n, dtype)
+    w4.matvec_w4_experts(x, q, s, torch.from_numpy(offsets).cuda(), out, order=torch.from_numpy(order).cuda(), top_k=1)
+    want, terms = torch.zeros((7, n), dtype=torch.float64), torch.zeros((7, n), dtype=torch.float64)
+    for e in (0, 3, 23):
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        rows, w = x[torch.from_numpy(order[at]).cuda().long()].double(), weights(e)
+        want[at], terms[at] = (rows @ w.T).cpu(), (rows.abs() @ w.abs().T).cpu()
+    check(out, want.numpy(), terms.numpy(), k, group, p, tiny)
+    assert guard.bands_intact()
+
+
+@pytest.mark.parametrize("wide_scales", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_a_staged_rows_sums_do_not_overflow_before_the_result(group, wide_scales):
+    # 4096 ones times codes of 7 and scales of 2^112: 7 * 2^124, exact in BF16
+    k, n = 4096, 19500
+    q = torch.full((n, k // 2), 0x77, dtype=torch.uint8, device="cuda")
+    s = torch.full((n, k // group), 2.0 ** 112, dtype=torch.float32 if wide_scales else torch.bfloat16, device="cuda")
+    x = torch.ones((1, k), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((1, n), dtype=torch.bfloat16, device="cuda")
+    w4.matvec_w4(x, q, s, out)
+    assert bool((out.double() == 7 * 2.0 ** 124).all())
+    few = torch.empty((1, 64), dtype=torch.bfloat16, device="cuda")
+    w4.matvec_w4(x, q[:64], s[:64], few)
+    assert torch.equal(few, out[:, :64])
+    q, s = (t[:n // 3].expand(6, -1, -1).contiguous() for t in (q, s))
+    rows = torch.empty((3, n // 3), dtype=torch.bfloat16, device="cuda")  # a row for each of the first three experts
+    offsets = torch.tensor([0, 1, 2, 3, 3, 3, 3], dtype=torch.int32, device="cuda")
+    w4.matvec_w4_experts(x.expand(3, k).contiguous(), q, s, offsets, rows)
+    assert bool((rows == out[0, 0]).all())
