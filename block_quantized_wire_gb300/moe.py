@@ -63,11 +63,16 @@ def decode_part(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w: Ex
 
 def decode_layer(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, ranks: Sequence[ExpertWeights],
                  mode: str = "i8_a2a") -> List[torch.Tensor]:
-    """The whole layer: every rank's part, summed through the wire mode ``mode`` (see
-    ``topology.MODES``; an empty name adds in float32). Returns what the owners hold: one
-    tensor for the all-to-all modes, row shards for the ring and all-gather modes."""
-    parts = [decode_part(x, ids, weights, w) for w in ranks]
+    """The whole layer: every rank's part, summed through the wire mode ``mode``: a ring,
+    all-to-all or all-gather mode of ``topology.MODES``, or an empty name for a sum in float32.
+    Returns what the owners hold: one tensor for the all-to-all modes, row shards for the ring
+    and all-gather modes. ``i8`` and ``mx`` are round trips of one tensor there, which sum
+    nothing, and raise ValueError."""
     reduce = topology.select_mode(mode)
+    if reduce in (topology.i8_roundtrip, topology.mx_roundtrip):
+        raise ValueError(f"wire mode {mode!r} is one tensor's round trip and sums no parts; the all-gather modes that "
+                         "do are 'i8_ag' and 'e4m3_ag'")
+    parts = [decode_part(x, ids, weights, w) for w in ranks]
     if reduce is None:
         return [torch.stack([p.float() for p in parts]).sum(0).to(x.dtype)]
     owned = reduce(parts)[2]

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_quantized_wire_gb300 import _lib, build, codec, moe, w4
+from block_quantized_wire_gb300 import _lib, build, codec, moe, topology, w4
 from tests.helpers import Guarded
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +121,18 @@ def test_training_form_and_its_gradients():
         bound = 2.0 ** -23 * n * float(ref.abs().max()) * 8 + 1e-12
         assert float((got.double().cpu() - ref).abs().max()) <= bound
     assert not dw.cpu()[~here].any()
+
+
+@pytest.mark.parametrize("mode", ["i8_ring", "i8_a2a", "i8_ag", "mx_ring", "mx_a2a", "e4m3_ag"])
+def test_decode_layer_returns_what_the_modes_owners_hold(mode):
+    torch.manual_seed(5)
+    tokens, n_ranks, hidden, inner = 8, 4, 256, 64
+    x = torch.randn(tokens, hidden, device="cuda").to(torch.bfloat16)
+    top, ids = torch.randn(tokens, 2 * n_ranks, device="cuda").topk(3, dim=1)
+    weights = torch.softmax(top, dim=1)
+    ranks = [moe.quantize_experts(2 * r, *((torch.randn(2, *shape, device="cuda") / 16).to(torch.bfloat16)
+                                           for shape in ((2 * inner, hidden), (hidden, inner)))) for r in range(n_ranks)]
+    parts = [moe.decode_part(x, ids, weights, w) for w in ranks]
+    owned = topology.MODES[mode](parts)[2]
+    want = owned if isinstance(owned, torch.Tensor) else torch.cat(owned)
+    assert torch.equal(torch.cat(moe.decode_layer(x, ids, weights, ranks, mode)), want)
