@@ -101,6 +101,8 @@ def ring(wire: Wire, xs: Sequence[torch.Tensor], stream=None):
             last = step == W - 1
             wire.hop(q, s, shards[rank][c], q2, s2, owner if last else None, stream)
             q, s = q2, s2
+        if W == 1:  # no hop has materialized the owner
+            wire.dequant(q, s, owner, stream)
         finals.append((q, s))
         owners.append(owner)
     outs = []

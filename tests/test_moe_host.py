@@ -30,3 +30,23 @@ def test_every_other_mode_sums_the_parts(mode, monkeypatch):
     monkeypatch.setattr(topology, "MODES", {m: fake for m in topology.MODES})
     (out,) = moe.decode_layer(parts[0], None, None, [0, 1], mode)
     assert torch.equal(out, parts[0] + parts[1]) and len(seen) == (1 if mode else 0)
+
+
+def test_a_ring_of_one_rank_materializes_its_owner():
+    # one rank: no hop runs, so the owner's copy comes from its own payload
+    import torch
+
+    def empty(n, device):
+        return None, torch.zeros(n), torch.zeros(1)
+
+    def quant(x, q, s, stream):
+        q.copy_(x.reshape(-1) * 2)
+
+    def dequant(q, s, out, stream):
+        out.copy_((q / 2).view(out.shape))
+
+    wire = topology.Wire(empty, quant, dequant, None, None)
+    x = torch.arange(256.0).view(2, 128)
+    outs, finals, owners = topology.ring(wire, [x])
+    assert torch.equal(outs[0], x) and torch.equal(finals[0][0], 2 * x.reshape(-1))
+    assert torch.equal(owners[0], x)
