@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
             const int e = base + threadIdx.x;
             const int lo = e < a.n_experts ? offset(e) : 0, hi = e < a.n_experts ? offset(e + 1) : 0;
             const unsigned has = __ballot_sync(kFull, hi > lo);
-            const int mine = hi > lo ? (hi - lo - 1) / pass_cap + 1 : 0;
+            const int mine = pass_count(hi - lo, pass_cap);
             int upto = mine;  // passes of this warp's experts up to this one
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
             else
                 hi = mid;
         }
-        const int each = kExperts ? (active[lo].hi - active[lo].lo - 1) / pass_cap + 1 : 1;
+        const int each = kExperts ? pass_count(active[lo].hi - active[lo].lo, pass_cap) : 1;
         const int64_t block = (cost - (int64_t)active[lo].before * row_blocks + each - 1) / each;
         return lo * row_blocks + (int)(block < row_blocks ? block : row_blocks);
     };
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
     const int align_s = Sc::align_of(scales, a.k / kGroup, a.ld_s, a.expert_s);
     const int my_plain = align_s >= Sc::kAlign && whole_steps > warp
                              ? (whole_steps - warp - 1) / kW4Warps + 1 : 0;
-    auto chunk_passes = [&](int rest) { return ((rest < chunk_cap ? rest : chunk_cap) + pass_cap - 1) / pass_cap; };
+    auto chunk_passes = [&](int rest) { return pass_count(rest < chunk_cap ? rest : chunk_cap, pass_cap); };
     auto open_chunk = [&]() {  // the run's first block again
         const int64_t r0 = (int64_t)f_first * kItemRows, e = active[f_active].expert;
         f_block = f_first;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
         int next_chunk = er.lo;
         while (next_chunk < er.hi) {
             const int chunk = next_chunk;
-            next_chunk = er.hi - chunk > chunk_cap ? chunk + chunk_cap : er.hi;
+            next_chunk = next_pass(chunk, er.hi, chunk_cap);
             if constexpr (kStaged) {
                 __syncthreads();  // the readers of the rows before
                 stage_x(chunk, next_chunk - chunk);
@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
                 const int r0 = block * kItemRows;
                 // rows g + 8 i all start in the same half of a word
                 const int row_skew = (int)(er.expert * a.expert_s + (r0 + g) * a.ld_s) & 1;
-                for (int p0 = chunk; p0 < next_chunk; p0 += pass_cap) {
-                    const int pass_rows = next_chunk - p0 < pass_cap ? next_chunk - p0 : pass_cap;
+                for (int p0 = chunk; p0 < next_chunk; p0 = next_pass(p0, next_chunk, pass_cap)) {
+                    const int pass_rows = next_pass(p0, next_chunk, pass_cap) - p0;
                     const int in_chunk = kStaged ? p0 - chunk : 0;
                     // This lane's rows of x, column g of each tile. Columns past the last row repeat
                     // it: their products are not stored.
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_w4_kernel(const __grid_con
                     }
 #pragma unroll
                     for (int m = 0; m < (kStaged ? 0 : kTiles); m++) {
-                        const int want = p0 + 8 * m + (kEven ? g / 2 : g), p = want < er.hi ? want : er.hi - 1;
+                        const int want = 8 * m + (kEven ? g / 2 : g), p = p0 + (want < pass_rows ? want : pass_rows - 1);
                         int row = p;
                         if (kExperts && a.order) row = dbg_ok(a.order + p, 4, false) ? __ldg(a.order + p) / a.top_k : 0;
                         if (row < 0 || row >= a.x_rows) row = 0;  // a wrong plan
