@@ -41,7 +41,7 @@ DEBUG_OBJDIR = os.path.join(PKG, "_build_debug")
 DEBUG_FLAGS = ["-DBQ_DEBUG=1"]
 
 SOURCES = ["bq_api.cu", "bq_i8.cu", "bq_mx.cu", "bq_mx_wire.cu", "bq_e4m3.cu", "bq_experts.cu", "bq_w4.cu"]
-HEADERS = ["bq_device.cuh", "bq_launch.h", "bq_chunks.cuh", "bq_rows.cuh"]
+HEADERS = ["bq_device.cuh", "bq_launch.h", "bq_chunks.cuh", "bq_rows.cuh", "bq_launch_cache.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [

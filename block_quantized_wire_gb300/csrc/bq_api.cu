@@ -6,6 +6,7 @@
 
 #include "bq.h"
 #include "bq_launch.h"
+#include "bq_launch_cache.h"
 
 #ifndef BQ_DEBUG
 #define BQ_DEBUG 0
@@ -57,18 +58,26 @@ namespace bqk {
 
 namespace {
 constexpr int kMaxDevices = 64;
-constexpr int kMaxKernels = 1024;  // (kernel, dynamic smem, block, device) entries
 std::atomic<int> g_sms[kMaxDevices];
-struct OccEntry {
-    const void *kernel;
-    size_t smem;
-    int block;
-    int device;
-    int ctas_per_sm;
+
+struct Runtime {
+    cudaError_t limit(const void *kernel, size_t *bytes)
+    {
+        cudaFuncAttributes attr;
+        if (cudaError_t e = cudaFuncGetAttributes(&attr, kernel)) return e;
+        *bytes = static_cast<size_t>(attr.maxDynamicSharedSizeBytes);
+        return cudaSuccess;
+    }
+    cudaError_t raise_limit(const void *kernel, size_t bytes)
+    {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    }
+    cudaError_t ctas_per_sm(const void *kernel, int block, size_t smem, int *ctas)
+    {
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, block, smem);
+    }
 };
-OccEntry g_occ[kMaxKernels];
-int g_occ_n = 0;
-std::mutex g_occ_mu;
+LaunchCache<Runtime> g_launches;
 }  // namespace
 
 namespace {
@@ -96,29 +105,8 @@ cudaError_t grid_for(const void *kernel, int64_t nchunk, int *grid, size_t smem,
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
     if (cudaError_t e = sm_count_of(dev, &sms)) return e;
     int occ = 0;
-    {
-        std::lock_guard<std::mutex> lock(g_occ_mu);
-        for (int i = 0; i < g_occ_n; i++)
-            if (g_occ[i].kernel == kernel && g_occ[i].smem == smem && g_occ[i].block == block && g_occ[i].device == dev)
-                occ = g_occ[i].ctas_per_sm;
-    }
-    if (occ == 0) {
-        // The kernel's shared memory limit is that of its largest entry: a call with less must
-        // not lower it for those that found theirs before. A full table starts anew.
-        std::lock_guard<std::mutex> lock(g_occ_mu);
-        if (g_occ_n == kMaxKernels) g_occ_n = 0;
-        size_t limit = 48 * 1024;
-        for (int i = 0; i < g_occ_n; i++)
-            if (g_occ[i].kernel == kernel && g_occ[i].device == dev && g_occ[i].smem > limit) limit = g_occ[i].smem;
-        if (smem > limit) {
-            if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(smem)))
-                return e;
-        }
-        if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, block, smem)) return e;
-        if (occ < 1) occ = 1;
-        g_occ[g_occ_n++] = OccEntry{kernel, smem, block, dev, occ};
-    }
+    Runtime rt;
+    if (int e = g_launches.ctas_per_sm(rt, kernel, smem, block, dev, &occ)) return static_cast<cudaError_t>(e);
     const int64_t warps_per_cta = block / 32;
     const int64_t need = (nchunk + warps_per_cta - 1) / warps_per_cta;
     const int64_t full = static_cast<int64_t>(sms) * occ;
