@@ -274,10 +274,10 @@ struct ExpertRows {
     int before;  // passes over a row block of the experts before this one
 };
 
-// Shared memory for staged rows of x, what two CTAs an SM leave beside their rings; a row is
-// padded to whole steps.
-constexpr int64_t kStagedBytes = 44 * 1024;
-constexpr int64_t kStagedItems = 1216;  // 16-row items that make staging pay: four for each of 304 CTAs
+// Shared memory of a CTA where two stay resident on an SM (228 KB, of which each takes 1 KB
+// more than it asks for, less the static part); staged rows of x fill what the rest leaves. A
+// row is padded to whole steps.
+constexpr int64_t kCtaBytes = 112 * 1024;
 inline int64_t staged_row_bytes(int64_t k) { return (k + 255) / 256 * 512; }
 
 template <class T_, class S_, int kGroup_, int kPassRows_, int kRowTiles_, bool kStaged_, bool kExperts_>
@@ -728,24 +728,31 @@ cudaError_t launch_w4(W4Args a, cudaStream_t st)
 template <class T, class S, int kGroup, bool kExperts>
 cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
 {
-    // Staging pays where one row goes over many long weight rows, so that few CTAs stage it
-    // and each uses it for long: one token's eight experts of 4096 x 7168 take 32.1 us staged
-    // and 36.3 us directly, one row times 32000 x 8192 33.5 and 39.9 us; one token's eight experts
-    // of 2432 x 4096 14.9 and 14.6 us.
-    const int64_t used = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
-    const int64_t cap = a.k > 0 ? kStagedBytes / staged_row_bytes(a.k) : 0;
-    if (rows == 1 && a.k >= 4096 && cap >= 1 && used * (a.n / 16) >= kStagedItems) {
-        a.staged_rows = (int)(!kExperts ? 1 : cap < 4 ? cap : cap / 4 * 4);
-        return launch_w4<W4Shape<T, S, kGroup, 4, 1, true, kExperts>>(a, st);
-    }
-    // One 16-row tile a warp makes twice the items of half the steps, each step a little dearer:
-    // taken where rounds of the two CTAs an SM, times the steps of a warp and one for the
-    // item's end, come out fewer.
+    // One 16-row tile a warp makes twice the items of half the steps: finer, each step dearer.
+    // Rows of x staged in shared memory make the finer one's steps cheaper, for a round's worth of
+    // setting up. The least of rounds (of two CTAs an SM) times steps (of a warp, and half a one
+    // for an item's end) times what a step takes, by a fit to 409 shapes of 1 to 8 rows. In us, one
+    // tile, two, staged:
+    //   one row x  9728 x 7168, group  32: 12.4, 11.4, 12.3;  x 14592: 17.0, 18.8, 15.9
+    //   one row x 58368 x 2048, group 128: 20.4, 17.0, 19.6;  x  1504 x 7168: 5.0, 6.4, 5.6
+    //   one token's eight experts of 4096 x 7168, group 32: 36.6, 36.4, 32.6; 7168 x 2048: 25.9, 21.2, 22.2
+    //   eight rows x 14592 x 7168, group 32: 17.8, 19.8;  x 9728 x 11264: 17.8, 16.2
     int sms = 1;
     if (cudaError_t e = sm_count(&sms)) return e;
-    const int64_t rounds1 = (used * ((a.n + 15) / 16) - 1) / (2 * sms) + 1, steps1 = (a.k + 2047) / 2048;
-    const int64_t rounds2 = (used * ((a.n + 31) / 32) - 1) / (2 * sms) + 1, steps2 = (a.k + 1023) / 1024;
-    const bool one = 11 * rounds1 * (steps1 + 1) < 10 * rounds2 * (steps2 + 1);
+    const int64_t used = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
+    auto half_steps = [&](int tiles) {
+        const int64_t items = used * ((a.n + 16 * tiles - 1) / (16 * tiles)), ctas = 2 * sms;
+        return ((items - 1) / ctas + 1) * (2 * ((a.k * tiles + 2047) / 2048) + 1);
+    };
+    const int64_t one_cost = 21 * half_steps(1), two_cost = 20 * half_steps(2), staged_cost = 18 * half_steps(1) + 40;
+    using Staged = W4Shape<T, S, kGroup, 4, 1, true, kExperts>;
+    const int64_t room = kCtaBytes - (int64_t)(Staged::kRingBytes + Staged::kSumBytes + sizeof(ExpertRows) * a.n_experts + 15);
+    const int64_t cap = a.k > 0 && room > 0 ? room / staged_row_bytes(a.k) : 0;
+    if (rows == 1 && cap >= 1 && staged_cost < one_cost && staged_cost < two_cost) {
+        a.staged_rows = (int)(!kExperts ? 1 : cap < 4 ? cap : cap / 4 * 4);
+        return launch_w4<Staged>(a, st);
+    }
+    const bool one = one_cost < two_cost;
     if (rows <= 4)
         return one ? launch_w4<W4Shape<T, S, kGroup, 4, 1, false, kExperts>>(a, st)
                    : launch_w4<W4Shape<T, S, kGroup, 4, 2, false, kExperts>>(a, st);

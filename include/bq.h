@@ -393,7 +393,11 @@ BQ_API bq_status bq_matvec_w4(const void *x, int type, int64_t rows, int64_t k, 
  *   scales   [n_experts][n][ld_s], experts expert_s values apart
  *   offsets  [n_experts + 1]; order [slots] or NULL; slots = tokens * top_k
  *   out      [slots][ld_out] (written, zeros past the kept places)
- * Only the weights of experts that have rows are read. */
+ * Only the weights of experts that have rows are read, once for each pass over the expert's
+ * rows: 16, 8 or 4 rows a pass where twice the average slots / n_experts is above 8, above 4 or
+ * less, and where it is at most 1 perhaps as few as fit into shared memory (one from about
+ * 16384 columns on). A plan that loads one expert with many times the average is right, and
+ * reads that expert's weights that often. */
 BQ_API bq_status bq_matvec_w4_experts(const void *x, int type, int64_t x_rows, int64_t k, int64_t ld_x,
                                       const uint8_t *q, int64_t n, int64_t ld_q, int64_t expert_q, const void *scales,
                                       int scale_type, int group, int64_t ld_s, int64_t expert_s,

@@ -437,3 +437,54 @@ def test_a_staged_rows_sums_do_not_overflow_before_the_result(group, wide_scales
     offsets = torch.tensor([0, 1, 2, 3, 3, 3, 3], dtype=torch.int32, device="cuda")
     w4.matvec_w4_experts(x.expand(3, k).contiguous(), q, s, offsets, rows)
     assert bool((rows == out[0, 0]).all())
+
+
+# 912 items of 16 weight rows, three rounds of the CTAs, where two-tile items would take two
+# longer ones: staged rows of lengths that end inside a step, with odd numbers of scales
+ODD_STAGED = [("bf16", False, 4160, 64), ("bf16", True, 7200, 32), ("bf16", False, 7200, 32), ("f16", False, 4160, 64)]
+
+
+@pytest.mark.parametrize("name,wide_scales,k,group", ODD_STAGED)
+def test_one_row_of_odd_length_times_many(name, wide_scales, k, group):
+    dtype, p, tiny = TYPES[name]
+    n = 14587
+    g, q, s, weights = staged_case(name, torch.float32 if wide_scales else dtype, (), n, k, group, k + 2)
+    x = torch.randn((1, k), generator=g, device="cuda").to(dtype)
+    out, guard = guarded_out(1, n, dtype)
+    w4.matvec_w4(x, q, s, out)
+    w, x64 = weights(), x.double()
+    check(out, (x64 @ w.T).cpu().numpy(), (x64.abs() @ w.abs().T).cpu().numpy(), k, group, p, tiny)
+    assert guard.bands_intact()
+
+
+@pytest.mark.parametrize("name,wide_scales,k,group", ODD_STAGED)
+def test_experts_rows_of_odd_length_beyond_the_staged_ones(name, wide_scales, k, group):
+    # 24 slots over 48 experts, one of which has ten rows, more than are staged at once
+    dtype, p, tiny = TYPES[name]
+    n, n_experts = 599, 48
+    g, q, s, weights = staged_case(name, torch.float32 if wide_scales else dtype, (n_experts,), n, k, group, k + 3)
+    ids = np.array([[7]] * 5 + [[e] for e in (0, 47, 60, 9, 33, 2, 2, 18, 5)] + [[7]] * 5 + [[e] for e in range(20, 25)])
+    offsets, order, _ = plan_of(ids, n_experts)
+    x = torch.randn((24, k), generator=g, device="cuda").to(dtype)
+    out, guard = guarded_out(24, n, dtype)
+    w4.matvec_w4_experts(x, q, s, torch.from_numpy(offsets).cuda(), out, order=torch.from_numpy(order).cuda(), top_k=1)
+    want, terms = torch.zeros((24, n), dtype=torch.float64), torch.zeros((24, n), dtype=torch.float64)
+    for e in range(n_experts):
+        at = slice(int(offsets[e]), int(offsets[e + 1]))
+        if at.start < at.stop:
+            rows, w = x[torch.from_numpy(order[at]).cuda().long()].double(), weights(e)
+            want[at], terms[at] = (rows @ w.T).cpu(), (rows.abs() @ w.abs().T).cpu()
+    check(out, want.numpy(), terms.numpy(), k, group, p, tiny)
+    assert not out[int(offsets[-1]):].any() and guard.bands_intact()
+
+
+def test_staged_rows_in_the_debug_build_decline_no_access(bq_lib):
+    with _lib.use_library(build.build_debug_library()):
+        codec.take_index_errors()
+        for case in ODD_STAGED:
+            test_one_row_of_odd_length_times_many(*case)
+            test_experts_rows_of_odd_length_beyond_the_staged_ones(*case)
+        for case in STAGED:
+            test_one_row_whose_largest_value_takes_no_part(*case)
+        torch.cuda.synchronize()
+        assert codec.take_index_errors() == 0
