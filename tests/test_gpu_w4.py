@@ -488,3 +488,36 @@ def test_staged_rows_in_the_debug_build_decline_no_access(bq_lib):
             test_one_row_whose_largest_value_takes_no_part(*case)
         torch.cuda.synchronize()
         assert codec.take_index_errors() == 0
+
+
+@pytest.mark.parametrize("n,rows", [(48, 1), (48, 6), (48, 12), (19500, 1)])
+@pytest.mark.parametrize("name", list(TYPES))
+def test_rows_of_subnormal_values(name, n, rows):
+    # the smallest values that x can hold, with FP32 scales that bring the result up: products
+    # and sums are exact multiples of x's smallest, so check's bound holds as it stands
+    dtype, p, tiny = TYPES[name]
+    k, group = 4096, 64
+    g, q, s, weights = staged_case(name, torch.float32, (), n, k, group, n + rows)
+    smallest = 2.0 ** -133 if name == "bf16" else 2.0 ** -24
+    s.copy_(s.abs().add_(0.01) * (2.0 ** 60 if name == "bf16" else 1.0))
+    x64 = torch.randint(-7, 8, (rows, k), generator=g, device="cuda").double() * smallest
+    x = x64.to(dtype)
+    assert torch.equal(x.double(), x64)
+    out, guard = guarded_out(rows, n, dtype)
+    w4.matvec_w4(x, q, s, out)
+    w = weights()
+    check(out, (x64 @ w.T).cpu().numpy(), (x64.abs() @ w.abs().T).cpu().numpy(), k, group, p, tiny)
+    assert guard.bands_intact()
+
+
+def test_equal_rows_give_equal_results_in_every_form():
+    # a row repeated at other places of one launch, and the launch repeated: the same bits
+    for rows, n, k in ((32, 200, 2048), (32, 40000, 1024), (4, 30000, 2048), (8, 4864, 4096)):
+        g, q, s, _ = staged_case("bf16", torch.bfloat16, (), n, k, 32, rows)
+        x = torch.randn((rows, k), generator=g, device="cuda").to(torch.bfloat16)
+        x[rows - 1], x[rows // 2] = x[0], x[0]
+        outs = [torch.empty((rows, n), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        for out in outs:
+            w4.matvec_w4(x, q, s, out)
+        assert torch.equal(outs[0], outs[1])
+        assert torch.equal(outs[0][0], outs[0][rows - 1]) and torch.equal(outs[0][0], outs[0][rows // 2])
