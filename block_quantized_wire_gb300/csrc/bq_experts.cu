@@ -321,8 +321,8 @@ struct Units {
 // out[inverse[t, j]] = x[t]: a warp holds a segment of one token's row in registers and
 // stores it to each of the token's places, so every row of x is read once. Rows past the
 // kept places are zeros. Bound by the stores: 16384 rows of 7168 BF16 values to 131072 places
-// (2.1 GB, 8 of 9 parts written) take 349 us, 6.06 TB/s, where the GPU writes at 6.55 TB/s
-// without reading.
+// (2.1 GB, 8 of 9 parts written) take 348 us, 6.08 TB/s, where the GPU writes at 6.55 TB/s
+// without reading. Rows of odd widths: 16384 x 1001 FP16, top-6, 78 us, 2.9 TB/s.
 constexpr int kGatherPieces = 4;
 constexpr int kGatherRows = 4;
 
@@ -411,8 +411,10 @@ gather_kernel(const T *__restrict__ x, int64_t tokens, int64_t hidden, int64_t l
 // sum, which is the gather's gradient. A warp takes a segment of one token's row. Its lanes
 // fetch the token's places and weights together, one each, and the rows of kCombineRows
 // kept slots are loaded before any is added, so that enough loads are in flight. Bound by the
-// memory: 65536 rows of 7168 BF16 values summed into 16384 take 176 us, 6.7 TB/s (254 us with
-// one row loaded after the other).
+// memory: 65536 rows of 7168 BF16 values summed into 16384 take 176 to 181 us, 6.5 to 6.7 TB/s
+// (254 us with one row loaded after the other). Rows of odd widths are bound by the instructions
+// that put their pieces together: 16384 x 1001 FP16, top-6, 50.3 us, 3.3 TB/s, the integer units
+// busy half of the time.
 template <bool kWide>
 constexpr int kCombinePieces = kWide ? 2 : 1;  // a piece put together holds twice the registers
 constexpr int kCombineRows = 4;
@@ -500,7 +502,8 @@ combine_kernel(const T *__restrict__ y, int64_t ld_y, const float *__restrict__ 
 // one pass over dout and y. A CTA takes up to kGradSlots slots of one token; its threads
 // walk the row together, each keeping one partial dot product per slot, and the partial
 // products are added up in a fixed tree at the end. dw of a dropped slot is 0. Bound by the
-// memory: 65536 rows of 4096 BF16 values (1.14 GB) take 176 us, 6.5 TB/s.
+// memory: 65536 rows of 4096 BF16 values (1.14 GB) take 176 us, 6.5 TB/s. Rows of odd widths, for
+// which dout is put together anew for every slot: 16384 x 1001 FP16, top-6, 202 us, 1.8 TB/s.
 constexpr int kGradSlots = 4;
 constexpr int kGradMaxThreads = 256;
 

@@ -179,7 +179,7 @@ struct Cut {
 };
 
 // Passes of up to `cap` rows over [lo, hi), hi at most 2^31 - 1: how many there are over `rows`
-// rows, and the first row of the pass after the one at p0 (hi after the last).
+// rows, and the first row after the pass that starts at p0 (hi after the last).
 __host__ __device__ __forceinline__ int pass_count(int rows, int cap) { return rows > 0 ? (rows - 1) / cap + 1 : 0; }
 __host__ __device__ __forceinline__ int next_pass(int p0, int hi, int cap) { return hi - p0 > cap ? p0 + cap : hi; }
 

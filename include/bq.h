@@ -359,7 +359,8 @@ BQ_API bq_status bq_expert_combine_grad(const void *dout, int type, int64_t ld_d
 /* Weights -> 4-bit codes with group scales, as the products below read them: per group of
  * `group` (32, 64 or 128) columns s = scale_type_rne(fl(amax / 7)), code = the integer
  * nearest to fl(x / s), ties to even, within [-7, 7]; a group with s == 0 has codes 0.
- * Bit-exact; non-finite weights are not specified.
+ * Bit-exact; weights that are not finite, or whose s is not (amax / 7 past the scale type's
+ * largest value), are not specified.
  *   x [n][ld_x] of type (read); q [n][ld_q] bytes, scales [n][ld_s] of scale_type (written)
  *   16-byte aligned x and q with rows a multiple of 16 bytes apart, scales 4-byte aligned;
  *   k % group == 0. Several experts' matrices of equal n are one matrix of n_experts * n
@@ -377,7 +378,8 @@ BQ_API bq_status bq_quant_w4(const void *x, int type, int64_t n, int64_t k, int6
  *   out     [rows][ld_out] of x's type (written)
  * The products x * code are exact; a group's are added in binary32 by the tensor cores, which
  * may truncate where a binary32 addition would round. The sum is multiplied by the scale and
- * added to the output's sum in binary32, and does not overflow where that product does not.
+ * added to the output's sum in binary32, and does not overflow where that product does not
+ * (for BF16 the output's sum is kept times 2^-12, in steps of at least 2^-137 of the result).
  * Any number of rows is right; the kernels are made for up to 16, and read the weights once
  * for every 16 rows. A wrong group, type or k returns BQ_ERR_SHAPE; n and k are at most
  * BQ_MAX_W4_DIM. */
@@ -395,9 +397,9 @@ BQ_API bq_status bq_matvec_w4(const void *x, int type, int64_t rows, int64_t k, 
  *   out      [slots][ld_out] (written, zeros past the kept places)
  * Only the weights of experts that have rows are read, once for each pass over the expert's
  * rows: 16, 8 or 4 rows a pass where twice the average slots / n_experts is above 8, above 4 or
- * less, and where it is at most 1 perhaps as few as fit into shared memory (one from about
- * 16384 columns on). A plan that loads one expert with many times the average is right, and
- * reads that expert's weights that often. */
+ * less; where it is at most 1 a pass may be the rows that fit into shared memory, at least one.
+ * A plan that loads one expert with many times the average is right, and reads that expert's
+ * weights that often. */
 BQ_API bq_status bq_matvec_w4_experts(const void *x, int type, int64_t x_rows, int64_t k, int64_t ld_x,
                                       const uint8_t *q, int64_t n, int64_t ld_q, int64_t expert_q, const void *scales,
                                       int scale_type, int group, int64_t ld_s, int64_t expert_s,
