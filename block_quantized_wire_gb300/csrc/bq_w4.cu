@@ -737,10 +737,10 @@ cudaError_t launch_w4_rows(W4Args a, int64_t rows, cudaStream_t st)
     // setting up. The least of rounds (of two CTAs an SM) times steps (of a warp, and half a one
     // for an item's end) times what a step takes, by a fit to 409 shapes of 1 to 8 rows. In us, one
     // tile, two, staged:
-    //   one row x  9728 x 7168, group  32: 12.4, 11.4, 12.3;  x 14592: 17.0, 18.8, 15.9
-    //   one row x 36864 x 2048, group 128: 15.1, 12.5, 14.4;  x 1500 x 7168: 5.0, 6.4, 5.6
-    //   one token's eight experts of 4096 x 7168, group 32: 36.6, 36.4, 32.6; 7168 x 2048: 25.9, 21.2, 22.2
-    //   eight rows x 14592 x 7168, group 32: 17.8, 19.8;  x 9728 x 11264: 17.8, 16.2
+    //   one row x 9728 x 7168, group 32: 12.1, 11.4, 12.0;  x 14592: 16.4, 18.9, 15.9
+    //   one row x 36864 x 2048, group 128: 14.6, 12.4, 14.0;  x 1500 x 7168: 4.8, 6.4, 5.5
+    //   one token's eight experts of 4096 x 7168, group 32: 36.3, 36.5, 32.1; 7168 x 2048: 25.4, 21.2, 21.5
+    //   eight rows x 14592 x 7168, group 32: 17.8, 20.1;  x 9728 x 11264: 18.1, 16.6
     int sms = 1;
     if (cudaError_t e = sm_count(&sms)) return e;
     const int64_t used = !kExperts ? 1 : a.slots < a.n_experts ? a.slots : a.n_experts;
