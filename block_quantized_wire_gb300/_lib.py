@@ -53,6 +53,11 @@ _PROTOS = {
     "bq_matvec_w4": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _P, _INT, _INT, _I64, _P, _I64, _P], _INT),
     "bq_matvec_w4_experts": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _I64, _I64, _P, _INT, _INT, _I64, _I64, _P, _INT,
                               _P, _INT, _I64, _P, _I64, _P], _INT),
+    "bq_kv4_write": ([_P, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _INT, _P], _INT),
+    "bq_kv4_read": ([_P, _P, _INT, _I64, _P, _I64, _I64, _P, _I64, _I64, _P], _INT),
+    "bq_kv4_attend": ([_P, _P, _I64, _I64, _I64, _I64, _INT, _INT, _P, _I64, _I64, _P, ctypes.c_float, _I64, _P, _I64,
+                       _I64, _I64, _P, _P, _I64, _P], _INT),
+    "bq_kv4_workspace_bytes": ([_INT, _INT, _INT, _INT], _I64),
     "bq_take_wait_timeouts": ([_P], ctypes.c_int),
     "bq_take_wait_unlanded": ([_P], ctypes.c_int),
     "bq_take_index_errors": ([_P], ctypes.c_int),
@@ -60,6 +65,14 @@ _PROTOS = {
     "bq_selftest_index_check": ([_P, _I64, _P], ctypes.c_int),
     "bq_selftest_wait_timeout": ([_P], ctypes.c_int),
 }
+
+
+class Kv4Cache(ctypes.Structure):
+    """bq_kv4_cache"""
+    _fields_ = [("k", _P), ("v", _P), ("k_scales", _P), ("v_scales", _P), ("pages", _I64), ("heads", _INT),
+                ("page", _INT), ("head_dim", _INT), ("group", _INT), ("type", _INT), ("page_stride", _I64),
+                ("head_stride", _I64), ("token_stride", _I64), ("page_stride_s", _I64), ("head_stride_s", _I64),
+                ("token_stride_s", _I64)]
 
 
 class BQError(RuntimeError):

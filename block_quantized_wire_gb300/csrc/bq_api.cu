@@ -634,6 +634,222 @@ bq_status bq_matvec_w4_experts(const void *x, int type, int64_t x_rows, int64_t 
 
 }  // extern "C"
 
+// ------------------------------------------------------------------ key-value cache in 4 bits
+namespace {
+// Dimensions of rows that lie `stride` bytes apart. True if no two rows of `row` bytes overlap;
+// `span` is then the bytes from the first row's start to the last one's end.
+struct Dim {
+    int64_t n, stride;
+};
+bool rows_apart(Dim (&d)[3], int64_t row, int64_t *span)
+{
+    for (int i = 0; i < 2; i++)
+        for (int j = 0; j < 2 - i; j++)
+            if (d[j].n <= 1 || (d[j + 1].n > 1 && d[j + 1].stride < d[j].stride)) {
+                const Dim t = d[j];
+                d[j] = d[j + 1];
+                d[j + 1] = t;
+            }
+    *span = row;
+    for (const Dim &x : d) {
+        if (x.n <= 1) continue;
+        if (x.stride < *span || x.stride > INT64_MAX / 4 / x.n) return false;
+        *span += (x.n - 1) * x.stride;
+        if (*span > INT64_MAX / 4) return false;
+    }
+    return true;
+}
+
+// One of a cache's arrays: where it starts, its bytes, and those of one page.
+struct Paged {
+    uintptr_t lo;
+    int64_t bytes, page_bytes, page_stride;
+};
+
+bool disjoint(const Paged &a, const Paged &b)
+{
+    if (!overlap(Range{a.lo, a.lo + (uintptr_t)a.bytes}, Range{b.lo, b.lo + (uintptr_t)b.bytes})) return true;
+    if (a.page_stride != b.page_stride || a.page_stride < a.page_bytes || a.page_stride < b.page_bytes) return false;
+    const Paged &first = a.lo < b.lo ? a : b, &second = a.lo < b.lo ? b : a;
+    const int64_t at = (int64_t)((second.lo - first.lo) % (uintptr_t)a.page_stride);
+    return at >= first.page_bytes && at + second.page_bytes <= a.page_stride;
+}
+
+// The checks that every call on a cache shares. Fills c, the spans of the four arrays and whether
+// there is a page at all.
+bq_status check_cache(const bq_kv4_cache *cache, bqk::Kv4Cache &c, Range (&spans)[4])
+{
+    if (!cache) return BQ_ERR_NULL;
+    const bq_kv4_cache &x = *cache;
+    if (x.type != BQ_BF16 && x.type != BQ_F16) return BQ_ERR_SHAPE;
+    if (x.head_dim < 64 || x.head_dim > 256 || x.head_dim % 64) return BQ_ERR_SHAPE;
+    if ((x.group != 32 && x.group != 64 && x.group != 128) || x.head_dim % x.group) return BQ_ERR_SHAPE;
+    if (x.pages < 0 || x.pages > INT32_MAX || x.heads < 1 || x.heads > BQ_KV4_MAX_HEADS) return BQ_ERR_SHAPE;
+    if (x.page < 1 || x.page > BQ_KV4_MAX_PAGE) return BQ_ERR_SHAPE;
+    const int64_t row = x.head_dim / 2, row_s = 4 * (x.head_dim / x.group);
+    const int64_t in_page = x.page > 1 ? (x.page - 1) : 0;
+    if (x.page > 1 && (x.token_stride < 0 || x.token_stride > (INT32_MAX - row) / in_page || x.token_stride_s < 0 ||
+                       x.token_stride_s > (INT32_MAX - row_s) / in_page))
+        return BQ_ERR_SHAPE;
+    Paged arrays[4];
+    for (int i = 0; i < 2; i++) {  // codes, pairs
+        const int64_t ps = i ? x.page_stride_s : x.page_stride, hs = i ? x.head_stride_s : x.head_stride;
+        const int64_t ts = i ? x.token_stride_s : x.token_stride;
+        const int64_t align = !i ? 16 : row_s % 16 == 0 ? 16 : row_s & -row_s;
+        Dim all[3] = {{x.page, ts}, {x.heads, hs}, {x.pages, ps}}, one[3] = {{x.page, ts}, {x.heads, hs}, {1, 0}};
+        int64_t bytes = 0, page_bytes = 0;
+        if (!rows_apart(one, i ? row_s : row, &page_bytes) || !rows_apart(all, i ? row_s : row, &bytes))
+            return BQ_ERR_SHAPE;
+        if ((x.page > 1 && ts % align) || (x.heads > 1 && hs % align) || (x.pages > 1 && ps % align)) return BQ_ERR_ALIGN;
+        const void *const of[2] = {i ? x.k_scales : x.k, i ? x.v_scales : x.v};
+        for (int j = 0; j < 2; j++) {
+            if (x.pages > 0 && !of[j]) return BQ_ERR_NULL;
+            if (!aligned(of[j], align)) return BQ_ERR_ALIGN;
+            arrays[2 * i + j] = Paged{reinterpret_cast<uintptr_t>(of[j]), bytes, page_bytes, x.pages > 1 ? ps : INT64_MAX};
+            spans[2 * i + j] = span(of[j], x.pages > 0 ? bytes : 0);
+        }
+    }
+    for (int i = 0; i < 4 && x.pages > 0; i++)
+        for (int j = i + 1; j < 4; j++)
+            if (!disjoint(arrays[i], arrays[j])) return BQ_ERR_ALIAS;
+    c.k = x.k, c.v = x.v;
+    c.k_scales = static_cast<unsigned char *>(x.k_scales), c.v_scales = static_cast<unsigned char *>(x.v_scales);
+    c.pages = x.pages, c.heads = x.heads, c.page = x.page, c.head_dim = x.head_dim, c.group = x.group;
+    c.page_stride = x.pages > 1 ? x.page_stride : 0, c.page_stride_s = x.pages > 1 ? x.page_stride_s : 0;
+    c.head_stride = x.heads > 1 ? x.head_stride : 0, c.head_stride_s = x.heads > 1 ? x.head_stride_s : 0;
+    c.token_stride = x.page > 1 ? (int32_t)x.token_stride : 0;
+    c.token_stride_s = x.page > 1 ? (int32_t)x.token_stride_s : 0;
+    return BQ_OK;
+}
+
+// [tokens][heads][head_dim] rows of 16-bit values. rows_apart is asked of rows that are written.
+bq_status check_kv_rows(const void *p, int64_t tokens, int heads, int dim, int64_t ld_token, int64_t ld_head, bool written,
+                        Range *range)
+{
+    if ((tokens > 1 && ld_token < 0) || (heads > 1 && ld_head < 0)) return BQ_ERR_SHAPE;
+    if ((tokens > 1 && ld_token > INT64_MAX / 16 / tokens) || (heads > 1 && ld_head > INT64_MAX / 16 / heads))
+        return BQ_ERR_SHAPE;
+    Dim d[3] = {{tokens, 2 * ld_token}, {heads, 2 * ld_head}, {1, 0}};
+    int64_t bytes = 0;
+    if (written && !rows_apart(d, 2 * dim, &bytes)) return BQ_ERR_SHAPE;
+    bytes = 2 * ((tokens > 1 ? (tokens - 1) * ld_token : 0) + (heads > 1 ? (heads - 1) * ld_head : 0) + dim);
+    if (!p) return BQ_ERR_NULL;
+    if (!aligned(p, 16) || (tokens > 1 && ld_token % 8) || (heads > 1 && ld_head % 8)) return BQ_ERR_ALIGN;
+    *range = span(p, bytes);
+    return BQ_OK;
+}
+
+bq_status kv4_rows(const bq_kv4_cache *cache, const void *k, int64_t k_ld_token, int64_t k_ld_head, const void *v,
+                   int64_t v_ld_token, int64_t v_ld_head, int64_t tokens, const void *slots, int slots_are_i64,
+                   bool write, cudaStream_t stream)
+{
+    bqk::Kv4Cache c;
+    Range held[4], k_rows, v_rows;
+    if (bq_status e = check_cache(cache, c, held)) return e;
+    if (tokens < 0 || tokens >= (1ll << 34) / c.heads / c.head_dim) return BQ_ERR_SHAPE;
+    if (tokens == 0) return BQ_OK;
+    if (bq_status e = check_kv_rows(k, tokens, c.heads, c.head_dim, k_ld_token, k_ld_head, !write, &k_rows)) return e;
+    if (bq_status e = check_kv_rows(v, tokens, c.heads, c.head_dim, v_ld_token, v_ld_head, !write, &v_rows)) return e;
+    if (!slots) return BQ_ERR_NULL;
+    const int size = slots_are_i64 ? 8 : 4;
+    if (!aligned(slots, size)) return BQ_ERR_ALIGN;
+    const Range in_slots = span(slots, size * tokens);
+    // the cache's own arrays are apart from each other already
+    for (const Range &h : held)
+        if (overlap(h, k_rows) || overlap(h, v_rows) || (write && overlap(h, in_slots))) return BQ_ERR_ALIAS;
+    if (!write && (overlap(k_rows, v_rows) || overlap(k_rows, in_slots) || overlap(v_rows, in_slots)))
+        return BQ_ERR_ALIAS;
+    const bqk::Kv4Rows kr = {const_cast<void *>(k), tokens > 1 ? k_ld_token : 0, c.heads > 1 ? k_ld_head : 0};
+    const bqk::Kv4Rows vr = {const_cast<void *>(v), tokens > 1 ? v_ld_token : 0, c.heads > 1 ? v_ld_head : 0};
+    const bqk::Kv4Slots at = {slots, slots_are_i64 != 0};
+    return from_cuda(write ? bqk::launch_kv4_write(cache->type, c, kr, vr, tokens, at, stream)
+                           : bqk::launch_kv4_read(cache->type, c, kr, vr, tokens, at, stream));
+}
+}  // namespace
+
+extern "C" {
+
+bq_status bq_kv4_write(const bq_kv4_cache *cache, const void *k, int64_t k_ld_token, int64_t k_ld_head, const void *v,
+                       int64_t v_ld_token, int64_t v_ld_head, int64_t tokens, const void *slots, int slots_are_i64,
+                       cudaStream_t stream)
+{
+    return kv4_rows(cache, k, k_ld_token, k_ld_head, v, v_ld_token, v_ld_head, tokens, slots, slots_are_i64, true, stream);
+}
+
+bq_status bq_kv4_read(const bq_kv4_cache *cache, const void *slots, int slots_are_i64, int64_t tokens, void *k,
+                      int64_t k_ld_token, int64_t k_ld_head, void *v, int64_t v_ld_token, int64_t v_ld_head,
+                      cudaStream_t stream)
+{
+    return kv4_rows(cache, k, k_ld_token, k_ld_head, v, v_ld_token, v_ld_head, tokens, slots, slots_are_i64, false, stream);
+}
+
+int64_t bq_kv4_workspace_bytes(int heads, int head_dim, int n_q, int q_heads)
+{
+    if (heads < 1 || heads > BQ_KV4_MAX_HEADS || head_dim < 64 || head_dim > 256 || head_dim % 64 || n_q < 1 ||
+        q_heads < 1 || q_heads > 65536 || q_heads % heads || n_q > (1 << 20) / q_heads)
+        return -1;
+    return bqk::kv4_workspace_bytes(heads, head_dim, n_q, q_heads);
+}
+
+bq_status bq_kv4_attend(const bq_kv4_cache *cache, const void *q, int64_t q_ld_batch, int64_t q_ld_query,
+                        int64_t q_ld_head, int64_t batch, int n_q, int q_heads, const int32_t *table, int64_t ld_table,
+                        int64_t width, const int32_t *lengths, float scale, int64_t window, void *out,
+                        int64_t out_ld_batch, int64_t out_ld_query, int64_t out_ld_head, float *lse, void *workspace,
+                        int64_t workspace_bytes, cudaStream_t stream)
+{
+    bqk::Kv4Cache c;
+    Range held[4];
+    if (bq_status e = check_cache(cache, c, held)) return e;
+    if (batch < 0 || batch > INT32_MAX || n_q < 0 || q_heads < 0 || q_heads > 65536 || q_heads % c.heads)
+        return BQ_ERR_SHAPE;
+    if (width < 0 || width > (INT32_MAX - (1 << 20)) / c.page || window < 0 || window > (1 << 30)) return BQ_ERR_SHAPE;
+    if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return BQ_ERR_SHAPE;
+    if (batch == 0 || n_q == 0 || q_heads == 0) return BQ_OK;
+    if (n_q > (1 << 20) / q_heads || (batch > 1 && ld_table < width)) return BQ_ERR_SHAPE;
+    // rows of q and out: [batch * n_q][q_heads] where batches and queries are dimensions of their own
+    const int64_t row = c.head_dim, lds[2][3] = {{q_ld_batch, q_ld_query, q_ld_head},
+                                                 {out_ld_batch, out_ld_query, out_ld_head}};
+    const int64_t ns[3] = {batch, n_q, q_heads};
+    int64_t bytes[2];
+    for (int i = 0; i < 2; i++) {
+        bytes[i] = 2 * row;
+        Dim d[3];
+        for (int j = 0; j < 3; j++) {
+            d[j] = Dim{ns[j], 2 * lds[i][j]};
+            if (ns[j] == 1) continue;
+            if (lds[i][j] < 0 || lds[i][j] > INT64_MAX / 64 / ns[j]) return BQ_ERR_SHAPE;
+            bytes[i] += 2 * (ns[j] - 1) * lds[i][j];
+        }
+        int64_t apart = 0;
+        if (i == 1 && !rows_apart(d, 2 * row, &apart)) return BQ_ERR_SHAPE;
+        const void *p = i ? out : q;
+        if (!p) return BQ_ERR_NULL;
+        if (!aligned(p, 16)) return BQ_ERR_ALIGN;
+        for (int j = 0; j < 3; j++)
+            if (ns[j] > 1 && lds[i][j] % 8) return BQ_ERR_ALIGN;
+    }
+    const int64_t need = bq_kv4_workspace_bytes(c.heads, c.head_dim, n_q, q_heads);
+    if (need < 0 || workspace_bytes < need) return BQ_ERR_SHAPE;
+    if (!lengths || !workspace || (width > 0 && !table)) return BQ_ERR_NULL;
+    if (!aligned(lengths, 4) || !aligned(table, 4) || !aligned(lse, 4) || !aligned(workspace, 16)) return BQ_ERR_ALIGN;
+    const Range none = span(lengths, 0);
+    const Range ins[] = {span(q, bytes[0]), width > 0 ? span(table, 4 * ((batch - 1) * ld_table + width)) : none,
+                         span(lengths, 4 * batch), held[0], held[1], held[2], held[3]};
+    const Range outs[] = {span(out, bytes[1]), span(workspace, need), lse ? span(lse, 4 * batch * n_q * q_heads) : none};
+    if (any_alias(outs, 3, ins, 7)) return BQ_ERR_ALIAS;
+    bqk::Kv4Attend a = {};
+    a.q = q, a.q_batch = batch > 1 ? q_ld_batch : 0, a.q_query = n_q > 1 ? q_ld_query : 0;
+    a.q_head = q_heads > 1 ? q_ld_head : 0;
+    a.out = out, a.out_batch = batch > 1 ? out_ld_batch : 0, a.out_query = n_q > 1 ? out_ld_query : 0;
+    a.out_head = q_heads > 1 ? out_ld_head : 0;
+    a.lse = lse, a.table = table, a.lengths = lengths, a.ld_table = batch > 1 ? ld_table : 0;
+    a.width = (int)width, a.batch = (int)batch, a.n_q = n_q, a.q_heads = q_heads, a.window = (int)window;
+    a.scale = scale, a.workspace = static_cast<float *>(workspace);
+    return from_cuda(bqk::launch_kv4_attend(cache->type, c, a, stream));
+}
+
+}  // extern "C"
+
 namespace {
 // Growth of the current device's counter `which` (0: abandoned waits, 1: copies that
 // did not land after one, 2: accesses a debug build declined) since the previous call
@@ -650,7 +866,8 @@ bq_status take_wait_counter(int which, int64_t *count)
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BQ_ERR_CUDA;
     unsigned long long total = 0;
     for (auto read : {bqk::read_wait_counters_i8, bqk::read_wait_counters_mx_wire, bqk::read_wait_counters_mx,
-                      bqk::read_wait_counters_e4m3, bqk::read_wait_counters_experts, bqk::read_wait_counters_w4}) {
+                      bqk::read_wait_counters_e4m3, bqk::read_wait_counters_experts, bqk::read_wait_counters_w4,
+                      bqk::read_wait_counters_kv4, bqk::read_wait_counters_attend}) {
         unsigned long long v[3] = {0, 0, 0};
         if (read(v) != cudaSuccess) return BQ_ERR_CUDA;
         total += v[which];

@@ -113,6 +113,58 @@ cudaError_t launch_quant_w4(int type, int scale_type, int group, const void *x, 
                             uint8_t *q, int64_t ld_q, void *scales, int64_t ld_s, cudaStream_t st);
 cudaError_t launch_matvec_w4(int x_type, int scale_type, int group, const W4Args &a, cudaStream_t st);
 
+// The key-value cache in 4 bits (bq_kv4.cu, bq_attend.cu).
+
+// Whole numbers below 2^31 divided by one that the host knows: n / d = (umulhi(n, mul) + n) >> shift.
+struct Divisor {
+    uint32_t d, mul, shift;
+};
+inline Divisor divisor(uint32_t d)  // 1 <= d < 2^31
+{
+    uint32_t shift = 0;
+    while ((1ull << shift) < d) shift++;
+    return Divisor{d, (uint32_t)((((1ull << shift) - d) << 32) / d + 1), shift};
+}
+
+// Strides in bytes, the same for keys and values.
+struct Kv4Cache {
+    uint8_t *k, *v;
+    unsigned char *k_scales, *v_scales;
+    int64_t pages;
+    int heads, page, head_dim, group;
+    int64_t page_stride, head_stride, page_stride_s, head_stride_s;
+    int32_t token_stride, token_stride_s;
+};
+// Rows of tokens beside a cache: token and head strides in values.
+struct Kv4Rows {
+    void *p;
+    int64_t ld_token, ld_head;
+};
+struct Kv4Slots {
+    const void *p;
+    bool wide;  // int64
+};
+cudaError_t launch_kv4_write(int type, const Kv4Cache &c, const Kv4Rows &k, const Kv4Rows &v, int64_t tokens,
+                             const Kv4Slots &slots, cudaStream_t st);
+cudaError_t launch_kv4_read(int type, const Kv4Cache &c, const Kv4Rows &k, const Kv4Rows &v, int64_t tokens,
+                            const Kv4Slots &slots, cudaStream_t st);
+
+// Attention over a cache. Strides of q and out in values.
+struct Kv4Attend {
+    const void *q;
+    int64_t q_batch, q_query, q_head;
+    void *out;
+    int64_t out_batch, out_query, out_head;
+    float *lse;
+    const int32_t *table, *lengths;
+    int64_t ld_table;
+    int width, batch, n_q, q_heads, window;
+    float scale;
+    float *workspace;
+};
+cudaError_t launch_kv4_attend(int type, const Kv4Cache &c, const Kv4Attend &a, cudaStream_t st);
+int64_t kv4_workspace_bytes(int heads, int head_dim, int n_q, int q_heads);
+
 // Programmatic dependent launch: every codec kernel is launched with programmatic
 // stream serialization and begins with griddepcontrol.wait, which returns once the
 // previous grid in the stream has completed and its memory is visible. The kernel then
@@ -171,6 +223,8 @@ cudaError_t read_wait_counters_mx(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_e4m3(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_experts(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_w4(unsigned long long (&v)[3]);
+cudaError_t read_wait_counters_kv4(unsigned long long (&v)[3]);
+cudaError_t read_wait_counters_attend(unsigned long long (&v)[3]);
 cudaError_t launch_wait_selftest(cudaStream_t st);
 // Debug build: one listed 256-byte range of buf and one load at byte 512 (declined).
 cudaError_t launch_index_selftest(void *buf, cudaStream_t st);

@@ -13,7 +13,7 @@ topologies. Two forms of a rank's part:
 """
 from __future__ import annotations
 
-from typing import Callable, List, NamedTuple, Sequence
+from typing import Callable, List, NamedTuple, Optional, Sequence
 
 import torch
 
@@ -61,6 +61,24 @@ def decode_part(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w: Ex
     return out
 
 
+def reduction(mode: str) -> Optional[Callable]:
+    """The topology that sums a layer's parts in wire mode ``mode``, None for an empty name. ``i8`` and
+    ``mx`` are round trips of one tensor there, which sum nothing, and raise ValueError."""
+    reduce = topology.select_mode(mode)
+    if reduce in (topology.i8_roundtrip, topology.mx_roundtrip):
+        raise ValueError(f"wire mode {mode!r} is one tensor's round trip and sums no parts; the all-gather modes that "
+                         "do are 'i8_ag' and 'e4m3_ag'")
+    return reduce
+
+
+def summed(parts: List[torch.Tensor], reduce: Optional[Callable]) -> List[torch.Tensor]:
+    """A layer's parts summed by ``reduction``'s answer: what the owners hold, or one sum in float32."""
+    if reduce is None:
+        return [torch.stack([p.float() for p in parts]).sum(0).to(parts[0].dtype)]
+    owned = reduce(parts)[2]
+    return [owned] if isinstance(owned, torch.Tensor) else list(owned)
+
+
 def decode_layer(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, ranks: Sequence[ExpertWeights],
                  mode: str = "i8_a2a") -> List[torch.Tensor]:
     """The whole layer: every rank's part, summed through the wire mode ``mode``: a ring,
@@ -68,15 +86,8 @@ def decode_layer(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, rank
     Returns what the owners hold: one tensor for the all-to-all modes, row shards for the ring
     and all-gather modes. ``i8`` and ``mx`` are round trips of one tensor there, which sum
     nothing, and raise ValueError."""
-    reduce = topology.select_mode(mode)
-    if reduce in (topology.i8_roundtrip, topology.mx_roundtrip):
-        raise ValueError(f"wire mode {mode!r} is one tensor's round trip and sums no parts; the all-gather modes that "
-                         "do are 'i8_ag' and 'e4m3_ag'")
-    parts = [decode_part(x, ids, weights, w) for w in ranks]
-    if reduce is None:
-        return [torch.stack([p.float() for p in parts]).sum(0).to(x.dtype)]
-    owned = reduce(parts)[2]
-    return [owned] if isinstance(owned, torch.Tensor) else list(owned)
+    reduce = reduction(mode)
+    return summed([decode_part(x, ids, weights, w) for w in ranks], reduce)
 
 
 class Part(NamedTuple):

@@ -406,6 +406,87 @@ BQ_API bq_status bq_matvec_w4_experts(const void *x, int type, int64_t x_rows, i
                                       const int32_t *offsets, int n_experts, const int32_t *order, int top_k,
                                       int64_t slots, void *out, int64_t ld_out, cudaStream_t stream);
 
+/* A key-value cache in 4 bits, in pages: rows (one head of one token, of keys or of values)
+ * written from 16-bit values, read back, and attended over.
+ *
+ * A row is head_dim signed 4-bit codes (two's complement, the even column in the low half of a
+ * byte, as the 4-bit products above read them) and, for each group of `group` consecutive
+ * columns, a pair (scale, offset) of the cache's type, BF16 or FP16. A code stands for
+ * fl(code * scale + offset) in binary32, the product exact. A slot is page * `page` + place: one
+ * token's place in the cache. */
+typedef struct {
+    uint8_t *k, *v;            /* codes of the keys and of the values */
+    void *k_scales, *v_scales; /* their pairs, 4 bytes each: the scale in the lower address */
+    int64_t pages;             /* 0 to 2^31 - 1 */
+    int heads;                 /* key-value heads, 1 to BQ_KV4_MAX_HEADS */
+    int page;                  /* tokens of a page, 1 to BQ_KV4_MAX_PAGE */
+    int head_dim;              /* 64, 128, 192 or 256 */
+    int group;                 /* 32, 64 or 128, a divisor of head_dim */
+    int type;                  /* BQ_BF16 or BQ_F16 */
+    /* Bytes from a page, head or token to the next, the same for keys and values. Any order of the
+     * three that keeps rows apart; where a dimension has size 1 its stride is not looked at. One
+     * head's rows of a page span less than 2^31 bytes. */
+    int64_t page_stride, head_stride, token_stride;       /* of codes */
+    int64_t page_stride_s, head_stride_s, token_stride_s; /* of pairs */
+} bq_kv4_cache;
+/* Codes: 16-byte aligned, strides multiples of 16. Pairs: aligned, with their strides, to the
+ * largest power of two that divides a row's 4 * head_dim / group bytes, at most 16. The four
+ * arrays may share one buffer (say, each page's keys, values and pairs in one block) where their
+ * strides show that they do not overlap: apart altogether, or in separate parts of pages that are
+ * equally far apart. */
+#define BQ_KV4_MAX_HEADS 1024
+#define BQ_KV4_MAX_PAGE 65536
+
+/* Rows of tokens into their slots. Per group, in binary32: lo and hi the smallest and largest value,
+ *   scale  = type_rne(fl((hi - lo) / 15)),  offset = type_rne(fl(fl(lo + 4 scale) + 4 scale)),
+ *   code   = the integer nearest to fl(fl(x - offset) / scale), ties to even, within [-8, 7];
+ * a scale of 0 has codes 0. A group with a value that is not finite, or with hi - lo past the largest
+ * binary32, has codes 0 and a NaN for scale and offset, so that it reads back as NaN. Bit-exact.
+ *   k, v     [tokens][heads][head_dim] of the cache's type (read): a head's row contiguous and
+ *            16-byte aligned, rows ld_head and tokens ld_token values apart (each its own)
+ *   slots    [tokens] int32, or int64 when slots_are_i64 != 0 (read): a slot outside [0, pages *
+ *            page) is skipped. Each slot at most once: of two tokens for one slot the row keeps
+ *            either's codes and pairs, or some of each.
+ * tokens * heads * head_dim < 2^34. */
+BQ_API bq_status bq_kv4_write(const bq_kv4_cache *cache, const void *k, int64_t k_ld_token, int64_t k_ld_head,
+                              const void *v, int64_t v_ld_token, int64_t v_ld_head, int64_t tokens, const void *slots,
+                              int slots_are_i64, cudaStream_t stream);
+
+/* The rows of slots as 16-bit values: type_rne(fl(code * scale + offset)); zeros for a slot outside the cache.
+ *   slots as above, any slot any number of times (read); k, v as above (written). */
+BQ_API bq_status bq_kv4_read(const bq_kv4_cache *cache, const void *slots, int slots_are_i64, int64_t tokens, void *k,
+                             int64_t k_ld_token, int64_t k_ld_head, void *v, int64_t v_ld_token, int64_t v_ld_head,
+                             cudaStream_t stream);
+
+/* Attention of the last n_q tokens of each sequence over its cache:
+ *   out[b][i][h] = sum over j of softmax_j(scale * <q[b][i][h], key_j>) * value_j
+ * over the positions j of sequence b that query i sees: j <= lengths[b] - n_q + i, and with window > 0 also j >
+ * lengths[b] - n_q + i - window. lengths counts the queries' own tokens, whose rows are in the cache. Query head
+ * h reads key-value head h / (q_heads / heads). A query that sees nothing gives zeros (lse: minus infinity).
+ *   q          [batch][n_q][q_heads][head_dim] of the cache's type (read): rows 16-byte aligned, batches,
+ *              queries and heads q_ld_batch, q_ld_query and q_ld_head values apart
+ *   table      [batch][ld_table] (read): the page of positions [c * page, (c + 1) * page) in column c < width;
+ *              positions of a page outside [0, pages) take part in nothing, and columns past a
+ *              sequence's length or before its window are not looked at
+ *   lengths    [batch] (read), taken as 0 below 0 and as width * page where above
+ *   out        [batch][n_q][q_heads][head_dim], strides as q's (written)
+ *   lse        [batch][n_q][q_heads] FP32 (written): log of the sum of exp(scale * <q, key>); or NULL
+ *   workspace  bq_kv4_workspace_bytes(...) bytes, 16-byte aligned, scratch of this call: its content means
+ *              nothing before and after. Calls that may run at the same time need one each.
+ * scale is finite. q_heads a multiple of heads, at most 65536; n_q * q_heads <= 2^20;
+ * width * page < 2^31 - 2^20; window <= 2^30. Products and sums are binary32 (the tensor cores may truncate where a
+ * binary32 addition would round), the output is rounded once. Made for up to 16 rows, queries times heads
+ * that share a key-value head; the cache is read once for every 16 of them. */
+BQ_API bq_status bq_kv4_attend(const bq_kv4_cache *cache, const void *q, int64_t q_ld_batch, int64_t q_ld_query,
+                               int64_t q_ld_head, int64_t batch, int n_q, int q_heads, const int32_t *table,
+                               int64_t ld_table, int64_t width, const int32_t *lengths, float scale, int64_t window,
+                               void *out, int64_t out_ld_batch, int64_t out_ld_query, int64_t out_ld_head, float *lse,
+                               void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace of bq_kv4_attend for so many queries and query heads over a cache of this
+ * shape (of which heads and head_dim are read); -1 for a shape that it refuses. */
+BQ_API int64_t bq_kv4_workspace_bytes(int heads, int head_dim, int n_q, int q_heads);
+
 /* Number of bounded waits inside codec kernels on the current device that ran out
  * since the previous call of this function there (the first call counts from library
  * load). Kernels that stage their inputs through shared memory (the bulk-copy ring
