@@ -41,8 +41,9 @@ DEBUG_OBJDIR = os.path.join(PKG, "_build_debug")
 DEBUG_FLAGS = ["-DBQ_DEBUG=1"]
 
 SOURCES = ["bq_api.cu", "bq_i8.cu", "bq_mx.cu", "bq_mx_wire.cu", "bq_e4m3.cu", "bq_experts.cu", "bq_w4.cu",
-           "bq_kv4.cu", "bq_attend.cu"]
-HEADERS = ["bq_device.cuh", "bq_launch.h", "bq_chunks.cuh", "bq_rows.cuh", "bq_launch_cache.h", "bq_kv4.cuh"]
+           "bq_kv4.cu", "bq_attend.cu", "bq_attend_bf16.cu", "bq_attend_f16.cu"]
+HEADERS = ["bq_device.cuh", "bq_launch.h", "bq_chunks.cuh", "bq_rows.cuh", "bq_launch_cache.h", "bq_kv4.cuh", "bq_codes.cuh",
+           "bq_attend.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [

@@ -867,7 +867,8 @@ bq_status take_wait_counter(int which, int64_t *count)
     unsigned long long total = 0;
     for (auto read : {bqk::read_wait_counters_i8, bqk::read_wait_counters_mx_wire, bqk::read_wait_counters_mx,
                       bqk::read_wait_counters_e4m3, bqk::read_wait_counters_experts, bqk::read_wait_counters_w4,
-                      bqk::read_wait_counters_kv4, bqk::read_wait_counters_attend}) {
+                      bqk::read_wait_counters_kv4, bqk::read_wait_counters_attend,
+                      bqk::read_wait_counters_attend_bf16, bqk::read_wait_counters_attend_f16}) {
         unsigned long long v[3] = {0, 0, 0};
         if (read(v) != cudaSuccess) return BQ_ERR_CUDA;
         total += v[which];

@@ -1,0 +1,878 @@
+// Attention over a key-value cache in 4 bits: the kernel that streams the cache.
+//
+// Work. The positions of every (sequence, key-value head, chunk of up to kRows query rows) are cut
+// into tiles of 32; all tiles of a call are one run that the CTAs take in equal shares, whatever the
+// sequences' lengths, and a CTA's warps take its tiles in turn, each with a ring of stages of its
+// own that cp.async fills across the borders of the pieces of work. A warp keeps a softmax reference and sums of
+// its own; the warps are joined in shared memory, pieces that several CTAs share through the
+// workspace by the kernel in bq_attend.cu.
+//
+// Products. With u = code + 8 (0 to 15) a key is s u + (z - 8 s), so a score is, per group of columns,
+//     s <q, u> + (z - 8 s) sum q,
+// and an output is  sum_t (p_t s_t) u_t - 8 sum_t (p_t s_t) + sum_t p_t z_t.  Both products run on
+// m16n8k16 mma with FP16 operands and binary32 sums. u needs no conversion: four bits in the low mantissa bits of
+// an FP16 are the subnormal u 2^-24 (u 2^-20 four bits higher), which the tensor cores take exactly, so that a word of
+// eight codes costs five logic instructions. q is scaled by a power of two per row that brings its
+// largest value to 2^14 .. 2^15, which FP16 then holds exactly down to 2^-28 of that. Only p s is rounded, to FP16
+// (2^-11): it is used rounded in the sum over u and in the -8 correction (a mma with a constant matrix), so that
+// u's offset does not enlarge that error. p's reference A takes in the size of s, p = 2^(y - A), A = max y + log2 max s
+// - 13, so that p s stays within 2^15 and is exact to 2^-11 down to 2^-28 of the largest.
+//
+// Fragments. Keys are the n side (a lane's column is a token), values the m side, so that the scores'
+// layout (rows = queries, columns = tokens) is the layout in which the second product takes its p s: nothing
+// moves between lanes. Column 2 i of a score tile of 8 is token i, column 2 i + 1 token i + 4, which
+// makes the four tokens that a lane needs of the values q, q + 4, q + 8, q + 12: their rows lie in different banks.
+#pragma once
+
+#include <cmath>
+#include <type_traits>
+
+#include "bq_codes.cuh"
+#include "bq_kv4.cuh"
+
+namespace bqk {
+
+constexpr int kAttendWarps = 4, kAttendThreads = 32 * kAttendWarps;
+constexpr int kTokens = 32;                       // of a tile
+constexpr float kNothing = -3.0e38f;              // the reference of a row that has seen nothing
+constexpr float kUnit = 0x1p-24f;                 // of a code held as an FP16's lowest mantissa bits
+constexpr float kLift = 13.0f;                    // log2 of the largest p s beside a fresh reference
+constexpr int kMaxAttendCtas = 608;               // four on each of 152 SMs
+
+// What a call's kernels share beside its arguments.
+struct AttendPlan {
+    int rows, share, chunks, items;  // query rows and query heads of a key-value head; items = heads * chunks
+    int ctas;                        // of the launch
+    Divisor by_share, by_page, by_chunks;
+};
+
+// ---------------------------------------------------------------- the run of tiles
+// First position that any query of sequence b looks at, and the end of the sequence.
+__device__ __forceinline__ void sequence_range(const Kv4Cache &c, const Kv4Attend &a, int b, int &begin, int &end)
+{
+    const int cap = a.width * c.page;
+    int length = dbg_ok(a.lengths + b, 4, false) ? __ldg(a.lengths + b) : 0;
+    length = length < 0 ? 0 : length < cap ? length : cap;
+    const int first = length - a.n_q + 1;  // end of the first query
+    begin = a.window > 0 && first > a.window ? first - a.window : 0;
+    end = length;
+}
+// A sequence without positions is one tile too: its rows are written.
+__device__ __forceinline__ int tiles_of(int begin, int end) { return end > begin ? (end - begin - 1) / kTokens + 1 : 1; }
+
+struct Share {
+    int64_t total;  // tiles of all items
+    int ctas;       // that take a share
+    __device__ __forceinline__ int64_t first(int cta) const { return total / ctas * cta + total % ctas * cta / ctas; }
+};
+// Where a tile of the run lies.
+struct Spot {
+    int b, begin, end, tiles;  // sequence, its range and tiles
+    int item;                  // head * chunks + chunk
+    int tile;
+};
+
+// Every CTA finds its share by itself, from the lengths: `spot` is where tile share.first(cta) lies. All threads of
+// the CTA call it.
+__device__ __forceinline__ void find_share(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int cta, Share &share,
+                                           Spot &spot)
+{
+    __shared__ int64_t warp_sum[kAttendWarps];
+    __shared__ Spot found;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int per = (a.batch - 1) / kAttendThreads + 1, b0 = a.batch / per < t ? a.batch : t * per;
+    const int b1 = a.batch - b0 < per ? a.batch : b0 + per;
+    int64_t mine = 0;
+    int begin = 0, end = 0;
+    for (int b = b0; b < b1; b++) {
+        sequence_range(c, a, b, begin, end);
+        mine += tiles_of(begin, end);
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t other = __shfl_up_sync(kFull, upto, d);
+        if (lane >= d) upto += other;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kAttendWarps; w++) {
+        if (w < warp) upto += warp_sum[w];
+        all += warp_sum[w];
+    }
+    share.total = all * plan.items;
+    const int64_t most = (share.total + kAttendWarps - 1) / kAttendWarps;
+    share.ctas = most < plan.ctas ? (int)most : plan.ctas;
+    const int64_t target = share.first(min(cta, share.ctas - 1));
+    int64_t at = upto - mine;  // tiles of one item before sequence b0
+    if (target >= at * plan.items && target < upto * plan.items) {
+        int b = b0;
+        for (;; b++) {
+            sequence_range(c, a, b, begin, end);
+            const int n = tiles_of(begin, end);
+            if (target < (at + n) * plan.items) {
+                const int64_t in = target - at * plan.items;
+                const int item = (int)(in / n);
+                found = Spot{b, begin, end, n, item, (int)(in - (int64_t)item * n)};
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    spot = found;
+}
+
+// The place of a CTA's partial sums: [kRows] references, [kRows] totals, [kRows][kDim] sums. A CTA has at most two pieces
+// that others share: one that began before its share, and one that goes on after it.
+__host__ __device__ __forceinline__ int64_t partial_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
+
+// ---------------------------------------------------------------- constants of a form
+template <int kDim_, int kGroup_, int kRows_>
+struct Form {
+    static constexpr int kDim = kDim_, kGroup = kGroup_, kRows = kRows_, kHalves = kRows / 8;
+    static constexpr int kGroups = kDim / kGroup, kWords = kGroup / 32;  // code words of a lane in a group of keys
+    static constexpr int kChunks = kDim / 32;                            // 16-byte pieces of a row of codes
+    static constexpr int kCodeBytes = kDim == 192 ? 16 * (kTokens * 6 + kTokens) : 16 * kTokens * kChunks;
+    static constexpr int kPairBytes = kTokens * 4 * kGroups;
+    static constexpr int kStage = 2 * (kCodeBytes + kPairBytes);
+    static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
+    // CTAs of an SM by their registers: up to 168 a thread with the sums of 8 rows of up to 128 columns, else up to 255
+    static constexpr int kCtas = kRows == 8 && kDim <= 128 ? 3 : 2;
+    static constexpr int kRoom = (227 * 1024 / kCtas - 1024 - 512 - kJoin) / (kAttendWarps * kStage);
+    static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
+    static constexpr int kSmem = kJoin + kAttendWarps * kStages * kStage;
+    static_assert(kStages >= 2, "a ring has two stages at least");
+};
+
+// 16-byte piece c of token t's row, in a stage: permuted so that the rows that one access reads lie in
+// different banks.
+template <int kDim>
+__host__ __device__ __forceinline__ int chunk_at(int t, int c)
+{
+    if (kDim == 192) return t * 6 + c + 4 * (t >> 2);
+    const int low = t & 3, bit = (t >> 2) & 1;
+    const int key = kDim == 64 ? 5 * bit : kDim == 128 ? (low & 2) ^ (3 * bit) : (2 * low) ^ (5 * bit);
+    return (t * (kDim / 32) + c) ^ key;
+}
+
+// ---------------------------------------------------------------- small steps
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// N code words or pairs at a shared address, in the widest loads that its alignment of 4 N (a power of two's part) allows.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N])
+{
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = lds_v4(at + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        }
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) lds_v2(at + 4 * i, w[i], w[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++) w[i] = lds_u32(at + 4 * i);
+    }
+}
+
+// Four 16-bit halves of codes -> four pairs of u in an FP16's lowest bits, the second and fourth 16 times as large.
+__device__ __forceinline__ void low_bits(uint32_t w, uint32_t (&v)[4])
+{
+    const uint32_t w8 = w >> 8;
+    v[0] = and_xor(w, 0x000f000fu, 0x00080008u);
+    v[1] = and_xor(w, 0x00f000f0u, 0x00800080u);
+    v[2] = and_xor(w8, 0x000f000fu, 0x00080008u);
+    v[3] = and_xor(w8, 0x00f000f0u, 0x00800080u);
+}
+
+// log2 bound of a 16-bit magnitude; not finite counts as nothing.
+template <class T>
+__device__ __forceinline__ int exponent_of(uint32_t bits)
+{
+    return std::is_same<T, __half>::value ? (int)(bits >> 10) - 15 : (int)(bits >> 7) - 127;
+}
+template <class T>
+__device__ __forceinline__ bool finite_bits(uint32_t bits)
+{
+    return bits < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
+}
+
+// ---------------------------------------------------------------- the warps' walk over tiles
+struct Walk {
+    int64_t rest;  // tiles of the CTA's share from this one on
+    Spot at;
+
+    __device__ __forceinline__ void step(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int n)
+    {
+        rest -= n;
+        if (rest <= 0) return;
+        at.tile += n;
+        while (at.tile >= at.tiles) {
+            at.tile -= at.tiles;
+            if (++at.item == plan.items) {
+                at.item = 0;
+                at.b++;
+                sequence_range(c, a, at.b, at.begin, at.end);
+                at.tiles = tiles_of(at.begin, at.end);
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t divide_by(uint32_t n, const Divisor &d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
+
+// A warp's copies: the tile after next is looked up in the table while the tile before it is
+// still on its way, so that no copy waits for its page number.
+template <class T, class F>
+struct Feed {
+    Walk walk;
+    int entry, place, head;
+
+    // a lane's token of the walk's tile
+    __device__ __forceinline__ void look_up(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int lane)
+    {
+        entry = -1;
+        if (walk.rest <= 0) return;
+        head = (int)divide_by(walk.at.item, plan.by_chunks);
+        const int j = walk.at.begin + walk.at.tile * kTokens + lane;
+        const int column = (int)divide_by(j, plan.by_page);
+        place = j - column * c.page;
+        if (j < walk.at.end) {
+            const int32_t *p = a.table + walk.at.b * a.ld_table + column;
+            if (dbg_ok(p, 4, false)) entry = __ldg(p);
+        }
+    }
+
+    __device__ __forceinline__ void issue(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int lane, uint32_t stage,
+                                          uint32_t *valid)
+    {
+        if (walk.rest > 0) {
+            const bool ok = entry >= 0 && entry < c.pages;
+            const uint32_t there = __ballot_sync(kFull, ok);
+            if (lane == 0) *valid = there;
+            const int64_t page = ok ? entry : 0;
+            const int64_t at = ok ? page * c.page_stride + head * c.head_stride + (int64_t)place * c.token_stride : 0;
+            const int64_t at_s = ok ? page * c.page_stride_s + head * c.head_stride_s + (int64_t)place * c.token_stride_s : 0;
+#pragma unroll
+            for (int i = 0; i < F::kChunks; i++) {
+                const int piece = 32 * i + lane, t = piece / F::kChunks, ch = piece % F::kChunks;
+                const int64_t from = __shfl_sync(kFull, at, t) + 16 * ch;
+                const int bytes = (there >> t) & 1 ? 16 : 0;
+                const uint32_t to = stage + 16 * chunk_at<F::kDim>(t, ch);
+                lane_copy_part<16>(to, c.k + from, bytes);
+                lane_copy_part<16>(to + F::kCodeBytes, c.v + from, bytes);
+            }
+            constexpr int kSize = F::kGroups % 4 == 0 ? 16 : F::kGroups % 2 == 0 ? 8 : 4;
+            const uint32_t to = stage + 2 * F::kCodeBytes + 4 * F::kGroups * lane;
+#pragma unroll
+            for (int i = 0; i < 4 * F::kGroups; i += kSize) {
+                lane_copy_part<kSize>(to + i, c.k_scales + at_s + i, ok ? kSize : 0);
+                lane_copy_part<kSize>(to + F::kPairBytes + i, c.v_scales + at_s + i, ok ? kSize : 0);
+            }
+            walk.step(c, a, plan, kAttendWarps);
+            look_up(c, a, plan, lane);
+        }
+        lane_copy_commit();
+    }
+};
+
+// ---------------------------------------------------------------- one piece of work of a warp
+// Lane 4 r + q. Scores: rows r and r + 8 (halves 0 and 1), of a tile of 8 tokens the tokens q and q + 4. Sums of the
+// output: columns of lane part r, rows 2 q and 2 q + 1 of a half.
+template <class T, class F>
+struct Rows {
+    uint32_t qf[F::kGroups][F::kWords][2][2 * F::kHalves];  // queries as mma fragments
+    float qsum[F::kHalves][F::kGroups];                     // kUnit times the sum of a group's scaled queries
+    float f[F::kHalves];                                    // from a score in units to its log2
+    float ref[F::kHalves];                                  // A
+    float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
+    float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
+    float eights[(F::kGroups + 1) / 2][F::kHalves][4];      // of 8 p s, in units: a group in c0 c1, the next in c2 c3
+
+    __device__ __forceinline__ void start(const Kv4Attend &a, const AttendPlan &plan, int b, int head, int row0, int lane)
+    {
+        const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) {
+            const int row = row0 + r + 8 * h;
+            uint4 raw[F::kGroups][F::kWords];
+            const int i = (int)divide_by(row < plan.rows ? row : 0, plan.by_share), in = (row < plan.rows ? row : 0) - i * plan.share;
+            const T *from = static_cast<const T *>(a.q) + b * a.q_batch + i * a.q_query +
+                            (int64_t)(head * plan.share + in) * a.q_head + q * (F::kGroup / 4);
+            uint32_t top = 0;
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++)
+#pragma unroll
+                for (int w = 0; w < F::kWords; w++) {
+                    uint4 &x = raw[g][w];
+                    x = row < plan.rows ? ld_keep_v4(from + g * F::kGroup + 8 * w) : make_uint4(0, 0, 0, 0);
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                 __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                }
+            top = max(top & 0xffffu, top >> 16);
+            top = max(top, __shfl_xor_sync(kFull, top, 1));
+            top = max(top, __shfl_xor_sync(kFull, top, 2));
+            const int e = max(exponent_of<T>(top), -100);  // the largest value is below 2^(e + 1)
+            const float by = copysignf(power_of_2(14 - e), a.scale), by16 = 0.0625f * by;
+            const int half = (e + 10) / 2;
+            f[h] = fminf(__fmul_rn(__fmul_rn(__fmul_rn(fabsf(a.scale), 1.4426950408889634f), power_of_2(half)),
+                                   power_of_2(e + 10 - half)), 3.0e38f);
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++) {
+                float total_q = 0.0f;
+#pragma unroll
+                for (int w = 0; w < F::kWords; w++) {
+                    const uint32_t u[4] = {raw[g][w].x, raw[g][w].y, raw[g][w].z, raw[g][w].w};
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        v[k] = Value<T>::widen((uint16_t)(k & 1 ? u[k / 2] >> 16 : u[k / 2] & 0xffffu));
+                        total_q = __fmaf_rn(v[k], by * kUnit, total_q);
+                    }
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        qf[g][w][m][h] = pack_f16(__fmul_rn(v[2 * m], by), __fmul_rn(v[2 * m + 4], by));
+                        qf[g][w][m][F::kHalves + h] = pack_f16(__fmul_rn(v[2 * m + 1], by16), __fmul_rn(v[2 * m + 5], by16));
+                    }
+                }
+                total_q = __fadd_rn(total_q, __shfl_xor_sync(kFull, total_q, 1));
+                qsum[h][g] = __fadd_rn(total_q, __shfl_xor_sync(kFull, total_q, 2));
+                off[h][g] = splat(0.0f);
+            }
+            ref[h] = kNothing;
+            total[h] = splat(0.0f);
+#pragma unroll
+            for (int m = 0; m < F::kDim / 16; m++)
+#pragma unroll
+                for (int k = 0; k < 4; k++) sum[m][h][k] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < (F::kGroups + 1) / 2; g++)
+#pragma unroll
+                for (int k = 0; k < 4; k++) eights[g][h][k] = 0.0f;
+        }
+    }
+
+    // x in units of tokens 8 n + q and 8 n + q + 4
+    __device__ __forceinline__ void scores(uint32_t stage, int lane, float2 (&x)[4][F::kHalves])
+    {
+        const int r = lane >> 2, q = lane & 3, t0 = (r >> 1) + 4 * (r & 1);
+        const uint32_t pairs = stage + 2 * F::kCodeBytes + 4 * F::kGroups * q;
+#pragma unroll
+        for (int n = 0; n < 4; n++) {
+            uint32_t pa[F::kGroups], pb[F::kGroups];
+            lds_words<F::kGroups>(pairs + 4 * F::kGroups * 8 * n, pa);
+            lds_words<F::kGroups>(pairs + 4 * F::kGroups * (8 * n + 4), pb);
+#pragma unroll
+            for (int h = 0; h < F::kHalves; h++) x[n][h] = splat(0.0f);
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++) {
+                // the lane's words: kWords * q and on, of the group's 4 kWords
+                uint32_t w[F::kWords];
+                const int piece = g * F::kWords + (F::kWords * q) / 4, in = (F::kWords * q) % 4;
+                lds_words<F::kWords>(stage + 16 * chunk_at<F::kDim>(t0 + 8 * n, piece) + 4 * in, w);
+                float c[4];
+#pragma unroll
+                for (int i = 0; i < F::kWords; i++) {
+                    uint32_t u[4];
+                    low_bits(w[i], u);
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        const uint32_t *a = qf[g][i][m];
+                        constexpr int kLast = F::kHalves - 1;
+                        const uint32_t a1 = kLast ? a[kLast] : 0u, a3 = kLast ? a[F::kHalves + kLast] : 0u;
+                        if (i == 0 && m == 0)
+                            mma_f16<true>(c, a[0], a1, a[F::kHalves], a3, u[0], u[1]);
+                        else
+                            mma_f16<false>(c, a[0], a1, a[F::kHalves], a3, u[2 * m], u[2 * m + 1]);
+                    }
+                }
+                const float2 one = pair_values<T>(pa[g]), two = pair_values<T>(pb[g]);
+                const float2 s = make_float2(one.x, two.x), z = fma2(s, splat(-8.0f), make_float2(one.y, two.y));
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    x[n][h] = fma2(s, make_float2(c[2 * h], c[2 * h + 1]), x[n][h]);
+                    x[n][h] = fma2(z, splat(qsum[h][g]), x[n][h]);
+                }
+            }
+        }
+    }
+
+    // A tile's values join the sums. seen: a bit a token for each half's row; kMasked is false where all are set.
+    template <bool kMasked>
+    __device__ __forceinline__ void take(uint32_t stage, int lane, float2 (&x)[4][F::kHalves], const uint32_t (&seen)[F::kHalves])
+    {
+        const int r = lane >> 2, q = lane & 3;
+        const uint32_t pairs = stage + 2 * F::kCodeBytes + F::kPairBytes;
+        // log2 of the largest scale of the tile's values; offsets count 2^-24, so that sums of p z stay in range
+        int k;
+        {
+            uint32_t w[F::kGroups];
+            lds_words<F::kGroups>(pairs + 4 * F::kGroups * lane, w);
+            k = -60;
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++) {
+                const uint32_t s = w[g] & 0x7fffu, z = (w[g] >> 16) & 0x7fffu;
+                if (finite_bits<T>(s)) k = max(k, exponent_of<T>(s) + 1);
+                if (finite_bits<T>(z)) k = max(k, exponent_of<T>(z) - 23);
+            }
+            k = __reduce_max_sync(kFull, k);
+        }
+        bool grown = false;
+        float now[F::kHalves];
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 4; n++) {
+                const float lo = !kMasked || ((seen[h] >> (8 * n + q)) & 1) ? x[n][h].x : -INFINITY;
+                const float hi = !kMasked || ((seen[h] >> (8 * n + q + 4)) & 1) ? x[n][h].y : -INFINITY;
+                top = fmaxf(top, fmaxf(lo, hi));
+            }
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            now[h] = top > -INFINITY ? __fadd_rn(__fmul_rn(top, f[h]), (float)k - kLift) : -INFINITY;
+            grown |= now[h] > __fadd_rn(ref[h], 1.0f);
+        }
+        if (__any_sync(kFull, grown)) {
+#pragma unroll
+            for (int h = 0; h < F::kHalves; h++) {
+                const float next = fmaxf(ref[h], now[h]), keep = exp2_fast(__fsub_rn(ref[h], next));
+                ref[h] = next;
+                total[h] = mul2(total[h], splat(keep));
+#pragma unroll
+                for (int g = 0; g < F::kGroups; g++) off[h][g] = mul2(off[h][g], splat(keep));
+                const float even = __shfl_sync(kFull, keep, 8 * q), odd = __shfl_sync(kFull, keep, 8 * q + 4);
+#pragma unroll
+                for (int m = 0; m < F::kDim / 16; m++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? odd : even);
+#pragma unroll
+                for (int g = 0; g < (F::kGroups + 1) / 2; g++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? odd : even);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; n++)
+#pragma unroll
+            for (int h = 0; h < F::kHalves; h++) {
+                const float2 y = fma2(x[n][h], splat(f[h]), splat(-ref[h]));
+                float2 &p = x[n][h];
+                p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                if (kMasked) {
+                    if (!((seen[h] >> (8 * n + q)) & 1)) p.x = 0.0f;
+                    if (!((seen[h] >> (8 * n + q + 4)) & 1)) p.y = 0.0f;
+                }
+                total[h] = add2(total[h], p);
+            }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            uint32_t pw[4][F::kGroups];
+#pragma unroll
+            for (int j = 0; j < 4; j++) lds_words<F::kGroups>(pairs + 4 * F::kGroups * (16 * i + 4 * j + q), pw[j]);
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++) {
+                uint32_t b[F::kHalves][2];
+#pragma unroll
+                for (int n = 0; n < 2; n++) {
+                    const float2 one = pair_values<T>(pw[2 * n][g]), two = pair_values<T>(pw[2 * n + 1][g]);
+                    const float2 s = make_float2(one.x, two.x), z = make_float2(one.y, two.y);
+#pragma unroll
+                    for (int h = 0; h < F::kHalves; h++) {
+                        const float2 p = x[2 * i + n][h];
+                        float2 sh = s, zh = z;
+                        if (kMasked) {  // a row that does not see a token takes nothing of it, a NaN neither
+                            if (!((seen[h] >> (16 * i + 8 * n + q)) & 1)) sh.x = zh.x = 0.0f;
+                            if (!((seen[h] >> (16 * i + 8 * n + q + 4)) & 1)) sh.y = zh.y = 0.0f;
+                        }
+                        const float2 ps = mul2(p, sh);
+                        b[h][n] = pack_f16(ps.x, ps.y);
+                        off[h][g] = fma2(p, zh, off[h][g]);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    constexpr uint32_t kEight = 0x00080008u;
+                    if (g & 1)
+                        mma_f16<false>(eights[g / 2][h], 0u, kEight, 0u, kEight, b[h][0], b[h][1]);
+                    else
+                        mma_f16<false>(eights[g / 2][h], kEight, 0u, kEight, 0u, b[h][0], b[h][1]);
+                }
+                values(stage + F::kCodeBytes, r, q, i, g, b);
+            }
+        }
+    }
+
+    // The codes of 16 tokens in group g against b.
+    __device__ __forceinline__ void values(uint32_t codes, int r, int q, int i, int g, const uint32_t (&b)[F::kHalves][2])
+    {
+        constexpr int kLaneWords = F::kGroup >= 64 ? F::kGroup / 64 : 1;
+        uint32_t w[4][kLaneWords];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            // groups of 32 columns have four words: lanes r and r + 4 share one, half a word each
+            const int word = F::kGroup >= 64 ? kLaneWords * r : r & 3;
+            const int piece = g * F::kWords + word / 4;
+            lds_words<kLaneWords>(codes + 16 * chunk_at<F::kDim>(16 * i + 4 * j + q, piece) + 4 * (word % 4), w[j]);
+        }
+#pragma unroll
+        for (int k = 0; k < kLaneWords; k++) {
+#pragma unroll
+            for (int half = 0; half < (F::kGroup >= 64 ? 2 : 1); half++) {
+                const uint32_t pick = F::kGroup >= 64 ? (half ? 0x7632u : 0x5410u) : (r & 4 ? 0x7632u : 0x5410u);
+                uint32_t lo[4], hi[4];
+                low_bits(__byte_perm(w[0][k], w[1][k], pick), lo);
+                low_bits(__byte_perm(w[2][k], w[3][k], pick), hi);
+#pragma unroll
+                for (int odd = 0; odd < 2; odd++) {
+                    const int m = F::kGroup >= 64 ? (g * kLaneWords + k) * 4 + 2 * half + odd : 2 * g + odd;
+#pragma unroll
+                    for (int h = 0; h < F::kHalves; h++)
+                        mma_f16<false>(sum[m][h], lo[odd], lo[2 + odd], hi[odd], hi[2 + odd], b[h][0], b[h][1]);
+                }
+            }
+        }
+    }
+
+    // Sums of quads brought together: total in every lane of a row's quad, sum the true sums of p v.
+    __device__ __forceinline__ void finish(int lane)
+    {
+        const int q = lane & 3;
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) {
+            float t = __fadd_rn(total[h].x, total[h].y);
+            t = __fadd_rn(t, __shfl_xor_sync(kFull, t, 1));
+            total[h].x = __fadd_rn(t, __shfl_xor_sync(kFull, t, 2));
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++) {
+                float z = __fadd_rn(off[h][g].x, off[h][g].y);
+                z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 1));
+                z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 2));
+                const float even = __shfl_sync(kFull, z, 8 * q), odd = __shfl_sync(kFull, z, 8 * q + 4);
+#pragma unroll
+                for (int k = 0; k < F::kGroup / 16; k++) {
+                    float(&v)[4] = sum[g * (F::kGroup / 16) + k][h];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float u = k & 1 ? __fmul_rn(v[i], 0.0625f) : v[i];
+                        const float c = eights[g / 2][h][2 * (g & 1) + (i & 1)];
+                        v[i] = __fmaf_rn(__fsub_rn(u, c), 1.0f / kUnit, i & 1 ? odd : even);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------- the kernel
+template <int N>
+__device__ __forceinline__ void store_floats(float *p, const float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        st_v4(p + i, make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                                __float_as_uint(v[i + 3])));
+}
+
+// Where an item's row goes.
+__device__ __forceinline__ int64_t out_row(const Kv4Attend &a, const AttendPlan &plan, int b, int head, int row, int64_t *lse)
+{
+    const int i = (int)divide_by(row, plan.by_share), h = head * plan.share + row - i * plan.share;
+    *lse = ((int64_t)b * a.n_q + i) * a.q_heads + h;
+    return b * a.out_batch + i * a.out_query + h * a.out_head;
+}
+
+__device__ __forceinline__ float lse_of(float ref, float total)
+{
+    return total == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(ref, log2f(total)), 0.6931471805599453f);
+}
+
+__device__ __forceinline__ void dbg_attend(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int64_t floats)
+{
+    dbg_begin();
+    dbg_cache(c, false);
+    dbg_allow(a.q, 2 * ((a.batch - 1) * a.q_batch + (a.n_q - 1) * a.q_query + (a.q_heads - 1) * a.q_head + c.head_dim), false);
+    dbg_allow(a.out, 2 * ((a.batch - 1) * a.out_batch + (a.n_q - 1) * a.out_query + (a.q_heads - 1) * a.out_head + c.head_dim),
+              true);
+    dbg_allow(a.table, a.width ? 4 * ((a.batch - 1) * a.ld_table + a.width) : 0, false);
+    dbg_allow(a.lengths, 4ll * a.batch, false);
+    dbg_allow(a.lse, a.lse ? 4ll * a.batch * a.n_q * a.q_heads : 0, true);
+    dbg_allow(a.workspace, 4 * 2 * plan.ctas * floats, true);
+    dbg_ready();
+}
+
+// A warp's sums beside those of another warp in shared memory: [kRows] references, [kRows] totals, [kRows][kDim].
+template <class T, class F>
+struct Join {
+    static constexpr int kRun = F::kGroup >= 64 ? 8 : 4;  // consecutive columns of a lane
+    // first column of run k of a lane's, k < kDim / 8 / kRun
+    static __device__ __forceinline__ int column(int r, int k)
+    {
+        if (F::kGroup == 32) return 32 * k + 8 * (r & 3) + 4 * (r >> 2);
+        constexpr int kLaneWords = F::kGroup >= 64 ? F::kGroup / 64 : 1;
+        return k / kLaneWords * F::kGroup + 8 * (kLaneWords * r + k % kLaneWords);
+    }
+    // run k's values of row 2 q + odd of half h, in order
+    static __device__ __forceinline__ void run_of(const Rows<T, F> &x, int k, int h, int odd, float (&v)[kRun])
+    {
+#pragma unroll
+        for (int i = 0; i < kRun; i++) {
+            // column i of a run: from m tile of its half word and parity, rows r (first of two) or r + 8
+            const int m = k * (kRun / 2) + 2 * (i / 4) + (i & 1);
+            v[i] = x.sum[m][h][2 * ((i >> 1) & 1) + odd];
+        }
+    }
+    static __device__ __forceinline__ void put(const Rows<T, F> &x, float *to, int lane)
+    {
+        const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) {
+            if (q == 0) to[8 * h + r] = x.ref[h], to[F::kRows + 8 * h + r] = x.total[h].x;
+#pragma unroll
+            for (int odd = 0; odd < 2; odd++)
+#pragma unroll
+                for (int k = 0; k < F::kDim / 8 / kRun; k++) {
+                    float v[kRun];
+                    run_of(x, k, h, odd, v);
+                    float *p = to + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + column(r, k);
+#pragma unroll
+                    for (int i = 0; i < kRun; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+        }
+    }
+    static __device__ __forceinline__ void add(Rows<T, F> &x, const float *from, int lane)
+    {
+        const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) {
+            const float other = from[8 * h + r], next = fmaxf(x.ref[h], other);
+            const float mine = exp2_fast(__fsub_rn(x.ref[h], next)), theirs = exp2_fast(__fsub_rn(other, next));
+            x.ref[h] = next;
+            x.total[h].x = __fmaf_rn(from[F::kRows + 8 * h + r], theirs, __fmul_rn(x.total[h].x, mine));
+#pragma unroll
+            for (int odd = 0; odd < 2; odd++) {
+                const float m = __shfl_sync(kFull, mine, 8 * q + 4 * odd), t = __shfl_sync(kFull, theirs, 8 * q + 4 * odd);
+#pragma unroll
+                for (int k = 0; k < F::kDim / 8 / kRun; k++) {
+                    const float *p = from + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + column(r, k);
+#pragma unroll
+                    for (int i = 0; i < kRun; i += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(p + i);
+                        const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            float &s = x.sum[k * (kRun / 2) + 2 * (i / 4) + (j & 1)][h][2 * (j >> 1) + odd];
+                            s = __fmaf_rn(w[j], t, __fmul_rn(s, m));
+                        }
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <class T, class F>
+__global__ void __launch_bounds__(kAttendThreads, F::kCtas)
+    attend_kernel(const __grid_constant__ Kv4Cache c, const __grid_constant__ Kv4Attend a, const __grid_constant__ AttendPlan plan)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ uint32_t valid[kAttendWarps][F::kStages];
+    using J = Join<T, F>;
+    constexpr int64_t kPartial = (int64_t)F::kRows * (F::kDim + 2);
+    pdl_begin();
+    dbg_attend(c, a, plan, kPartial);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Share share;
+    Spot now;
+    find_share(c, a, plan, blockIdx.x, share, now);
+    if ((int)blockIdx.x >= share.ctas) return;
+    const int64_t tiles = share.first(blockIdx.x + 1) - share.first(blockIdx.x);
+
+    float *const joins = reinterpret_cast<float *>(smem);
+    const uint32_t ring = smem_u32(smem) + F::kJoin + warp * F::kStages * F::kStage;
+    Feed<T, F> feed;
+    feed.walk = Walk{tiles, now};
+    feed.walk.step(c, a, plan, warp);
+    feed.look_up(c, a, plan, lane);
+#pragma unroll
+    for (int s = 0; s < F::kStages - 1; s++) feed.issue(c, a, plan, lane, ring + s * F::kStage, &valid[warp][s]);
+
+    Rows<T, F> x;
+    int slot = 0;
+    for (int64_t done = 0; done < tiles;) {
+        const int64_t left = tiles - done;
+        const int last = left < now.tiles - now.tile ? now.tile + (int)left : now.tiles;  // of the item in this share
+        const int head = (int)divide_by(now.item, plan.by_chunks), row0 = (now.item - head * plan.chunks) * F::kRows;
+        x.start(a, plan, now.b, head, row0, lane);
+        // the positions that the lane's rows see, and that all rows of the item do
+        int lo[F::kHalves], hi[F::kHalves];
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) {
+            const int row = min(row0 + (lane >> 2) + 8 * h, plan.rows - 1);
+            hi[h] = now.end - a.n_q + 1 + (int)divide_by(row, plan.by_share);
+            lo[h] = a.window > 0 && hi[h] > a.window ? hi[h] - a.window : 0;
+        }
+        const int all_hi = now.end - a.n_q + 1 + (int)divide_by(row0, plan.by_share);
+        const int last_hi = now.end - a.n_q + 1 + (int)divide_by(min(row0 + F::kRows, plan.rows) - 1, plan.by_share);
+        const int all_lo = a.window > 0 && last_hi > a.window ? last_hi - a.window : 0;
+        for (int t = now.tile + ((warp - (int)done) & (kAttendWarps - 1)); t < last; t += kAttendWarps) {
+            lane_copy_wait<F::kStages - 2>();
+            __syncwarp();
+            const uint32_t stage = ring + slot * F::kStage, there = valid[warp][slot];
+            const int fill = slot == 0 ? F::kStages - 1 : slot - 1;
+            feed.issue(c, a, plan, lane, ring + fill * F::kStage, &valid[warp][fill]);
+            if (++slot == F::kStages) slot = 0;
+            const int at = now.begin + t * kTokens;
+            float2 s[4][F::kHalves];
+            x.scores(stage, lane, s);
+            uint32_t seen[F::kHalves];
+            if (there == kFull && at >= all_lo && at + kTokens <= all_hi) {
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) seen[h] = kFull;
+                x.template take<false>(stage, lane, s, seen);
+            } else {
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    const int from = max(lo[h] - at, 0), to = min(hi[h] - at, kTokens);
+                    const uint32_t above = from < kTokens ? kFull << from : 0u, below = to <= 0 ? 0u : kFull >> (kTokens - to);
+                    seen[h] = there & above & below;
+                }
+                x.template take<true>(stage, lane, s, seen);
+            }
+        }
+        x.finish(lane);
+        // warps 2 and 3 to 0 and 1, then 1 to 0; the last step's place is read by warp 0 before the next item's first
+        // barrier, and the first step's before this item's second
+        if (warp >= 2) J::put(x, joins + (warp - 2) * kPartial, lane);
+        __syncthreads();
+        if (warp < 2) J::add(x, joins + warp * kPartial, lane);
+        if (warp == 1) J::put(x, joins + 2 * kPartial, lane);
+        __syncthreads();
+        if (warp == 0) {
+            J::add(x, joins + 2 * kPartial, lane);
+            const int r = lane >> 2, q = lane & 3;
+            if (now.tile == 0 && last == now.tiles) {
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    const float inv = x.total[h].x == 0.0f ? 0.0f : __fdiv_rn(1.0f, x.total[h].x);
+                    if (q == 0 && a.lse && row0 + 8 * h + r < plan.rows) {
+                        int64_t at;
+                        out_row(a, plan, now.b, head, row0 + 8 * h + r, &at);
+                        if (dbg_ok(a.lse + at, 4, true)) a.lse[at] = lse_of(x.ref[h], x.total[h].x);
+                    }
+#pragma unroll
+                    for (int odd = 0; odd < 2; odd++) {
+                        const int row = row0 + 8 * h + 2 * q + odd;
+                        const float by = __shfl_sync(kFull, inv, 8 * q + 4 * odd);
+                        int64_t unused;
+                        if (row < plan.rows) {
+                            T *to = static_cast<T *>(a.out) + out_row(a, plan, now.b, head, row, &unused);
+#pragma unroll
+                            for (int k = 0; k < F::kDim / 8 / J::kRun; k++) {
+                                float v[J::kRun];
+                                J::run_of(x, k, h, odd, v);
+                                uint32_t w[J::kRun / 2];
+#pragma unroll
+                                for (int i = 0; i < J::kRun / 2; i++)
+                                    w[i] = Value<T>::round2(__fmul_rn(v[2 * i], by), __fmul_rn(v[2 * i + 1], by));
+                                if constexpr (J::kRun == 8)
+                                    st_v4(to + J::column(r, k), make_uint4(w[0], w[1], w[2], w[3]));
+                                else
+                                    st_v2(to + J::column(r, k), make_uint2(w[0], w[1]));
+                            }
+                        }
+                    }
+                }
+            } else {
+                float *const to = a.workspace + (2 * (int64_t)blockIdx.x + (now.tile == 0)) * kPartial;
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    if (q == 0 && dbg_ok(to + 8 * h + r, 4, true)) to[8 * h + r] = x.ref[h];
+                    if (q == 0 && dbg_ok(to + F::kRows + 8 * h + r, 4, true)) to[F::kRows + 8 * h + r] = x.total[h].x;
+#pragma unroll
+                    for (int odd = 0; odd < 2; odd++)
+#pragma unroll
+                        for (int k = 0; k < F::kDim / 8 / J::kRun; k++) {
+                            float v[J::kRun];
+                            J::run_of(x, k, h, odd, v);
+                            store_floats(to + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + J::column(r, k), v);
+                        }
+                }
+            }
+        }
+        done += last - now.tile;
+        now.tile = 0;
+        if (done < tiles && ++now.item == plan.items) {
+            now.item = 0;
+            now.b++;
+            sequence_range(c, a, now.b, now.begin, now.end);
+            now.tiles = tiles_of(now.begin, now.end);
+        }
+    }
+    lane_copy_wait<0>();
+}
+
+// ---------------------------------------------------------------- launch
+template <class T, class F>
+cudaError_t launch_form(const Kv4Cache &c, const Kv4Attend &a, AttendPlan &plan, cudaStream_t st)
+{
+    void (*kernel)(Kv4Cache, Kv4Attend, AttendPlan) = attend_kernel<T, F>;
+    plan.chunks = (plan.rows + F::kRows - 1) / F::kRows;
+    plan.items = c.heads * plan.chunks;
+    plan.by_chunks = divisor((uint32_t)plan.chunks);
+    // enough CTAs for any lengths: a share of one tile a warp at least
+    const int64_t longest = ((int64_t)a.width * c.page + kTokens) / kTokens;
+    const int64_t tiles = (int64_t)(a.batch < 4096 ? a.batch : 4096) * plan.items * longest;
+    if (cudaError_t e = grid_for((const void *)kernel, tiles, &plan.ctas, F::kSmem, kAttendThreads)) return e;
+    if (plan.ctas > kMaxAttendCtas) plan.ctas = kMaxAttendCtas;
+    return launch_kernel_block(kernel, plan.ctas, kAttendThreads, F::kSmem, st, c, a, plan);
+}
+
+// Rows of a form: what fits the registers.
+__host__ __device__ inline int form_rows(int rows, int dim) { return rows > 8 && dim <= 128 ? 16 : 8; }
+
+template <class T>
+cudaError_t launch_attend(const Kv4Cache &c, const Kv4Attend &a, AttendPlan &plan, cudaStream_t st)
+{
+    const bool wide = form_rows(plan.rows, c.head_dim) == 16;
+#define BQ_FORM(D, G) \
+    if (c.head_dim == D && c.group == G) return launch_form<T, Form<D, G, 8>>(c, a, plan, st);
+#define BQ_FORMS(D, G)                                                                       \
+    if (c.head_dim == D && c.group == G)                                                     \
+        return wide ? launch_form<T, Form<D, G, 16>>(c, a, plan, st) : launch_form<T, Form<D, G, 8>>(c, a, plan, st);
+    BQ_FORMS(64, 32)
+    BQ_FORMS(64, 64)
+    BQ_FORMS(128, 32)
+    BQ_FORMS(128, 64)
+    BQ_FORMS(128, 128)
+    BQ_FORM(192, 32)
+    BQ_FORM(192, 64)
+    BQ_FORM(256, 32)
+    BQ_FORM(256, 64)
+    BQ_FORM(256, 128)
+#undef BQ_FORM
+#undef BQ_FORMS
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_attend_bf16(const Kv4Cache &c, const Kv4Attend &a, AttendPlan &plan, cudaStream_t st);
+cudaError_t launch_attend_f16(const Kv4Cache &c, const Kv4Attend &a, AttendPlan &plan, cudaStream_t st);
+
+}  // namespace bqk

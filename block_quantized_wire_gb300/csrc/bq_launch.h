@@ -225,6 +225,8 @@ cudaError_t read_wait_counters_experts(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_w4(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_kv4(unsigned long long (&v)[3]);
 cudaError_t read_wait_counters_attend(unsigned long long (&v)[3]);
+cudaError_t read_wait_counters_attend_bf16(unsigned long long (&v)[3]);
+cudaError_t read_wait_counters_attend_f16(unsigned long long (&v)[3]);
 cudaError_t launch_wait_selftest(cudaStream_t st);
 // Debug build: one listed 256-byte range of buf and one load at byte 512 (declined).
 cudaError_t launch_index_selftest(void *buf, cudaStream_t st);

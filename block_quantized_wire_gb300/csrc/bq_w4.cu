@@ -23,7 +23,7 @@
 // the next, shifts as high products (slower: four cycles each), x shared by a ring of its own.
 #include <climits>
 
-#include "bq_rows.cuh"
+#include "bq_codes.cuh"
 
 namespace bqk {
 namespace {
@@ -43,14 +43,6 @@ constexpr int kW4Stages = 3;  // steps of a warp's ring
 // Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale Production", 2022.)
 template <class T>
 struct Codes;
-
-// (w & mask) ^ x in one instruction
-__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t mask, uint32_t x)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(w), "r"(mask), "r"(x));
-    return r;
-}
 
 // BF16 codes come out times 2^-12, so that no group's binary32 sum overflows where its
 // product with the scale would not (128 codes of 8 times the largest BF16 value are 2^138);
@@ -103,53 +95,9 @@ struct Codes<__half> {
     template <bool kFirst>
     static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t *a, uint32_t b0, uint32_t b1)
     {
-        if constexpr (kFirst)
-            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                "{%8, %9}, {%10, %10, %10, %10};"
-                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-        else
-            asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-                "{%8, %9}, {%0, %1, %2, %3};"
-                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        mma_f16<kFirst>(c, a[0], a[1], a[2], a[3], b0, b1);
     }
 };
-
-// ---------------------------------------------------------------- shared memory
-__device__ __forceinline__ uint32_t lds_u32(uint32_t a)
-{
-    uint32_t r;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
-    return r;
-}
-
-__device__ __forceinline__ uint4 lds_v4(uint32_t a)
-{
-    uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "r"(a)
-                 : "memory");
-    return r;
-}
-
-__device__ __forceinline__ void lds_v2(uint32_t a, uint32_t &x, uint32_t &y)
-{
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a) : "memory");
-}
-
-// Copies `bytes` of kSize bytes and fills the rest with zeros.
-template <int kSize>
-__device__ __forceinline__ void lane_copy_part(uint32_t dst, const void *src, int bytes)
-{
-    if (bytes > 0 && !dbg_ok(src, bytes, false)) bytes = 0;
-    if constexpr (kSize == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kSize), "r"(bytes)
-                     : "memory");
-}
 
 // Bytes into a warp's stage at which the 16 bytes (32 codes) c of weight row r lie. The
 // 16-byte pieces of a 128-byte line (one row of 256 columns or two of 128) are permuted by
