@@ -5,52 +5,81 @@
 namespace bqk {
 namespace {
 
-// A warp a row: CTA c of a group of four rows joins the item that goes on from share c to the next, if it began there.
-template <class T, int kDim>
-__global__ void __launch_bounds__(kAttendThreads) attend_join_kernel(const __grid_constant__ Kv4Cache c,
-                                                                    const __grid_constant__ Kv4Attend a,
-                                                                    const __grid_constant__ AttendPlan plan, int form, int groups)
+__device__ __forceinline__ uint4 ld_plain_v4(const float *p)
 {
-    constexpr int kPer = kDim / 32;  // columns of a lane
-    const int64_t partial = partial_floats(form, kDim);
+    if (!dbg_ok(p, 16, false)) return make_uint4(0, 0, 0, 0);
+    return *reinterpret_cast<const uint4 *>(p);
+}
+
+// A CTA four rows of an item that goes on after share blockIdx.x / groups, if there is one. A thread takes four columns of one
+// row, of every kGroups-th part.
+constexpr int kJoinRows = 4, kJoinThreads = 512;
+
+template <class T, int kDim>
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ Kv4Cache c,
+                                                                  const __grid_constant__ Kv4Attend a,
+                                                                  const __grid_constant__ AttendPlan plan, int form, int groups)
+{
+    constexpr int kGroups = kJoinThreads / kDim;
+    __shared__ float weight[kJoinRows][kMaxAttendCtas + 1], refs[kJoinRows], totals[kJoinRows];
+    __shared__ float4 sums[kGroups][kDim];
+    const int64_t floats = partial_floats(form, kDim);
     pdl_begin();
-    dbg_attend(c, a, plan, partial);
-    const int cta = blockIdx.x / groups, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Share share;
-    Spot at;
-    find_share(c, a, plan, cta + 1, share, at);
-    if (cta + 1 >= share.ctas || at.tile == 0) return;
-    const int64_t begin = share.first(cta + 1) - at.tile, end = begin + at.tiles;
-    if (begin < share.first(cta)) return;
-    const int head = (int)divide_by(at.item, plan.by_chunks), row = (blockIdx.x - cta * groups) * kAttendWarps + warp;
-    const int item_row = (at.item - head * plan.chunks) * form + row;
-    if (row >= form || item_row >= plan.rows) return;
-    int last = cta + 1;  // past the last share with a part of the item
-    while (last < share.ctas && share.first(last) < end) last++;
+    dbg_attend(c, a, plan, floats);
+    const int cta = blockIdx.x / groups, row0 = (blockIdx.x - cta * groups) * kJoinRows;
+    const uint4 word = ld_plain_v4(a.workspace + 4 * cta);
+    const Split at = {(int)word.x, (int)word.y, (int)word.z, 0};
+    const int head = (int)divide_by(at.item, plan.by_chunks), first = (at.item - head * plan.chunks) * form + row0;
+    const int rows = min(min(form - row0, plan.rows - first), kJoinRows);
+    if (at.parts == 0 || rows <= 0) return;
     // share `cta` left it as what goes on after it, the others as what began before them
-    const auto part = [&](int i) { return a.workspace + (2 * (int64_t)i + (i == cta)) * partial; };
+    const auto part = [&](int i) { return partial_of(a.workspace, cta + i, i == 0, floats); };
     const auto load = [&](const float *p) { return dbg_ok(p, 4, false) ? *p : 0.0f; };
-    float ref = kNothing;
-    for (int i = cta + lane; i < last; i += 32) ref = fmaxf(ref, load(part(i) + row));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < rows) {
+        float ref = kNothing, total = 0.0f;
+        for (int i = lane; i < at.parts; i += 32) {
+            const float r = load(part(i) + row0 + warp);
+            weight[warp][i] = r;
+            ref = fmaxf(ref, r);
+        }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(kFull, ref, d));
-    float total = 0.0f, sum[kPer] = {};
-#pragma unroll 4
-    for (int i = cta; i < last; i++) {
-        const float *p = part(i);
-        const float by = exp2_fast(__fsub_rn(load(p + row), ref));
-        total = __fmaf_rn(load(p + form + row), by, total);
+        for (int d = 16; d; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(kFull, ref, d));
+        for (int i = lane; i < at.parts; i += 32) {
+            const float by = exp2_fast(__fsub_rn(weight[warp][i], ref));
+            weight[warp][i] = by;
+            total = __fmaf_rn(load(part(i) + form + row0 + warp), by, total);
+        }
 #pragma unroll
-        for (int k = 0; k < kPer; k++) sum[k] = __fmaf_rn(load(p + 2 * form + row * kDim + 32 * k + lane), by, sum[k]);
+        for (int d = 16; d; d >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kFull, total, d));
+        if (lane == 0) refs[warp] = ref, totals[warp] = total;
+    }
+    __syncthreads();
+    const int group = threadIdx.x / kDim, in = threadIdx.x - group * kDim, row = in / (kDim / 4), col = 4 * (in - row * (kDim / 4));
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (group < kGroups && row < rows) {
+#pragma unroll 8
+        for (int i = group; i < at.parts; i += kGroups) {
+            const uint4 v = ld_plain_v4(part(i) + 2 * form + (row0 + row) * kDim + col);
+            const float by = weight[row][i];
+            sum = make_float4(__fmaf_rn(__uint_as_float(v.x), by, sum.x), __fmaf_rn(__uint_as_float(v.y), by, sum.y),
+                              __fmaf_rn(__uint_as_float(v.z), by, sum.z), __fmaf_rn(__uint_as_float(v.w), by, sum.w));
+        }
+        sums[group][in] = sum;
+    }
+    __syncthreads();
+    if (group != 0 || row >= rows) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; i++) {
+        const float4 v = sums[i][in];
+        sum = make_float4(__fadd_rn(sum.x, v.x), __fadd_rn(sum.y, v.y), __fadd_rn(sum.z, v.z), __fadd_rn(sum.w, v.w));
     }
     int64_t at_lse;
-    T *to = static_cast<T *>(a.out) + out_row(a, plan, at.b, head, item_row, &at_lse);
-    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-#pragma unroll
-    for (int k = 0; k < kPer; k++)
-        if (dbg_ok(to + 32 * k + lane, 2, true))
-            *reinterpret_cast<uint16_t *>(to + 32 * k + lane) = Value<T>::round(__fmul_rn(sum[k], inv));
-    if (a.lse && lane == 0 && dbg_ok(a.lse + at_lse, 4, true)) a.lse[at_lse] = lse_of(ref, total);
+    T *to = static_cast<T *>(a.out) + out_row(a, plan, at.b, head, first + row, &at_lse);
+    const float total = totals[row], inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+    st_v2(to + col, make_uint2(Value<T>::round2(__fmul_rn(sum.x, inv), __fmul_rn(sum.y, inv)),
+                               Value<T>::round2(__fmul_rn(sum.z, inv), __fmul_rn(sum.w, inv))));
+    if (a.lse && col == 0 && dbg_ok(a.lse + at_lse, 4, true)) a.lse[at_lse] = lse_of(refs[row], total);
 }
 
 template <class T>
@@ -61,15 +90,15 @@ cudaError_t launch_join(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan 
                                                                 : c.head_dim == 192 ? attend_join_kernel<T, 192>
                                                                                     : attend_join_kernel<T, 256>;
     const int form = form_rows(plan.rows, c.head_dim);
-    const int groups = ((plan.rows < form ? plan.rows : form) + kAttendWarps - 1) / kAttendWarps;
-    return launch_kernel_block(kernel, (plan.ctas - 1) * groups, kAttendThreads, 0, st, c, a, plan, form, groups);
+    const int groups = ((plan.rows < form ? plan.rows : form) + kJoinRows - 1) / kJoinRows;
+    return launch_kernel_block(kernel, (plan.ctas - 1) * groups, kJoinThreads, 0, st, c, a, plan, form, groups);
 }
 
 }  // namespace
 
 int64_t kv4_workspace_bytes(int heads, int head_dim, int n_q, int q_heads)
 {
-    return 4 * 2 * kMaxAttendCtas * partial_floats(form_rows(n_q * (q_heads / heads), head_dim), head_dim);
+    return 4 * kMaxAttendCtas * (4 + 2 * partial_floats(form_rows(n_q * (q_heads / heads), head_dim), head_dim));
 }
 
 cudaError_t launch_kv4_attend(int type, const Kv4Cache &c, const Kv4Attend &a, cudaStream_t st)

@@ -60,22 +60,28 @@ __device__ __forceinline__ void sequence_range(const Kv4Cache &c, const Kv4Atten
 // A sequence without positions is one tile too: its rows are written.
 __device__ __forceinline__ int tiles_of(int begin, int end) { return end > begin ? (end - begin - 1) / kTokens + 1 : 1; }
 
+// What an item costs beside its tiles (its queries, the join of its warps), in tiles.
+#ifndef KSETUP
+#define KSETUP 12
+#endif
+constexpr int kSetup = KSETUP;
+
+// CTA i takes the run from i * per on. An item is kSetup places without a tile, then its tiles.
 struct Share {
-    int64_t total;  // tiles of all items
-    int ctas;       // that take a share
-    __device__ __forceinline__ int64_t first(int cta) const { return total / ctas * cta + total % ctas * cta / ctas; }
+    int64_t total, per;
+    int ctas;  // that take any
+    __device__ __forceinline__ int64_t first(int cta) const { return cta < ctas ? cta * per : total; }
 };
 // Where a tile of the run lies.
 struct Spot {
     int b, begin, end, tiles;  // sequence, its range and tiles
     int item;                  // head * chunks + chunk
     int tile;
+    int64_t base;              // place of the item's tile 0, counted from the CTA's first
 };
 
-// Every CTA finds its share by itself, from the lengths: `spot` is where tile share.first(cta) lies. All threads of
-// the CTA call it.
-__device__ __forceinline__ void find_share(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int cta, Share &share,
-                                           Spot &spot)
+// Every CTA finds its share by itself, from the lengths: `spot` is where its first tile lies. All threads call it.
+__device__ __forceinline__ void find_share(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, Share &share, Spot &spot)
 {
     __shared__ int64_t warp_sum[kAttendWarps];
     __shared__ Spot found;
@@ -86,7 +92,7 @@ __device__ __forceinline__ void find_share(const Kv4Cache &c, const Kv4Attend &a
     int begin = 0, end = 0;
     for (int b = b0; b < b1; b++) {
         sequence_range(c, a, b, begin, end);
-        mine += tiles_of(begin, end);
+        mine += tiles_of(begin, end) + kSetup;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -103,31 +109,46 @@ __device__ __forceinline__ void find_share(const Kv4Cache &c, const Kv4Attend &a
         all += warp_sum[w];
     }
     share.total = all * plan.items;
-    const int64_t most = (share.total + kAttendWarps - 1) / kAttendWarps;
-    share.ctas = most < plan.ctas ? (int)most : plan.ctas;
-    const int64_t target = share.first(min(cta, share.ctas - 1));
-    int64_t at = upto - mine;  // tiles of one item before sequence b0
+    if (share.total < 0x7fffffff) {  // divisions of 64 bits take long
+        share.per = max(((uint32_t)share.total - 1) / (uint32_t)plan.ctas + 1, (uint32_t)kAttendWarps);
+        share.ctas = (int)(((uint32_t)share.total - 1) / (uint32_t)share.per + 1);
+    } else {
+        share.per = (share.total - 1) / plan.ctas + 1;
+        share.ctas = (int)((share.total - 1) / share.per + 1);
+    }
+    const int64_t target = share.first(min((int)blockIdx.x, share.ctas - 1));
+    int64_t at = upto - mine;  // of one item before sequence b0
     if (target >= at * plan.items && target < upto * plan.items) {
         int b = b0;
         for (;; b++) {
             sequence_range(c, a, b, begin, end);
             const int n = tiles_of(begin, end);
-            if (target < (at + n) * plan.items) {
+            if (target < (at + n + kSetup) * plan.items) {
                 const int64_t in = target - at * plan.items;
-                const int item = (int)(in / n);
-                found = Spot{b, begin, end, n, item, (int)(in - (int64_t)item * n)};
+                const int cost = n + kSetup;
+                const int item = in < 0x7fffffff ? (int)((uint32_t)in / (uint32_t)cost) : (int)(in / cost);
+                const int off = (int)(in - (int64_t)item * cost);
+                found = Spot{b, begin, end, n, item, off > kSetup ? off - kSetup : 0, kSetup - off};
                 break;
             }
-            at += n;
+            at += n + kSetup;
         }
     }
     __syncthreads();
     spot = found;
 }
 
-// The place of a CTA's partial sums: [kRows] references, [kRows] totals, [kRows][kDim] sums. A CTA has at most two pieces
-// that others share: one that began before its share, and one that goes on after it.
+// The workspace: a word a CTA that says whether an item goes on after its share and how many shares take part, then two
+// partial sums a CTA (an item that began before its share, one that goes on after it): [kRows] references, [kRows]
+// totals, [kRows][kDim] sums.
+struct Split {
+    int b, item, parts, unused;
+};
 __host__ __device__ __forceinline__ int64_t partial_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
+__host__ __device__ __forceinline__ float *partial_of(float *workspace, int cta, bool goes_on, int64_t floats)
+{
+    return workspace + 4 * kMaxAttendCtas + (2 * (int64_t)cta + goes_on) * floats;
+}
 
 // ---------------------------------------------------------------- constants of a form
 template <int kDim_, int kGroup_, int kRows_>
@@ -135,27 +156,29 @@ struct Form {
     static constexpr int kDim = kDim_, kGroup = kGroup_, kRows = kRows_, kHalves = kRows / 8;
     static constexpr int kGroups = kDim / kGroup, kWords = kGroup / 32;  // code words of a lane in a group of keys
     static constexpr int kChunks = kDim / 32;                            // 16-byte pieces of a row of codes
-    static constexpr int kCodeBytes = kDim == 192 ? 16 * (kTokens * 6 + kTokens) : 16 * kTokens * kChunks;
+    static constexpr int kCodeBytes = kDim == 192 ? 16 * (kTokens * 6 + kTokens / 4) : 16 * kTokens * kChunks;
     static constexpr int kPairBytes = kTokens * 4 * kGroups;
     static constexpr int kStage = 2 * (kCodeBytes + kPairBytes);
     static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
     // CTAs of an SM by their registers: up to 168 a thread with the sums of 8 rows of up to 128 columns, else up to 255
-    static constexpr int kCtas = kRows == 8 && kDim <= 128 ? 3 : 2;
+    #ifndef KC
+#define KC 3
+#endif
+    static constexpr int kCtas = kRows == 8 && kDim <= 128 ? KC : 2;
     static constexpr int kRoom = (227 * 1024 / kCtas - 1024 - 512 - kJoin) / (kAttendWarps * kStage);
     static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
     static constexpr int kSmem = kJoin + kAttendWarps * kStages * kStage;
     static_assert(kStages >= 2, "a ring has two stages at least");
 };
 
-// 16-byte piece c of token t's row, in a stage: permuted so that the rows that one access reads lie in
-// different banks.
+// 16-byte piece c of token t's row, in a stage: permuted so that a piece of eight tokens in a row lies in
+// eight different groups of banks.
 template <int kDim>
 __host__ __device__ __forceinline__ int chunk_at(int t, int c)
 {
-    if (kDim == 192) return t * 6 + c + 4 * (t >> 2);
-    const int low = t & 3, bit = (t >> 2) & 1;
-    const int key = kDim == 64 ? 5 * bit : kDim == 128 ? (low & 2) ^ (3 * bit) : (2 * low) ^ (5 * bit);
-    return (t * (kDim / 32) + c) ^ key;
+    if (kDim == 192) return t * 6 + c + (t >> 2);
+    const int key = kDim == 64 ? (t >> 2) & 1 : kDim == 128 ? (t >> 1) & 3 : t & 7;
+    return t * (kDim / 32) + (c ^ key);
 }
 
 // ---------------------------------------------------------------- small steps
@@ -173,7 +196,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 }
 __device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
-// N code words or pairs at a shared address, in the widest loads that its alignment of 4 N (a power of two's part) allows.
+// N pairs at a shared address, in the widest loads that its alignment (the largest power of two in 4 N bytes) allows.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N])
 {
@@ -192,6 +215,26 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N])
     }
 }
 
+// 8x8 matrices of 16-bit elements, the row of lane 8 m + i row i of matrix m.
+__device__ __forceinline__ void load_matrices(uint32_t at, uint32_t *v)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void load_two_matrices(uint32_t at, uint32_t *v)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&v)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+
 // Four 16-bit halves of codes -> four pairs of u in an FP16's lowest bits, the second and fourth 16 times as large.
 __device__ __forceinline__ void low_bits(uint32_t w, uint32_t (&v)[4])
 {
@@ -201,6 +244,34 @@ __device__ __forceinline__ void low_bits(uint32_t w, uint32_t (&v)[4])
     v[2] = and_xor(w8, 0x000f000fu, 0x00080008u);
     v[3] = and_xor(w8, 0x00f000f0u, 0x00800080u);
 }
+
+// Sums of a group's queries, times (scale, offset) pairs as they lie in memory: T operands, binary32 sums. A sum is cut
+// into kParts values of T that hold 24 or 22 bits of it.
+template <class T>
+struct PairSum;
+template <>
+struct PairSum<__nv_bfloat16> {
+    static constexpr int kParts = 3;
+    static constexpr float kScale = 1.0f;  // of the sums
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Value<__nv_bfloat16>::round2(lo, hi); }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t *a, uint32_t a1, uint32_t a3, uint32_t b0, uint32_t b1)
+    {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a1), "r"(a[1]), "r"(a3), "r"(b0), "r"(b1));
+    }
+};
+template <>
+struct PairSum<__half> {
+    static constexpr int kParts = 2;
+    static constexpr float kScale = 0x1p14f;  // 8 times a sum of 128 values of 2^15 is 2^25 kUnit kScale = 2^15
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_f16(lo, hi); }
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t *a, uint32_t a1, uint32_t a3, uint32_t b0, uint32_t b1)
+    {
+        mma_f16<false>(c, a[0], a1, a[1], a3, b0, b1);
+    }
+};
 
 // log2 bound of a 16-bit magnitude; not finite counts as nothing.
 template <class T>
@@ -216,16 +287,18 @@ __device__ __forceinline__ bool finite_bits(uint32_t bits)
 
 // ---------------------------------------------------------------- the warps' walk over tiles
 struct Walk {
-    int64_t rest;  // tiles of the CTA's share from this one on
     Spot at;
+    int64_t n;  // places of the CTA's share
+    bool more;  // `at` is one of them
 
-    __device__ __forceinline__ void step(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int n)
+    __device__ __forceinline__ void step(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int count)
     {
-        rest -= n;
-        if (rest <= 0) return;
-        at.tile += n;
+        at.tile += count;
         while (at.tile >= at.tiles) {
             at.tile -= at.tiles;
+            at.base += at.tiles + kSetup;
+            more = at.base < n;
+            if (!more) return;
             if (++at.item == plan.items) {
                 at.item = 0;
                 at.b++;
@@ -233,6 +306,7 @@ struct Walk {
                 at.tiles = tiles_of(at.begin, at.end);
             }
         }
+        more = at.base + at.tile < n;
     }
 };
 
@@ -243,14 +317,21 @@ __device__ __forceinline__ uint32_t divide_by(uint32_t n, const Divisor &d) { re
 template <class T, class F>
 struct Feed {
     Walk walk;
-    int entry, place, head;
+    int entry, place;
+    int64_t at_head, at_head_s;  // of the walk's head, and the lane's part of a page where tokens lie at equal steps
+
+    __device__ __forceinline__ void new_item(const Kv4Cache &c, const AttendPlan &plan, int lane)
+    {
+        const int head = (int)divide_by(walk.at.item, plan.by_chunks);
+        at_head = head * c.head_stride;
+        at_head_s = head * c.head_stride_s;
+    }
 
     // a lane's token of the walk's tile
     __device__ __forceinline__ void look_up(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int lane)
     {
         entry = -1;
-        if (walk.rest <= 0) return;
-        head = (int)divide_by(walk.at.item, plan.by_chunks);
+        if (!walk.more) return;
         const int j = walk.at.begin + walk.at.tile * kTokens + lane;
         const int column = (int)divide_by(j, plan.by_page);
         place = j - column * c.page;
@@ -263,30 +344,65 @@ struct Feed {
     __device__ __forceinline__ void issue(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int lane, uint32_t stage,
                                           uint32_t *valid)
     {
-        if (walk.rest > 0) {
+        if (walk.more) {
             const bool ok = entry >= 0 && entry < c.pages;
             const uint32_t there = __ballot_sync(kFull, ok);
             if (lane == 0) *valid = there;
-            const int64_t page = ok ? entry : 0;
-            const int64_t at = ok ? page * c.page_stride + head * c.head_stride + (int64_t)place * c.token_stride : 0;
-            const int64_t at_s = ok ? page * c.page_stride_s + head * c.head_stride_s + (int64_t)place * c.token_stride_s : 0;
-#pragma unroll
-            for (int i = 0; i < F::kChunks; i++) {
-                const int piece = 32 * i + lane, t = piece / F::kChunks, ch = piece % F::kChunks;
-                const int64_t from = __shfl_sync(kFull, at, t) + 16 * ch;
-                const int bytes = (there >> t) & 1 ? 16 : 0;
-                const uint32_t to = stage + 16 * chunk_at<F::kDim>(t, ch);
-                lane_copy_part<16>(to, c.k + from, bytes);
-                lane_copy_part<16>(to + F::kCodeBytes, c.v + from, bytes);
-            }
             constexpr int kSize = F::kGroups % 4 == 0 ? 16 : F::kGroups % 2 == 0 ? 8 : 4;
-            const uint32_t to = stage + 2 * F::kCodeBytes + 4 * F::kGroups * lane;
+            const uint32_t to_s = stage + 2 * F::kCodeBytes + 4 * F::kGroups * lane;
+            const int first = __shfl_sync(kFull, place, 0);
+            if (there == kFull && first + kTokens <= c.page) {  // one page: tokens at equal steps
+                const int64_t page = __shfl_sync(kFull, entry, 0);
+                const int64_t at = page * c.page_stride + at_head + first * c.token_stride;
+                const int64_t at_s = page * c.page_stride_s + at_head_s + place * c.token_stride_s;
+                if constexpr (32 % F::kChunks == 0) {
+                    const int t0 = lane / F::kChunks, ch = lane % F::kChunks;
+                    const int64_t step = 32 / F::kChunks * c.token_stride;
+                    const uint8_t *k = c.k + at + t0 * c.token_stride + 16 * ch, *v = c.v + (k - c.k);
 #pragma unroll
-            for (int i = 0; i < 4 * F::kGroups; i += kSize) {
-                lane_copy_part<kSize>(to + i, c.k_scales + at_s + i, ok ? kSize : 0);
-                lane_copy_part<kSize>(to + F::kPairBytes + i, c.v_scales + at_s + i, ok ? kSize : 0);
+                    for (int i = 0; i < F::kChunks; i++) {
+                        const uint32_t to = stage + 16 * chunk_at<F::kDim>(32 / F::kChunks * i + t0, ch);
+                        lane_copy16(to, k);
+                        lane_copy16(to + F::kCodeBytes, v);
+                        k += step, v += step;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < F::kChunks; i++) {
+                        const int piece = 32 * i + lane, t = piece / F::kChunks, ch = piece % F::kChunks;
+                        const int64_t from = at + t * c.token_stride + 16 * ch;
+                        const uint32_t to = stage + 16 * chunk_at<F::kDim>(t, ch);
+                        lane_copy16(to, c.k + from);
+                        lane_copy16(to + F::kCodeBytes, c.v + from);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4 * F::kGroups; i += kSize) {
+                    lane_copy_part<kSize>(to_s + i, c.k_scales + at_s + i, kSize);
+                    lane_copy_part<kSize>(to_s + F::kPairBytes + i, c.v_scales + at_s + i, kSize);
+                }
+            } else {
+                const int64_t page = ok ? entry : 0;
+                const int64_t at = ok ? page * c.page_stride + at_head + place * c.token_stride : 0;
+                const int64_t at_s = ok ? page * c.page_stride_s + at_head_s + place * c.token_stride_s : 0;
+#pragma unroll
+                for (int i = 0; i < F::kChunks; i++) {
+                    const int piece = 32 * i + lane, t = piece / F::kChunks, ch = piece % F::kChunks;
+                    const int64_t from = __shfl_sync(kFull, at, t) + 16 * ch;
+                    const int bytes = (there >> t) & 1 ? 16 : 0;
+                    const uint32_t to = stage + 16 * chunk_at<F::kDim>(t, ch);
+                    lane_copy_part<16>(to, c.k + from, bytes);
+                    lane_copy_part<16>(to + F::kCodeBytes, c.v + from, bytes);
+                }
+#pragma unroll
+                for (int i = 0; i < 4 * F::kGroups; i += kSize) {
+                    lane_copy_part<kSize>(to_s + i, c.k_scales + at_s + i, ok ? kSize : 0);
+                    lane_copy_part<kSize>(to_s + F::kPairBytes + i, c.v_scales + at_s + i, ok ? kSize : 0);
+                }
             }
+            const int item = walk.at.item;
             walk.step(c, a, plan, kAttendWarps);
+            if (item != walk.at.item) new_item(c, plan, lane);
             look_up(c, a, plan, lane);
         }
         lane_copy_commit();
@@ -294,17 +410,20 @@ struct Feed {
 };
 
 // ---------------------------------------------------------------- one piece of work of a warp
-// Lane 4 r + q. Scores: rows r and r + 8 (halves 0 and 1), of a tile of 8 tokens the tokens q and q + 4. Sums of the
-// output: columns of lane part r, rows 2 q and 2 q + 1 of a half.
+// Lane 4 r + q. Scores: rows r and r + 8 (halves 0 and 1), of eight tokens 2 q and 2 q + 1. Sums of the output:
+// columns 4 r .. 4 r + 3 of every 32, rows 2 q and 2 q + 1 of a half.
 template <class T, class F>
 struct Rows {
+    // mma that multiply the groups' sums of queries: eight pairs of a token each
+    static constexpr int kSums = (PairSum<T>::kParts * F::kGroups + 7) / 8;
     uint32_t qf[F::kGroups][F::kWords][2][2 * F::kHalves];  // queries as mma fragments
-    float qsum[F::kHalves][F::kGroups];                     // kUnit times the sum of a group's scaled queries
+    uint32_t qsum[kSums][2 * F::kHalves];             // fragments of a group's sum of scaled queries, times kUnit
     float f[F::kHalves];                                    // from a score in units to its log2
     float ref[F::kHalves];                                  // A
     float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
     float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
     float eights[(F::kGroups + 1) / 2][F::kHalves][4];      // of 8 p s, in units: a group in c0 c1, the next in c2 c3
+    uint32_t pieces[4];                                     // of values: two pieces of 16 tokens
 
     __device__ __forceinline__ void start(const Kv4Attend &a, const AttendPlan &plan, int b, int head, int row0, int lane)
     {
@@ -315,14 +434,14 @@ struct Rows {
             uint4 raw[F::kGroups][F::kWords];
             const int i = (int)divide_by(row < plan.rows ? row : 0, plan.by_share), in = (row < plan.rows ? row : 0) - i * plan.share;
             const T *from = static_cast<const T *>(a.q) + b * a.q_batch + i * a.q_query +
-                            (int64_t)(head * plan.share + in) * a.q_head + q * (F::kGroup / 4);
+                            (int64_t)(head * plan.share + in) * a.q_head + 8 * q;
             uint32_t top = 0;
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++)
 #pragma unroll
                 for (int w = 0; w < F::kWords; w++) {
                     uint4 &x = raw[g][w];
-                    x = row < plan.rows ? ld_keep_v4(from + g * F::kGroup + 8 * w) : make_uint4(0, 0, 0, 0);
+                    x = row < plan.rows ? ld_keep_v4(from + g * F::kGroup + 32 * w) : make_uint4(0, 0, 0, 0);
                     top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
                                                  __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
                 }
@@ -331,6 +450,7 @@ struct Rows {
             top = max(top, __shfl_xor_sync(kFull, top, 2));
             const int e = max(exponent_of<T>(top), -100);  // the largest value is below 2^(e + 1)
             const float by = copysignf(power_of_2(14 - e), a.scale), by16 = 0.0625f * by;
+            float all[F::kGroups];
             const int half = (e + 10) / 2;
             f[h] = fminf(__fmul_rn(__fmul_rn(__fmul_rn(fabsf(a.scale), 1.4426950408889634f), power_of_2(half)),
                                    power_of_2(e + 10 - half)), 3.0e38f);
@@ -353,9 +473,27 @@ struct Rows {
                     }
                 }
                 total_q = __fadd_rn(total_q, __shfl_xor_sync(kFull, total_q, 1));
-                qsum[h][g] = __fadd_rn(total_q, __shfl_xor_sync(kFull, total_q, 2));
+                all[g] = __fmul_rn(__fadd_rn(total_q, __shfl_xor_sync(kFull, total_q, 2)), PairSum<T>::kScale);
                 off[h][g] = splat(0.0f);
             }
+#pragma unroll
+            for (int m = 0; m < kSums; m++)
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    // slot: part slot / kGroups of group slot % kGroups
+                    const int slot = 8 * m + 4 * j + q, part = slot / F::kGroups;
+                    float rest = 0.0f, value = 0.0f;
+#pragma unroll
+                    for (int g = 0; g < F::kGroups; g++)
+                        if (g == slot % F::kGroups) rest = all[g];
+#pragma unroll
+                    for (int i = 0; i < PairSum<T>::kParts; i++) {
+                        const float v = Value<T>::widen(Value<T>::round(rest));
+                        if (i == part) value = v;
+                        rest = __fsub_rn(rest, v);
+                    }
+                    qsum[m][F::kHalves * j + h] = PairSum<T>::pack(-8.0f * value, value);
+                }
             ref[h] = kNothing;
             total[h] = splat(0.0f);
 #pragma unroll
@@ -369,47 +507,62 @@ struct Rows {
         }
     }
 
-    // x in units of tokens 8 n + q and 8 n + q + 4
+    // x in units of tokens 8 n + 2 q and the next
     __device__ __forceinline__ void scores(uint32_t stage, int lane, float2 (&x)[4][F::kHalves])
     {
-        const int r = lane >> 2, q = lane & 3, t0 = (r >> 1) + 4 * (r & 1);
-        const uint32_t pairs = stage + 2 * F::kCodeBytes + 4 * F::kGroups * q;
+        constexpr int kLast = F::kHalves - 1;
+        const int r = lane >> 2, q = lane & 3;
+        const uint32_t pairs = stage + 2 * F::kCodeBytes;
 #pragma unroll
         for (int n = 0; n < 4; n++) {
-            uint32_t pa[F::kGroups], pb[F::kGroups];
-            lds_words<F::kGroups>(pairs + 4 * F::kGroups * 8 * n, pa);
-            lds_words<F::kGroups>(pairs + 4 * F::kGroups * (8 * n + 4), pb);
+            // word q of every piece of token 8 n + r
+            uint32_t w[F::kChunks];
+            const int row = 8 * n + (lane & 7);
 #pragma unroll
-            for (int h = 0; h < F::kHalves; h++) x[n][h] = splat(0.0f);
+            for (int i = 0; i + 4 <= F::kChunks; i += 4) load_matrices(stage + 16 * chunk_at<F::kDim>(row, i + (lane >> 3)), w + i);
+            if constexpr (F::kChunks % 4 != 0)
+                load_two_matrices(stage + 16 * chunk_at<F::kDim>(row, F::kChunks - 2 + ((lane >> 3) & 1)), w + F::kChunks - 2);
+            uint32_t pw[2 * F::kGroups];
+            lds_words<2 * F::kGroups>(pairs + 4 * F::kGroups * (8 * n + 2 * q), pw);
+            float c[4] = {};
+            {
+                constexpr bool kOne = 4 % F::kGroups == 0, kTwo = F::kGroups == 8;  // words that all slots share
+                const uint32_t at = pairs + 4 * F::kGroups * (8 * n + r);
+                const uint32_t b0 = lds_u32(at + 4 * (q % F::kGroups)), b1 = kTwo ? lds_u32(at + 4 * (4 + q)) : b0;
+#pragma unroll
+                for (int m = 0; m < kSums; m++) {
+                    const uint32_t *a = qsum[m];
+                    const uint32_t pair[2] = {a[0], a[F::kHalves]};
+                    const uint32_t first = kOne || kTwo || m == 0 ? b0 : lds_u32(at + 4 * ((8 * m + q) % F::kGroups));
+                    const uint32_t second = kOne || kTwo ? b1 : lds_u32(at + 4 * ((8 * m + 4 + q) % F::kGroups));
+                    PairSum<T>::mma(c, pair, kLast ? a[kLast] : 0u, kLast ? a[F::kHalves + kLast] : 0u, first, second);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < F::kHalves; h++) {
+                x[n][h] = make_float2(c[2 * h], c[2 * h + 1]);
+                if (PairSum<T>::kScale != 1.0f) x[n][h] = mul2(x[n][h], splat(1.0f / PairSum<T>::kScale));
+            }
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++) {
-                // the lane's words: kWords * q and on, of the group's 4 kWords
-                uint32_t w[F::kWords];
-                const int piece = g * F::kWords + (F::kWords * q) / 4, in = (F::kWords * q) % 4;
-                lds_words<F::kWords>(stage + 16 * chunk_at<F::kDim>(t0 + 8 * n, piece) + 4 * in, w);
-                float c[4];
+                float d[4];
 #pragma unroll
                 for (int i = 0; i < F::kWords; i++) {
                     uint32_t u[4];
-                    low_bits(w[i], u);
+                    low_bits(w[g * F::kWords + i], u);
 #pragma unroll
                     for (int m = 0; m < 2; m++) {
                         const uint32_t *a = qf[g][i][m];
-                        constexpr int kLast = F::kHalves - 1;
                         const uint32_t a1 = kLast ? a[kLast] : 0u, a3 = kLast ? a[F::kHalves + kLast] : 0u;
                         if (i == 0 && m == 0)
-                            mma_f16<true>(c, a[0], a1, a[F::kHalves], a3, u[0], u[1]);
+                            mma_f16<true>(d, a[0], a1, a[F::kHalves], a3, u[0], u[1]);
                         else
-                            mma_f16<false>(c, a[0], a1, a[F::kHalves], a3, u[2 * m], u[2 * m + 1]);
+                            mma_f16<false>(d, a[0], a1, a[F::kHalves], a3, u[2 * m], u[2 * m + 1]);
                     }
                 }
-                const float2 one = pair_values<T>(pa[g]), two = pair_values<T>(pb[g]);
-                const float2 s = make_float2(one.x, two.x), z = fma2(s, splat(-8.0f), make_float2(one.y, two.y));
+                const float2 s = make_float2(pair_values<T>(pw[g]).x, pair_values<T>(pw[F::kGroups + g]).x);
 #pragma unroll
-                for (int h = 0; h < F::kHalves; h++) {
-                    x[n][h] = fma2(s, make_float2(c[2 * h], c[2 * h + 1]), x[n][h]);
-                    x[n][h] = fma2(z, splat(qsum[h][g]), x[n][h]);
-                }
+                for (int h = 0; h < F::kHalves; h++) x[n][h] = fma2(s, make_float2(d[2 * h], d[2 * h + 1]), x[n][h]);
             }
         }
     }
@@ -418,19 +571,26 @@ struct Rows {
     template <bool kMasked>
     __device__ __forceinline__ void take(uint32_t stage, int lane, float2 (&x)[4][F::kHalves], const uint32_t (&seen)[F::kHalves])
     {
-        const int r = lane >> 2, q = lane & 3;
+        const int q = lane & 3;
         const uint32_t pairs = stage + 2 * F::kCodeBytes + F::kPairBytes;
         // log2 of the largest scale of the tile's values; offsets count 2^-24, so that sums of p z stay in range
         int k;
         {
             uint32_t w[F::kGroups];
             lds_words<F::kGroups>(pairs + 4 * F::kGroups * lane, w);
-            k = -60;
+            uint32_t top = 0;
 #pragma unroll
-            for (int g = 0; g < F::kGroups; g++) {
-                const uint32_t s = w[g] & 0x7fffu, z = (w[g] >> 16) & 0x7fffu;
-                if (finite_bits<T>(s)) k = max(k, exponent_of<T>(s) + 1);
-                if (finite_bits<T>(z)) k = max(k, exponent_of<T>(z) - 23);
+            for (int g = 0; g < F::kGroups; g++) top = __vmaxu2(top, w[g] & 0x7fff7fffu);
+            k = -60;
+            if (finite_bits<T>(top & 0xffffu) && finite_bits<T>(top >> 16)) {
+                k = max(k, max(exponent_of<T>(top & 0xffffu) + 1, exponent_of<T>(top >> 16) - 23));
+            } else {
+#pragma unroll
+                for (int g = 0; g < F::kGroups; g++) {
+                    const uint32_t s = w[g] & 0x7fffu, z = (w[g] >> 16) & 0x7fffu;
+                    if (finite_bits<T>(s)) k = max(k, exponent_of<T>(s) + 1);
+                    if (finite_bits<T>(z)) k = max(k, exponent_of<T>(z) - 23);
+                }
             }
             k = __reduce_max_sync(kFull, k);
         }
@@ -441,8 +601,8 @@ struct Rows {
             float top = -INFINITY;
 #pragma unroll
             for (int n = 0; n < 4; n++) {
-                const float lo = !kMasked || ((seen[h] >> (8 * n + q)) & 1) ? x[n][h].x : -INFINITY;
-                const float hi = !kMasked || ((seen[h] >> (8 * n + q + 4)) & 1) ? x[n][h].y : -INFINITY;
+                const float lo = !kMasked || ((seen[h] >> (8 * n + 2 * q)) & 1) ? x[n][h].x : -INFINITY;
+                const float hi = !kMasked || ((seen[h] >> (8 * n + 2 * q + 1)) & 1) ? x[n][h].y : -INFINITY;
                 top = fmaxf(top, fmaxf(lo, hi));
             }
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
@@ -477,30 +637,30 @@ struct Rows {
                 float2 &p = x[n][h];
                 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                 if (kMasked) {
-                    if (!((seen[h] >> (8 * n + q)) & 1)) p.x = 0.0f;
-                    if (!((seen[h] >> (8 * n + q + 4)) & 1)) p.y = 0.0f;
+                    if (!((seen[h] >> (8 * n + 2 * q)) & 1)) p.x = 0.0f;
+                    if (!((seen[h] >> (8 * n + 2 * q + 1)) & 1)) p.y = 0.0f;
                 }
                 total[h] = add2(total[h], p);
             }
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            uint32_t pw[4][F::kGroups];
+            uint32_t pw[2][2 * F::kGroups];
 #pragma unroll
-            for (int j = 0; j < 4; j++) lds_words<F::kGroups>(pairs + 4 * F::kGroups * (16 * i + 4 * j + q), pw[j]);
+            for (int n = 0; n < 2; n++) lds_words<2 * F::kGroups>(pairs + 4 * F::kGroups * (16 * i + 8 * n + 2 * q), pw[n]);
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++) {
                 uint32_t b[F::kHalves][2];
 #pragma unroll
                 for (int n = 0; n < 2; n++) {
-                    const float2 one = pair_values<T>(pw[2 * n][g]), two = pair_values<T>(pw[2 * n + 1][g]);
+                    const float2 one = pair_values<T>(pw[n][g]), two = pair_values<T>(pw[n][F::kGroups + g]);
                     const float2 s = make_float2(one.x, two.x), z = make_float2(one.y, two.y);
 #pragma unroll
                     for (int h = 0; h < F::kHalves; h++) {
                         const float2 p = x[2 * i + n][h];
                         float2 sh = s, zh = z;
                         if (kMasked) {  // a row that does not see a token takes nothing of it, a NaN neither
-                            if (!((seen[h] >> (16 * i + 8 * n + q)) & 1)) sh.x = zh.x = 0.0f;
-                            if (!((seen[h] >> (16 * i + 8 * n + q + 4)) & 1)) sh.y = zh.y = 0.0f;
+                            if (!((seen[h] >> (16 * i + 8 * n + 2 * q)) & 1)) sh.x = zh.x = 0.0f;
+                            if (!((seen[h] >> (16 * i + 8 * n + 2 * q + 1)) & 1)) sh.y = zh.y = 0.0f;
                         }
                         const float2 ps = mul2(p, sh);
                         b[h][n] = pack_f16(ps.x, ps.y);
@@ -515,39 +675,27 @@ struct Rows {
                     else
                         mma_f16<false>(eights[g / 2][h], kEight, 0u, kEight, 0u, b[h][0], b[h][1]);
                 }
-                values(stage + F::kCodeBytes, r, q, i, g, b);
+                values(stage + F::kCodeBytes, lane, i, g, b);
             }
         }
     }
 
-    // The codes of 16 tokens in group g against b.
-    __device__ __forceinline__ void values(uint32_t codes, int r, int q, int i, int g, const uint32_t (&b)[F::kHalves][2])
+    // The codes of 16 tokens in group g against b. A transposed matrix of eight tokens and one piece gives a lane four
+    // columns' codes of two tokens, side by side as a fragment of the values takes them.
+    __device__ __forceinline__ void values(uint32_t codes, int lane, int i, int g, const uint32_t (&b)[F::kHalves][2])
     {
-        constexpr int kLaneWords = F::kGroup >= 64 ? F::kGroup / 64 : 1;
-        uint32_t w[4][kLaneWords];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            // groups of 32 columns have four words: lanes r and r + 4 share one, half a word each
-            const int word = F::kGroup >= 64 ? kLaneWords * r : r & 3;
-            const int piece = g * F::kWords + word / 4;
-            lds_words<kLaneWords>(codes + 16 * chunk_at<F::kDim>(16 * i + 4 * j + q, piece) + 4 * (word % 4), w[j]);
-        }
+        for (int k = 0; k < F::kWords; k++) {
+            const int piece = g * F::kWords + k;
+            if (piece % 2 == 0) load_transposed(codes + 16 * chunk_at<F::kDim>(16 * i + (lane & 15), piece + (lane >> 4)), pieces);
+            uint32_t lo[4], hi[4];
+            low_bits(pieces[2 * (piece % 2)], lo);
+            low_bits(pieces[2 * (piece % 2) + 1], hi);
 #pragma unroll
-        for (int k = 0; k < kLaneWords; k++) {
+            for (int odd = 0; odd < 2; odd++)
 #pragma unroll
-            for (int half = 0; half < (F::kGroup >= 64 ? 2 : 1); half++) {
-                const uint32_t pick = F::kGroup >= 64 ? (half ? 0x7632u : 0x5410u) : (r & 4 ? 0x7632u : 0x5410u);
-                uint32_t lo[4], hi[4];
-                low_bits(__byte_perm(w[0][k], w[1][k], pick), lo);
-                low_bits(__byte_perm(w[2][k], w[3][k], pick), hi);
-#pragma unroll
-                for (int odd = 0; odd < 2; odd++) {
-                    const int m = F::kGroup >= 64 ? (g * kLaneWords + k) * 4 + 2 * half + odd : 2 * g + odd;
-#pragma unroll
-                    for (int h = 0; h < F::kHalves; h++)
-                        mma_f16<false>(sum[m][h], lo[odd], lo[2 + odd], hi[odd], hi[2 + odd], b[h][0], b[h][1]);
-                }
-            }
+                for (int h = 0; h < F::kHalves; h++)
+                    mma_f16<false>(sum[2 * piece + odd][h], lo[odd], lo[2 + odd], hi[odd], hi[2 + odd], b[h][0], b[h][1]);
         }
     }
 
@@ -582,15 +730,6 @@ struct Rows {
 };
 
 // ---------------------------------------------------------------- the kernel
-template <int N>
-__device__ __forceinline__ void store_floats(float *p, const float (&v)[N])
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-        st_v4(p + i, make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
-                                __float_as_uint(v[i + 3])));
-}
-
 // Where an item's row goes.
 __device__ __forceinline__ int64_t out_row(const Kv4Attend &a, const AttendPlan &plan, int b, int head, int row, int64_t *lse)
 {
@@ -614,30 +753,19 @@ __device__ __forceinline__ void dbg_attend(const Kv4Cache &c, const Kv4Attend &a
     dbg_allow(a.table, a.width ? 4 * ((a.batch - 1) * a.ld_table + a.width) : 0, false);
     dbg_allow(a.lengths, 4ll * a.batch, false);
     dbg_allow(a.lse, a.lse ? 4ll * a.batch * a.n_q * a.q_heads : 0, true);
-    dbg_allow(a.workspace, 4 * 2 * plan.ctas * floats, true);
+    dbg_allow(a.workspace, 4 * (4 * kMaxAttendCtas + 2 * plan.ctas * floats), true);
     dbg_ready();
 }
 
 // A warp's sums beside those of another warp in shared memory: [kRows] references, [kRows] totals, [kRows][kDim].
 template <class T, class F>
 struct Join {
-    static constexpr int kRun = F::kGroup >= 64 ? 8 : 4;  // consecutive columns of a lane
-    // first column of run k of a lane's, k < kDim / 8 / kRun
-    static __device__ __forceinline__ int column(int r, int k)
+    static constexpr int kRuns = F::kDim / 32;  // of four columns of a lane
+    static __device__ __forceinline__ int column(int r, int k) { return 32 * k + 4 * r; }
+    // run k's values of row 2 q + odd of half h, in order: rows r and r + 8 of the even columns' tile and the odd ones'
+    static __device__ __forceinline__ float4 run_of(const Rows<T, F> &x, int k, int h, int odd)
     {
-        if (F::kGroup == 32) return 32 * k + 8 * (r & 3) + 4 * (r >> 2);
-        constexpr int kLaneWords = F::kGroup >= 64 ? F::kGroup / 64 : 1;
-        return k / kLaneWords * F::kGroup + 8 * (kLaneWords * r + k % kLaneWords);
-    }
-    // run k's values of row 2 q + odd of half h, in order
-    static __device__ __forceinline__ void run_of(const Rows<T, F> &x, int k, int h, int odd, float (&v)[kRun])
-    {
-#pragma unroll
-        for (int i = 0; i < kRun; i++) {
-            // column i of a run: from m tile of its half word and parity, rows r (first of two) or r + 8
-            const int m = k * (kRun / 2) + 2 * (i / 4) + (i & 1);
-            v[i] = x.sum[m][h][2 * ((i >> 1) & 1) + odd];
-        }
+        return make_float4(x.sum[2 * k][h][odd], x.sum[2 * k + 1][h][odd], x.sum[2 * k][h][2 + odd], x.sum[2 * k + 1][h][2 + odd]);
     }
     static __device__ __forceinline__ void put(const Rows<T, F> &x, float *to, int lane)
     {
@@ -648,13 +776,9 @@ struct Join {
 #pragma unroll
             for (int odd = 0; odd < 2; odd++)
 #pragma unroll
-                for (int k = 0; k < F::kDim / 8 / kRun; k++) {
-                    float v[kRun];
-                    run_of(x, k, h, odd, v);
-                    float *p = to + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + column(r, k);
-#pragma unroll
-                    for (int i = 0; i < kRun; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                }
+                for (int k = 0; k < kRuns; k++)
+                    *reinterpret_cast<float4 *>(to + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + column(r, k)) =
+                        run_of(x, k, h, odd);
         }
     }
     static __device__ __forceinline__ void add(Rows<T, F> &x, const float *from, int lane)
@@ -670,17 +794,14 @@ struct Join {
             for (int odd = 0; odd < 2; odd++) {
                 const float m = __shfl_sync(kFull, mine, 8 * q + 4 * odd), t = __shfl_sync(kFull, theirs, 8 * q + 4 * odd);
 #pragma unroll
-                for (int k = 0; k < F::kDim / 8 / kRun; k++) {
-                    const float *p = from + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + column(r, k);
+                for (int k = 0; k < kRuns; k++) {
+                    const float4 v = *reinterpret_cast<const float4 *>(from + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim +
+                                                                       column(r, k));
+                    const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int i = 0; i < kRun; i += 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(p + i);
-                        const float w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            float &s = x.sum[k * (kRun / 2) + 2 * (i / 4) + (j & 1)][h][2 * (j >> 1) + odd];
-                            s = __fmaf_rn(w[j], t, __fmul_rn(s, m));
-                        }
+                    for (int j = 0; j < 4; j++) {
+                        float &s = x.sum[2 * k + (j & 1)][h][2 * (j >> 1) + odd];
+                        s = __fmaf_rn(w[j], t, __fmul_rn(s, m));
                     }
                 }
             }
@@ -701,24 +822,26 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Share share;
     Spot now;
-    find_share(c, a, plan, blockIdx.x, share, now);
+    find_share(c, a, plan, share, now);
+    if (threadIdx.x == 0) st_v4(a.workspace + 4 * blockIdx.x, make_uint4(0, 0, 0, 0));
     if ((int)blockIdx.x >= share.ctas) return;
-    const int64_t tiles = share.first(blockIdx.x + 1) - share.first(blockIdx.x);
+    const int64_t places = share.first(blockIdx.x + 1) - share.first(blockIdx.x);
 
     float *const joins = reinterpret_cast<float *>(smem);
     const uint32_t ring = smem_u32(smem) + F::kJoin + warp * F::kStages * F::kStage;
     Feed<T, F> feed;
-    feed.walk = Walk{tiles, now};
+    feed.walk = Walk{now, places, now.base + now.tile < places};
     feed.walk.step(c, a, plan, warp);
+    feed.new_item(c, plan, lane);
     feed.look_up(c, a, plan, lane);
 #pragma unroll
     for (int s = 0; s < F::kStages - 1; s++) feed.issue(c, a, plan, lane, ring + s * F::kStage, &valid[warp][s]);
 
     Rows<T, F> x;
     int slot = 0;
-    for (int64_t done = 0; done < tiles;) {
-        const int64_t left = tiles - done;
-        const int last = left < now.tiles - now.tile ? now.tile + (int)left : now.tiles;  // of the item in this share
+    for (int turn = 0; now.base + now.tile < places;) {
+        const int64_t left = places - now.base;
+        const int last = left < now.tiles ? (int)left : now.tiles;  // of the item in this share
         const int head = (int)divide_by(now.item, plan.by_chunks), row0 = (now.item - head * plan.chunks) * F::kRows;
         x.start(a, plan, now.b, head, row0, lane);
         // the positions that the lane's rows see, and that all rows of the item do
@@ -732,7 +855,7 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
         const int all_hi = now.end - a.n_q + 1 + (int)divide_by(row0, plan.by_share);
         const int last_hi = now.end - a.n_q + 1 + (int)divide_by(min(row0 + F::kRows, plan.rows) - 1, plan.by_share);
         const int all_lo = a.window > 0 && last_hi > a.window ? last_hi - a.window : 0;
-        for (int t = now.tile + ((warp - (int)done) & (kAttendWarps - 1)); t < last; t += kAttendWarps) {
+        for (int t = now.tile + ((warp - turn) & (kAttendWarps - 1)); t < last; t += kAttendWarps) {
             lane_copy_wait<F::kStages - 2>();
             __syncwarp();
             const uint32_t stage = ring + slot * F::kStage, there = valid[warp][slot];
@@ -785,23 +908,22 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                         if (row < plan.rows) {
                             T *to = static_cast<T *>(a.out) + out_row(a, plan, now.b, head, row, &unused);
 #pragma unroll
-                            for (int k = 0; k < F::kDim / 8 / J::kRun; k++) {
-                                float v[J::kRun];
-                                J::run_of(x, k, h, odd, v);
-                                uint32_t w[J::kRun / 2];
-#pragma unroll
-                                for (int i = 0; i < J::kRun / 2; i++)
-                                    w[i] = Value<T>::round2(__fmul_rn(v[2 * i], by), __fmul_rn(v[2 * i + 1], by));
-                                if constexpr (J::kRun == 8)
-                                    st_v4(to + J::column(r, k), make_uint4(w[0], w[1], w[2], w[3]));
-                                else
-                                    st_v2(to + J::column(r, k), make_uint2(w[0], w[1]));
+                            for (int k = 0; k < J::kRuns; k++) {
+                                const float4 v = J::run_of(x, k, h, odd);
+                                st_v2(to + J::column(r, k), make_uint2(Value<T>::round2(__fmul_rn(v.x, by), __fmul_rn(v.y, by)),
+                                                                       Value<T>::round2(__fmul_rn(v.z, by), __fmul_rn(v.w, by))));
                             }
                         }
                     }
                 }
             } else {
-                float *const to = a.workspace + (2 * (int64_t)blockIdx.x + (now.tile == 0)) * kPartial;
+                const bool goes_on = now.tile == 0;
+                float *const to = partial_of(a.workspace, blockIdx.x, goes_on, kPartial);
+                if (goes_on && lane == 0) {
+                    const int64_t rest = now.tiles - last + share.per - 1;
+                    const int more = rest < 0x7fffffff ? (int)((uint32_t)rest / (uint32_t)share.per) : (int)(rest / share.per);
+                    st_v4(a.workspace + 4 * blockIdx.x, make_uint4(now.b, now.item, 1 + more, 0));
+                }
 #pragma unroll
                 for (int h = 0; h < F::kHalves; h++) {
                     if (q == 0 && dbg_ok(to + 8 * h + r, 4, true)) to[8 * h + r] = x.ref[h];
@@ -809,17 +931,19 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
 #pragma unroll
                     for (int odd = 0; odd < 2; odd++)
 #pragma unroll
-                        for (int k = 0; k < F::kDim / 8 / J::kRun; k++) {
-                            float v[J::kRun];
-                            J::run_of(x, k, h, odd, v);
-                            store_floats(to + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + J::column(r, k), v);
+                        for (int k = 0; k < J::kRuns; k++) {
+                            const float4 v = J::run_of(x, k, h, odd);
+                            st_v4(to + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim + J::column(r, k),
+                                  make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)));
                         }
                 }
             }
         }
-        done += last - now.tile;
+        turn += last - now.tile;
+        if (last < now.tiles) break;
+        now.base += now.tiles + kSetup;
         now.tile = 0;
-        if (done < tiles && ++now.item == plan.items) {
+        if (now.base < places && ++now.item == plan.items) {
             now.item = 0;
             now.b++;
             sequence_range(c, a, now.b, now.begin, now.end);
