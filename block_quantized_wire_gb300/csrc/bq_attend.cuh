@@ -18,10 +18,10 @@
 // u's offset does not enlarge that error. p's reference A takes in the size of s, p = 2^(y - A), A = max y + log2 max s
 // - 13, so that p s stays within 2^15 and is exact to 2^-11 down to 2^-28 of the largest.
 //
-// Fragments. Keys are the n side (a lane's column is a token), values the m side, so that the scores'
-// layout (rows = queries, columns = tokens) is the layout in which the second product takes its p s: nothing
-// moves between lanes. Column 2 i of a score tile of 8 is token i, column 2 i + 1 token i + 4, which
-// makes the four tokens that a lane needs of the values q, q + 4, q + 8, q + 12: their rows lie in different banks.
+// Fragments. Codes are the m side of both products: tokens of the keys, columns of the values, which ldmatrix and its
+// transposing form deliver as they lie. Scores come with tokens as rows and queries as columns; p s, rounded, is
+// turned over by movmatrix into the n side of the second product. So up to 8 query rows cost half the mma that 16 do, and all
+// that belongs to a query row (reference, sums, weights) lies in the lanes that hold its columns.
 #pragma once
 
 #include <cmath>
@@ -61,10 +61,7 @@ __device__ __forceinline__ void sequence_range(const Kv4Cache &c, const Kv4Atten
 __device__ __forceinline__ int tiles_of(int begin, int end) { return end > begin ? (end - begin - 1) / kTokens + 1 : 1; }
 
 // What an item costs beside its tiles (its queries, the join of its warps), in tiles.
-#ifndef KSETUP
-#define KSETUP 12
-#endif
-constexpr int kSetup = KSETUP;
+constexpr int kSetup = 12;
 
 // CTA i takes the run from i * per on. An item is kSetup places without a tile, then its tiles.
 struct Share {
@@ -160,11 +157,8 @@ struct Form {
     static constexpr int kPairBytes = kTokens * 4 * kGroups;
     static constexpr int kStage = 2 * (kCodeBytes + kPairBytes);
     static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
-    // CTAs of an SM by their registers: up to 168 a thread with the sums of 8 rows of up to 128 columns, else up to 255
-    #ifndef KC
-#define KC 3
-#endif
-    static constexpr int kCtas = kRows == 8 && kDim <= 128 ? KC : 2;
+    // CTAs of an SM by their registers: the sums of 8 rows of 64 columns fit 128 a thread, of 128 columns 168
+        static constexpr int kCtas = kRows == 8 && kDim <= 128 ? (kDim == 64 ? 4 : 3) : 2;
     static constexpr int kRoom = (227 * 1024 / kCtas - 1024 - 512 - kJoin) / (kAttendWarps * kStage);
     static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
     static constexpr int kSmem = kJoin + kAttendWarps * kStages * kStage;
@@ -223,9 +217,12 @@ __device__ __forceinline__ void load_matrices(uint32_t at, uint32_t *v)
                  : "r"(at)
                  : "memory");
 }
-__device__ __forceinline__ void load_two_matrices(uint32_t at, uint32_t *v)
+// An 8x8 matrix of 16-bit elements turned over its diagonal.
+__device__ __forceinline__ uint32_t transposed(uint32_t v)
 {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at) : "memory");
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&v)[4])
 {
@@ -254,12 +251,15 @@ struct PairSum<__nv_bfloat16> {
     static constexpr int kParts = 3;
     static constexpr float kScale = 1.0f;  // of the sums
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return Value<__nv_bfloat16>::round2(lo, hi); }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t *a, uint32_t a1, uint32_t a3, uint32_t b0, uint32_t b1)
+    template <bool kFirst>
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
     {
+        if constexpr (kFirst)
+            c[0] = c[1] = c[2] = c[3] = 0.0f;
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
             "{%8, %9}, {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a1), "r"(a[1]), "r"(a3), "r"(b0), "r"(b1));
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
 };
 template <>
@@ -267,9 +267,10 @@ struct PairSum<__half> {
     static constexpr int kParts = 2;
     static constexpr float kScale = 0x1p14f;  // 8 times a sum of 128 values of 2^15 is 2^25 kUnit kScale = 2^15
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_f16(lo, hi); }
-    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t *a, uint32_t a1, uint32_t a3, uint32_t b0, uint32_t b1)
+    template <bool kFirst>
+    static __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
     {
-        mma_f16<false>(c, a[0], a1, a[1], a3, b0, b1);
+        mma_f16<kFirst>(c, a[0], a[1], a[2], a[3], b0, b1);
     }
 };
 
@@ -410,20 +411,19 @@ struct Feed {
 };
 
 // ---------------------------------------------------------------- one piece of work of a warp
-// Lane 4 r + q. Scores: rows r and r + 8 (halves 0 and 1), of eight tokens 2 q and 2 q + 1. Sums of the output:
-// columns 4 r .. 4 r + 3 of every 32, rows 2 q and 2 q + 1 of a half.
+// Lane 4 r + q. Scores of 16 tokens: tokens r and r + 8, query rows 2 q and 2 q + 1 of each half. Sums of the output:
+// columns 4 r .. 4 r + 3 of every 32, the same rows. All that belongs to a row lies in its lanes, eight times over.
 template <class T, class F>
 struct Rows {
     // mma that multiply the groups' sums of queries: eight pairs of a token each
     static constexpr int kSums = (PairSum<T>::kParts * F::kGroups + 7) / 8;
-    uint32_t qf[F::kGroups][F::kWords][2][2 * F::kHalves];  // queries as mma fragments
-    uint32_t qsum[kSums][2 * F::kHalves];             // fragments of a group's sum of scaled queries, times kUnit
-    float f[F::kHalves];                                    // from a score in units to its log2
-    float ref[F::kHalves];                                  // A
+    uint32_t qf[F::kGroups][F::kWords][2][2][F::kHalves];   // queries as mma fragments
+    uint32_t qsum[kSums][2][F::kHalves];                    // fragments of a group's sum of scaled queries, times kUnit
+    float2 f[F::kHalves];                                   // from a score in units to its log2
+    float2 ref[F::kHalves];                                 // A
     float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
     float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
     float eights[(F::kGroups + 1) / 2][F::kHalves][4];      // of 8 p s, in units: a group in c0 c1, the next in c2 c3
-    uint32_t pieces[4];                                     // of values: two pieces of 16 tokens
 
     __device__ __forceinline__ void start(const Kv4Attend &a, const AttendPlan &plan, int b, int head, int row0, int lane)
     {
@@ -452,8 +452,9 @@ struct Rows {
             const float by = copysignf(power_of_2(14 - e), a.scale), by16 = 0.0625f * by;
             float all[F::kGroups];
             const int half = (e + 10) / 2;
-            f[h] = fminf(__fmul_rn(__fmul_rn(__fmul_rn(fabsf(a.scale), 1.4426950408889634f), power_of_2(half)),
+            const float to_log2 = fminf(__fmul_rn(__fmul_rn(__fmul_rn(fabsf(a.scale), 1.4426950408889634f), power_of_2(half)),
                                    power_of_2(e + 10 - half)), 3.0e38f);
+            f[h] = make_float2(__shfl_sync(kFull, to_log2, 8 * q), __shfl_sync(kFull, to_log2, 8 * q + 4));
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++) {
                 float total_q = 0.0f;
@@ -468,8 +469,8 @@ struct Rows {
                     }
 #pragma unroll
                     for (int m = 0; m < 2; m++) {
-                        qf[g][w][m][h] = pack_f16(__fmul_rn(v[2 * m], by), __fmul_rn(v[2 * m + 4], by));
-                        qf[g][w][m][F::kHalves + h] = pack_f16(__fmul_rn(v[2 * m + 1], by16), __fmul_rn(v[2 * m + 5], by16));
+                        qf[g][w][m][0][h] = pack_f16(__fmul_rn(v[2 * m], by), __fmul_rn(v[2 * m + 4], by));
+                        qf[g][w][m][1][h] = pack_f16(__fmul_rn(v[2 * m + 1], by16), __fmul_rn(v[2 * m + 5], by16));
                     }
                 }
                 total_q = __fadd_rn(total_q, __shfl_xor_sync(kFull, total_q, 1));
@@ -492,9 +493,9 @@ struct Rows {
                         if (i == part) value = v;
                         rest = __fsub_rn(rest, v);
                     }
-                    qsum[m][F::kHalves * j + h] = PairSum<T>::pack(-8.0f * value, value);
+                    qsum[m][j][h] = PairSum<T>::pack(-8.0f * value, value);
                 }
-            ref[h] = kNothing;
+            ref[h] = splat(kNothing);
             total[h] = splat(0.0f);
 #pragma unroll
             for (int m = 0; m < F::kDim / 16; m++)
@@ -507,71 +508,86 @@ struct Rows {
         }
     }
 
-    // x in units of tokens 8 n + 2 q and the next
-    __device__ __forceinline__ void scores(uint32_t stage, int lane, float2 (&x)[4][F::kHalves])
+    // x[n][t]: in units, of token 16 n + 8 t + r
+    __device__ __forceinline__ void scores(uint32_t stage, int lane, float2 (&x)[2][2][F::kHalves])
     {
-        constexpr int kLast = F::kHalves - 1;
         const int r = lane >> 2, q = lane & 3;
-        const uint32_t pairs = stage + 2 * F::kCodeBytes;
+        const uint32_t pairs = stage + 2 * F::kCodeBytes + 4 * F::kGroups * r;
 #pragma unroll
-        for (int n = 0; n < 4; n++) {
-            // word q of every piece of token 8 n + r
-            uint32_t w[F::kChunks];
-            const int row = 8 * n + (lane & 7);
+        for (int n = 0; n < 2; n++) {
+            // word q of every piece of tokens r and r + 8: w[2 piece], w[2 piece + 1]
+            uint32_t w[2 * F::kChunks];
+            const int row = 16 * n + (lane & 15);
 #pragma unroll
-            for (int i = 0; i + 4 <= F::kChunks; i += 4) load_matrices(stage + 16 * chunk_at<F::kDim>(row, i + (lane >> 3)), w + i);
-            if constexpr (F::kChunks % 4 != 0)
-                load_two_matrices(stage + 16 * chunk_at<F::kDim>(row, F::kChunks - 2 + ((lane >> 3) & 1)), w + F::kChunks - 2);
-            uint32_t pw[2 * F::kGroups];
-            lds_words<2 * F::kGroups>(pairs + 4 * F::kGroups * (8 * n + 2 * q), pw);
-            float c[4] = {};
+            for (int i = 0; i < F::kChunks; i += 2)
+                load_matrices(stage + 16 * chunk_at<F::kDim>(row, i + (lane >> 4)), w + 2 * i);
+            uint32_t pw[2][F::kGroups];
+#pragma unroll
+            for (int t = 0; t < 2; t++) lds_words<F::kGroups>(pairs + 4 * F::kGroups * (16 * n + 8 * t), pw[t]);
+            float c[F::kHalves][4];
             {
                 constexpr bool kOne = 4 % F::kGroups == 0, kTwo = F::kGroups == 8;  // words that all slots share
-                const uint32_t at = pairs + 4 * F::kGroups * (8 * n + r);
-                const uint32_t b0 = lds_u32(at + 4 * (q % F::kGroups)), b1 = kTwo ? lds_u32(at + 4 * (4 + q)) : b0;
+                const uint32_t at = pairs + 4 * F::kGroups * 16 * n;
+                uint32_t a[4];
 #pragma unroll
                 for (int m = 0; m < kSums; m++) {
-                    const uint32_t *a = qsum[m];
-                    const uint32_t pair[2] = {a[0], a[F::kHalves]};
-                    const uint32_t first = kOne || kTwo || m == 0 ? b0 : lds_u32(at + 4 * ((8 * m + q) % F::kGroups));
-                    const uint32_t second = kOne || kTwo ? b1 : lds_u32(at + 4 * ((8 * m + 4 + q) % F::kGroups));
-                    PairSum<T>::mma(c, pair, kLast ? a[kLast] : 0u, kLast ? a[F::kHalves + kLast] : 0u, first, second);
-                }
-            }
 #pragma unroll
-            for (int h = 0; h < F::kHalves; h++) {
-                x[n][h] = make_float2(c[2 * h], c[2 * h + 1]);
-                if (PairSum<T>::kScale != 1.0f) x[n][h] = mul2(x[n][h], splat(1.0f / PairSum<T>::kScale));
-            }
+                    for (int i = 0; i < 4; i++) {  // tokens r, r + 8, then their later slots
+                        const int slot = 8 * m + 4 * (i >> 1) + q;
+                        if (m == 0 || !(kOne || kTwo))
+                            a[i] = i >= 2 && kOne ? a[i - 2] : lds_u32(at + 4 * (F::kGroups * 8 * (i & 1) + slot % F::kGroups));
+                    }
 #pragma unroll
-            for (int g = 0; g < F::kGroups; g++) {
-                float d[4];
-#pragma unroll
-                for (int i = 0; i < F::kWords; i++) {
-                    uint32_t u[4];
-                    low_bits(w[g * F::kWords + i], u);
-#pragma unroll
-                    for (int m = 0; m < 2; m++) {
-                        const uint32_t *a = qf[g][i][m];
-                        const uint32_t a1 = kLast ? a[kLast] : 0u, a3 = kLast ? a[F::kHalves + kLast] : 0u;
-                        if (i == 0 && m == 0)
-                            mma_f16<true>(d, a[0], a1, a[F::kHalves], a3, u[0], u[1]);
+                    for (int h = 0; h < F::kHalves; h++) {
+                        if (m == 0)
+                            PairSum<T>::template mma<true>(c[h], a, qsum[m][0][h], qsum[m][1][h]);
                         else
-                            mma_f16<false>(d, a[0], a1, a[F::kHalves], a3, u[2 * m], u[2 * m + 1]);
+                            PairSum<T>::template mma<false>(c[h], a, qsum[m][0][h], qsum[m][1][h]);
                     }
                 }
-                const float2 s = make_float2(pair_values<T>(pw[g]).x, pair_values<T>(pw[F::kGroups + g]).x);
+            }
 #pragma unroll
-                for (int h = 0; h < F::kHalves; h++) x[n][h] = fma2(s, make_float2(d[2 * h], d[2 * h + 1]), x[n][h]);
+            for (int h = 0; h < F::kHalves; h++)
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    x[n][t][h] = make_float2(c[h][2 * t], c[h][2 * t + 1]);
+                    if (PairSum<T>::kScale != 1.0f) x[n][t][h] = mul2(x[n][t][h], splat(1.0f / PairSum<T>::kScale));
+                }
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++) {
+                float d[F::kHalves][4];
+#pragma unroll
+                for (int i = 0; i < F::kWords; i++) {
+                    uint32_t u[4], v[4];
+                    low_bits(w[2 * (g * F::kWords + i)], u);
+                    low_bits(w[2 * (g * F::kWords + i) + 1], v);
+#pragma unroll
+                    for (int m = 0; m < 2; m++)
+#pragma unroll
+                        for (int h = 0; h < F::kHalves; h++) {
+                            const uint32_t b0 = qf[g][i][m][0][h], b1 = qf[g][i][m][1][h];
+                            if (i == 0 && m == 0)
+                                mma_f16<true>(d[h], u[0], v[0], u[1], v[1], b0, b1);
+                            else
+                                mma_f16<false>(d[h], u[2 * m], v[2 * m], u[2 * m + 1], v[2 * m + 1], b0, b1);
+                        }
+                }
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    const float2 s = splat(pair_values<T>(pw[t][g]).x);
+#pragma unroll
+                    for (int h = 0; h < F::kHalves; h++) x[n][t][h] = fma2(s, make_float2(d[h][2 * t], d[h][2 * t + 1]), x[n][t][h]);
+                }
             }
         }
     }
 
-    // A tile's values join the sums. seen: a bit a token for each half's row; kMasked is false where all are set.
+    // A tile's values join the sums. seen: a bit a token for the rows 2 q and 2 q + 1 of each half; kMasked is false where
+    // all are set.
     template <bool kMasked>
-    __device__ __forceinline__ void take(uint32_t stage, int lane, float2 (&x)[4][F::kHalves], const uint32_t (&seen)[F::kHalves])
+    __device__ __forceinline__ void take(uint32_t stage, int lane, float2 (&x)[2][2][F::kHalves], const uint32_t (&seen)[F::kHalves][2])
     {
-        const int q = lane & 3;
+        const int r = lane >> 2;
         const uint32_t pairs = stage + 2 * F::kCodeBytes + F::kPairBytes;
         // log2 of the largest scale of the tile's values; offsets count 2^-24, so that sums of p z stay in range
         int k;
@@ -594,77 +610,83 @@ struct Rows {
             }
             k = __reduce_max_sync(kFull, k);
         }
+        const auto sees = [&](int h, int odd, int n, int t) { return !kMasked || ((seen[h][odd] >> (16 * n + 8 * t + r)) & 1); };
         bool grown = false;
-        float now[F::kHalves];
+        float2 now[F::kHalves];
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
-            float top = -INFINITY;
+            float2 top = splat(-INFINITY);
 #pragma unroll
-            for (int n = 0; n < 4; n++) {
-                const float lo = !kMasked || ((seen[h] >> (8 * n + 2 * q)) & 1) ? x[n][h].x : -INFINITY;
-                const float hi = !kMasked || ((seen[h] >> (8 * n + 2 * q + 1)) & 1) ? x[n][h].y : -INFINITY;
-                top = fmaxf(top, fmaxf(lo, hi));
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    if (sees(h, 0, n, t)) top.x = fmaxf(top.x, x[n][t][h].x);
+                    if (sees(h, 1, n, t)) top.y = fmaxf(top.y, x[n][t][h].y);
+                }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, d));
+                top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
             }
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-            now[h] = top > -INFINITY ? __fadd_rn(__fmul_rn(top, f[h]), (float)k - kLift) : -INFINITY;
-            grown |= now[h] > __fadd_rn(ref[h], 1.0f);
+            const float up = (float)k - kLift;
+            now[h].x = top.x > -INFINITY ? __fadd_rn(__fmul_rn(top.x, f[h].x), up) : -INFINITY;
+            now[h].y = top.y > -INFINITY ? __fadd_rn(__fmul_rn(top.y, f[h].y), up) : -INFINITY;
+            grown |= now[h].x > __fadd_rn(ref[h].x, 1.0f) || now[h].y > __fadd_rn(ref[h].y, 1.0f);
         }
         if (__any_sync(kFull, grown)) {
 #pragma unroll
             for (int h = 0; h < F::kHalves; h++) {
-                const float next = fmaxf(ref[h], now[h]), keep = exp2_fast(__fsub_rn(ref[h], next));
+                const float2 next = make_float2(fmaxf(ref[h].x, now[h].x), fmaxf(ref[h].y, now[h].y));
+                const float2 keep = make_float2(exp2_fast(__fsub_rn(ref[h].x, next.x)), exp2_fast(__fsub_rn(ref[h].y, next.y)));
                 ref[h] = next;
-                total[h] = mul2(total[h], splat(keep));
+                total[h] = mul2(total[h], keep);
 #pragma unroll
-                for (int g = 0; g < F::kGroups; g++) off[h][g] = mul2(off[h][g], splat(keep));
-                const float even = __shfl_sync(kFull, keep, 8 * q), odd = __shfl_sync(kFull, keep, 8 * q + 4);
+                for (int g = 0; g < F::kGroups; g++) off[h][g] = mul2(off[h][g], keep);
 #pragma unroll
                 for (int m = 0; m < F::kDim / 16; m++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? odd : even);
+                    for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? keep.y : keep.x);
 #pragma unroll
                 for (int g = 0; g < (F::kGroups + 1) / 2; g++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? odd : even);
+                    for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? keep.y : keep.x);
             }
         }
 #pragma unroll
-        for (int n = 0; n < 4; n++)
+        for (int n = 0; n < 2; n++)
 #pragma unroll
-            for (int h = 0; h < F::kHalves; h++) {
-                const float2 y = fma2(x[n][h], splat(f[h]), splat(-ref[h]));
-                float2 &p = x[n][h];
-                p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                if (kMasked) {
-                    if (!((seen[h] >> (8 * n + 2 * q)) & 1)) p.x = 0.0f;
-                    if (!((seen[h] >> (8 * n + 2 * q + 1)) & 1)) p.y = 0.0f;
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    const float2 y = fma2(x[n][t][h], f[h], make_float2(-ref[h].x, -ref[h].y));
+                    float2 &p = x[n][t][h];
+                    p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                    if (!sees(h, 0, n, t)) p.x = 0.0f;
+                    if (!sees(h, 1, n, t)) p.y = 0.0f;
+                    total[h] = add2(total[h], p);
                 }
-                total[h] = add2(total[h], p);
-            }
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            uint32_t pw[2][2 * F::kGroups];
+        for (int n = 0; n < 2; n++) {
+            uint32_t pw[2][F::kGroups], codes[4];
 #pragma unroll
-            for (int n = 0; n < 2; n++) lds_words<2 * F::kGroups>(pairs + 4 * F::kGroups * (16 * i + 8 * n + 2 * q), pw[n]);
+            for (int t = 0; t < 2; t++) lds_words<F::kGroups>(pairs + 4 * F::kGroups * (16 * n + 8 * t + r), pw[t]);
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++) {
                 uint32_t b[F::kHalves][2];
 #pragma unroll
-                for (int n = 0; n < 2; n++) {
-                    const float2 one = pair_values<T>(pw[n][g]), two = pair_values<T>(pw[n][F::kGroups + g]);
-                    const float2 s = make_float2(one.x, two.x), z = make_float2(one.y, two.y);
+                for (int t = 0; t < 2; t++) {
+                    const float2 pair = pair_values<T>(pw[t][g]);
 #pragma unroll
                     for (int h = 0; h < F::kHalves; h++) {
-                        const float2 p = x[2 * i + n][h];
-                        float2 sh = s, zh = z;
+                        const float2 p = x[n][t][h];
+                        float2 s = splat(pair.x), z = splat(pair.y);
                         if (kMasked) {  // a row that does not see a token takes nothing of it, a NaN neither
-                            if (!((seen[h] >> (16 * i + 8 * n + 2 * q)) & 1)) sh.x = zh.x = 0.0f;
-                            if (!((seen[h] >> (16 * i + 8 * n + 2 * q + 1)) & 1)) sh.y = zh.y = 0.0f;
+                            if (!sees(h, 0, n, t)) s.x = z.x = 0.0f;
+                            if (!sees(h, 1, n, t)) s.y = z.y = 0.0f;
                         }
-                        const float2 ps = mul2(p, sh);
-                        b[h][n] = pack_f16(ps.x, ps.y);
-                        off[h][g] = fma2(p, zh, off[h][g]);
+                        const float2 ps = mul2(p, s);
+                        b[h][t] = transposed(pack_f16(ps.x, ps.y));
+                        off[h][g] = fma2(p, z, off[h][g]);
                     }
                 }
 #pragma unroll
@@ -675,14 +697,15 @@ struct Rows {
                     else
                         mma_f16<false>(eights[g / 2][h], kEight, 0u, kEight, 0u, b[h][0], b[h][1]);
                 }
-                values(stage + F::kCodeBytes, lane, i, g, b);
+                values(stage + F::kCodeBytes, lane, n, g, b, codes);
             }
         }
     }
 
     // The codes of 16 tokens in group g against b. A transposed matrix of eight tokens and one piece gives a lane four
     // columns' codes of two tokens, side by side as a fragment of the values takes them.
-    __device__ __forceinline__ void values(uint32_t codes, int lane, int i, int g, const uint32_t (&b)[F::kHalves][2])
+    __device__ __forceinline__ void values(uint32_t codes, int lane, int i, int g, const uint32_t (&b)[F::kHalves][2],
+                                           uint32_t (&pieces)[4])
     {
 #pragma unroll
         for (int k = 0; k < F::kWords; k++) {
@@ -699,21 +722,21 @@ struct Rows {
         }
     }
 
-    // Sums of quads brought together: total in every lane of a row's quad, sum the true sums of p v.
-    __device__ __forceinline__ void finish(int lane)
+    // The lanes' parts brought together: total in every lane of a row, sum the true sums of p v.
+    __device__ __forceinline__ void finish()
     {
-        const int q = lane & 3;
+        const auto all = [](float2 v) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+                v = add2(v, make_float2(__shfl_xor_sync(kFull, v.x, d), __shfl_xor_sync(kFull, v.y, d)));
+            return v;
+        };
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
-            float t = __fadd_rn(total[h].x, total[h].y);
-            t = __fadd_rn(t, __shfl_xor_sync(kFull, t, 1));
-            total[h].x = __fadd_rn(t, __shfl_xor_sync(kFull, t, 2));
+            total[h] = all(total[h]);
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++) {
-                float z = __fadd_rn(off[h][g].x, off[h][g].y);
-                z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 1));
-                z = __fadd_rn(z, __shfl_xor_sync(kFull, z, 2));
-                const float even = __shfl_sync(kFull, z, 8 * q), odd = __shfl_sync(kFull, z, 8 * q + 4);
+                const float2 z = all(off[h][g]);
 #pragma unroll
                 for (int k = 0; k < F::kGroup / 16; k++) {
                     float(&v)[4] = sum[g * (F::kGroup / 16) + k][h];
@@ -721,7 +744,7 @@ struct Rows {
                     for (int i = 0; i < 4; i++) {
                         const float u = k & 1 ? __fmul_rn(v[i], 0.0625f) : v[i];
                         const float c = eights[g / 2][h][2 * (g & 1) + (i & 1)];
-                        v[i] = __fmaf_rn(__fsub_rn(u, c), 1.0f / kUnit, i & 1 ? odd : even);
+                        v[i] = __fmaf_rn(__fsub_rn(u, c), 1.0f / kUnit, i & 1 ? z.y : z.x);
                     }
                 }
             }
@@ -772,7 +795,10 @@ struct Join {
         const int r = lane >> 2, q = lane & 3;
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
-            if (q == 0) to[8 * h + r] = x.ref[h], to[F::kRows + 8 * h + r] = x.total[h].x;
+            if (r == 0) {
+                *reinterpret_cast<float2 *>(to + 8 * h + 2 * q) = x.ref[h];
+                *reinterpret_cast<float2 *>(to + F::kRows + 8 * h + 2 * q) = x.total[h];
+            }
 #pragma unroll
             for (int odd = 0; odd < 2; odd++)
 #pragma unroll
@@ -786,13 +812,15 @@ struct Join {
         const int r = lane >> 2, q = lane & 3;
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
-            const float other = from[8 * h + r], next = fmaxf(x.ref[h], other);
-            const float mine = exp2_fast(__fsub_rn(x.ref[h], next)), theirs = exp2_fast(__fsub_rn(other, next));
+            const float2 other = *reinterpret_cast<const float2 *>(from + 8 * h + 2 * q), ref = x.ref[h];
+            const float2 next = make_float2(fmaxf(ref.x, other.x), fmaxf(ref.y, other.y));
+            const float2 mine = make_float2(exp2_fast(__fsub_rn(ref.x, next.x)), exp2_fast(__fsub_rn(ref.y, next.y)));
+            const float2 theirs = make_float2(exp2_fast(__fsub_rn(other.x, next.x)), exp2_fast(__fsub_rn(other.y, next.y)));
             x.ref[h] = next;
-            x.total[h].x = __fmaf_rn(from[F::kRows + 8 * h + r], theirs, __fmul_rn(x.total[h].x, mine));
+            x.total[h] = fma2(*reinterpret_cast<const float2 *>(from + F::kRows + 8 * h + 2 * q), theirs, mul2(x.total[h], mine));
 #pragma unroll
             for (int odd = 0; odd < 2; odd++) {
-                const float m = __shfl_sync(kFull, mine, 8 * q + 4 * odd), t = __shfl_sync(kFull, theirs, 8 * q + 4 * odd);
+                const float m = odd ? mine.y : mine.x, t = odd ? theirs.y : theirs.x;
 #pragma unroll
                 for (int k = 0; k < kRuns; k++) {
                     const float4 v = *reinterpret_cast<const float4 *>(from + 2 * F::kRows + (8 * h + 2 * q + odd) * F::kDim +
@@ -845,12 +873,13 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
         const int head = (int)divide_by(now.item, plan.by_chunks), row0 = (now.item - head * plan.chunks) * F::kRows;
         x.start(a, plan, now.b, head, row0, lane);
         // the positions that the lane's rows see, and that all rows of the item do
-        int lo[F::kHalves], hi[F::kHalves];
+        int lo[F::kHalves][2], hi[F::kHalves][2];
 #pragma unroll
-        for (int h = 0; h < F::kHalves; h++) {
-            const int row = min(row0 + (lane >> 2) + 8 * h, plan.rows - 1);
-            hi[h] = now.end - a.n_q + 1 + (int)divide_by(row, plan.by_share);
-            lo[h] = a.window > 0 && hi[h] > a.window ? hi[h] - a.window : 0;
+        for (int i = 0; i < 2 * F::kHalves; i++) {
+            const int row = min(row0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1), plan.rows - 1);
+            int &end = hi[i >> 1][i & 1];
+            end = now.end - a.n_q + 1 + (int)divide_by(row, plan.by_share);
+            lo[i >> 1][i & 1] = a.window > 0 && end > a.window ? end - a.window : 0;
         }
         const int all_hi = now.end - a.n_q + 1 + (int)divide_by(row0, plan.by_share);
         const int last_hi = now.end - a.n_q + 1 + (int)divide_by(min(row0 + F::kRows, plan.rows) - 1, plan.by_share);
@@ -863,24 +892,22 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
             feed.issue(c, a, plan, lane, ring + fill * F::kStage, &valid[warp][fill]);
             if (++slot == F::kStages) slot = 0;
             const int at = now.begin + t * kTokens;
-            float2 s[4][F::kHalves];
+            float2 s[2][2][F::kHalves];
             x.scores(stage, lane, s);
-            uint32_t seen[F::kHalves];
+            uint32_t seen[F::kHalves][2];
             if (there == kFull && at >= all_lo && at + kTokens <= all_hi) {
-#pragma unroll
-                for (int h = 0; h < F::kHalves; h++) seen[h] = kFull;
                 x.template take<false>(stage, lane, s, seen);
             } else {
 #pragma unroll
-                for (int h = 0; h < F::kHalves; h++) {
-                    const int from = max(lo[h] - at, 0), to = min(hi[h] - at, kTokens);
+                for (int i = 0; i < 2 * F::kHalves; i++) {
+                    const int from = max(lo[i >> 1][i & 1] - at, 0), to = min(hi[i >> 1][i & 1] - at, kTokens);
                     const uint32_t above = from < kTokens ? kFull << from : 0u, below = to <= 0 ? 0u : kFull >> (kTokens - to);
-                    seen[h] = there & above & below;
+                    seen[i >> 1][i & 1] = there & above & below;
                 }
                 x.template take<true>(stage, lane, s, seen);
             }
         }
-        x.finish(lane);
+        x.finish();
         // warps 2 and 3 to 0 and 1, then 1 to 0; the last step's place is read by warp 0 before the next item's first
         // barrier, and the first step's before this item's second
         if (warp >= 2) J::put(x, joins + (warp - 2) * kPartial, lane);
@@ -894,19 +921,15 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
             if (now.tile == 0 && last == now.tiles) {
 #pragma unroll
                 for (int h = 0; h < F::kHalves; h++) {
-                    const float inv = x.total[h].x == 0.0f ? 0.0f : __fdiv_rn(1.0f, x.total[h].x);
-                    if (q == 0 && a.lse && row0 + 8 * h + r < plan.rows) {
-                        int64_t at;
-                        out_row(a, plan, now.b, head, row0 + 8 * h + r, &at);
-                        if (dbg_ok(a.lse + at, 4, true)) a.lse[at] = lse_of(x.ref[h], x.total[h].x);
-                    }
 #pragma unroll
                     for (int odd = 0; odd < 2; odd++) {
                         const int row = row0 + 8 * h + 2 * q + odd;
-                        const float by = __shfl_sync(kFull, inv, 8 * q + 4 * odd);
-                        int64_t unused;
+                        const float total = odd ? x.total[h].y : x.total[h].x, by = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
                         if (row < plan.rows) {
-                            T *to = static_cast<T *>(a.out) + out_row(a, plan, now.b, head, row, &unused);
+                            int64_t at;
+                            T *to = static_cast<T *>(a.out) + out_row(a, plan, now.b, head, row, &at);
+                            if (r == 0 && a.lse && dbg_ok(a.lse + at, 4, true))
+                                a.lse[at] = lse_of(odd ? x.ref[h].y : x.ref[h].x, total);
 #pragma unroll
                             for (int k = 0; k < J::kRuns; k++) {
                                 const float4 v = J::run_of(x, k, h, odd);
@@ -926,8 +949,10 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                 }
 #pragma unroll
                 for (int h = 0; h < F::kHalves; h++) {
-                    if (q == 0 && dbg_ok(to + 8 * h + r, 4, true)) to[8 * h + r] = x.ref[h];
-                    if (q == 0 && dbg_ok(to + F::kRows + 8 * h + r, 4, true)) to[F::kRows + 8 * h + r] = x.total[h].x;
+                    if (r == 0) {
+                        st_v2(to + 8 * h + 2 * q, make_uint2(__float_as_uint(x.ref[h].x), __float_as_uint(x.ref[h].y)));
+                        st_v2(to + F::kRows + 8 * h + 2 * q, make_uint2(__float_as_uint(x.total[h].x), __float_as_uint(x.total[h].y)));
+                    }
 #pragma unroll
                     for (int odd = 0; odd < 2; odd++)
 #pragma unroll
