@@ -11,87 +11,104 @@ __device__ __forceinline__ uint4 ld_plain_v4(const float *p)
     return *reinterpret_cast<const uint4 *>(p);
 }
 
-// A CTA four rows of an item that goes on after share blockIdx.x / groups, if there is one. A thread takes four columns of one
-// row, of every kGroups-th part.
-constexpr int kJoinRows = 4, kJoinThreads = 512;
+// CTA i takes rows of the item that word i / splits names, if more than one share worked on it: all of them, or where there
+// are few items (a long sequence or two, with many parts each) a few, down to one. A thread takes four columns of one row, of
+// every groups-th part.
+constexpr int kJoinThreads = 512;
 
 template <class T, int kDim>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ Kv4Cache c,
                                                                   const __grid_constant__ Kv4Attend a,
-                                                                  const __grid_constant__ AttendPlan plan, int form, int groups)
+                                                                  const __grid_constant__ AttendPlan plan, int form, int per, int splits)
 {
-    constexpr int kGroups = kJoinThreads / kDim;
-    __shared__ float weight[kJoinRows][kMaxAttendCtas + 1], refs[kJoinRows], totals[kJoinRows];
-    __shared__ float4 sums[kGroups][kDim];
+    constexpr int kAhead = 4;  // parts that a thread loads before the weights are known
+    __shared__ float refs[16], totals[16];
+    __shared__ float4 sums[kJoinThreads];
     const int64_t floats = partial_floats(form, kDim);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_begin();
     dbg_attend(c, a, plan, floats);
-    const int cta = blockIdx.x / groups, row0 = (blockIdx.x - cta * groups) * kJoinRows;
-    const uint4 word = ld_plain_v4(a.workspace + 4 * cta);
-    const Split at = {(int)word.x, (int)word.y, (int)word.z, 0};
-    const int head = (int)divide_by(at.item, plan.by_chunks), first = (at.item - head * plan.chunks) * form + row0;
-    const int rows = min(min(form - row0, plan.rows - first), kJoinRows);
-    if (at.parts == 0 || rows <= 0) return;
-    // share `cta` left it as what goes on after it, the others as what began before them
-    const auto part = [&](int i) { return partial_of(a.workspace, cta + i, i == 0, floats); };
+    const uint4 word = ld_plain_v4(a.workspace + 4 * (blockIdx.x / splits));
+    const int parts = (int)word.z;
+    if (parts < 2) return;
+    const int width = per * (kDim / 4), groups = kJoinThreads / width;
+    const int group = threadIdx.x / width, in = threadIdx.x - group * width, row = in / (kDim / 4), col = 4 * (in - row * (kDim / 4));
     const auto load = [&](const float *p) { return dbg_ok(p, 4, false) ? *p : 0.0f; };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = (int)word.x, item = (int)word.y, cta = (int)word.w, row0 = blockIdx.x % splits * per;
+    const int head = (int)divide_by(item, plan.by_chunks), first = (item - head * plan.chunks) * form + row0;
+    const int rows = min(min(plan.rows - first, form - row0), per);
+    if (rows <= 0) return;
+    // the share left it as what goes on after it, the others as what began before them
+    const auto part = [&](int i) { return partial_of(a.workspace, cta + i, i == 0, floats); };
+    const bool busy = group < groups && row < rows;
+    const auto piece = [&](int i) { return ld_plain_v4(part(i) + 2 * form + (row0 + row) * kDim + col); };
+    uint4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; k++)
+        if (busy && group + k * groups < parts) v[k] = piece(group + k * groups);
     if (warp < rows) {
         float ref = kNothing, total = 0.0f;
-        for (int i = lane; i < at.parts; i += 32) {
-            const float r = load(part(i) + row0 + warp);
-            weight[warp][i] = r;
-            ref = fmaxf(ref, r);
+#pragma unroll 4
+        for (int i = lane; i < parts; i += 32) {
+            const float r = load(part(i) + row0 + warp), t = load(part(i) + form + row0 + warp), next = fmaxf(ref, r);
+            total = __fmaf_rn(t, exp2_fast(__fsub_rn(r, next)), __fmul_rn(total, exp2_fast(__fsub_rn(ref, next))));
+            ref = next;
         }
 #pragma unroll
-        for (int d = 16; d; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(kFull, ref, d));
-        for (int i = lane; i < at.parts; i += 32) {
-            const float by = exp2_fast(__fsub_rn(weight[warp][i], ref));
-            weight[warp][i] = by;
-            total = __fmaf_rn(load(part(i) + form + row0 + warp), by, total);
+        for (int d = 16; d; d >>= 1) {
+            const float r = __shfl_xor_sync(kFull, ref, d), t = __shfl_xor_sync(kFull, total, d), next = fmaxf(ref, r);
+            total = __fadd_rn(__fmul_rn(t, exp2_fast(__fsub_rn(r, next))), __fmul_rn(total, exp2_fast(__fsub_rn(ref, next))));
+            ref = next;
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) total = __fadd_rn(total, __shfl_xor_sync(kFull, total, d));
         if (lane == 0) refs[warp] = ref, totals[warp] = total;
     }
     __syncthreads();
-    const int group = threadIdx.x / kDim, in = threadIdx.x - group * kDim, row = in / (kDim / 4), col = 4 * (in - row * (kDim / 4));
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (group < kGroups && row < rows) {
-#pragma unroll 8
-        for (int i = group; i < at.parts; i += kGroups) {
-            const uint4 v = ld_plain_v4(part(i) + 2 * form + (row0 + row) * kDim + col);
-            const float by = weight[row][i];
+    if (busy) {
+        const float ref = refs[row];
+        const auto add = [&](int i, uint4 v) {
+            const float by = exp2_fast(__fsub_rn(load(part(i) + row0 + row), ref));
             sum = make_float4(__fmaf_rn(__uint_as_float(v.x), by, sum.x), __fmaf_rn(__uint_as_float(v.y), by, sum.y),
                               __fmaf_rn(__uint_as_float(v.z), by, sum.z), __fmaf_rn(__uint_as_float(v.w), by, sum.w));
-        }
-        sums[group][in] = sum;
-    }
-    __syncthreads();
-    if (group != 0 || row >= rows) return;
+        };
 #pragma unroll
-    for (int i = 1; i < kGroups; i++) {
-        const float4 v = sums[i][in];
-        sum = make_float4(__fadd_rn(sum.x, v.x), __fadd_rn(sum.y, v.y), __fadd_rn(sum.z, v.z), __fadd_rn(sum.w, v.w));
+        for (int k = 0; k < kAhead; k++)
+            if (group + k * groups < parts) add(group + k * groups, v[k]);
+#pragma unroll 4
+        for (int i = group + kAhead * groups; i < parts; i += groups) add(i, piece(i));
     }
-    int64_t at_lse;
-    T *to = static_cast<T *>(a.out) + out_row(a, plan, at.b, head, first + row, &at_lse);
-    const float total = totals[row], inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-    st_v2(to + col, make_uint2(Value<T>::round2(__fmul_rn(sum.x, inv), __fmul_rn(sum.y, inv)),
-                               Value<T>::round2(__fmul_rn(sum.z, inv), __fmul_rn(sum.w, inv))));
-    if (a.lse && col == 0 && dbg_ok(a.lse + at_lse, 4, true)) a.lse[at_lse] = lse_of(refs[row], total);
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    if (group == 0 && row < rows) {
+        for (int i = 1; i < groups; i++) {
+            const float4 v = sums[i * width + in];
+            sum = make_float4(__fadd_rn(sum.x, v.x), __fadd_rn(sum.y, v.y), __fadd_rn(sum.z, v.z), __fadd_rn(sum.w, v.w));
+        }
+        int64_t at_lse;
+        T *to = static_cast<T *>(a.out) + out_row(a, plan, b, head, first + row, &at_lse);
+        const float total = totals[row], inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+        st_v2(to + col, make_uint2(Value<T>::round2(__fmul_rn(sum.x, inv), __fmul_rn(sum.y, inv)),
+                                   Value<T>::round2(__fmul_rn(sum.z, inv), __fmul_rn(sum.w, inv))));
+        if (a.lse && col == 0 && dbg_ok(a.lse + at_lse, 4, true)) a.lse[at_lse] = lse_of(refs[row], total);
+    }
 }
 
 template <class T>
 cudaError_t launch_join(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, cudaStream_t st)
 {
-    void (*kernel)(Kv4Cache, Kv4Attend, AttendPlan, int, int) = c.head_dim == 64    ? attend_join_kernel<T, 64>
+    void (*kernel)(Kv4Cache, Kv4Attend, AttendPlan, int, int, int) = c.head_dim == 64    ? attend_join_kernel<T, 64>
                                                                 : c.head_dim == 128 ? attend_join_kernel<T, 128>
                                                                 : c.head_dim == 192 ? attend_join_kernel<T, 192>
                                                                                     : attend_join_kernel<T, 256>;
     const int form = form_rows(plan.rows, c.head_dim);
-    const int groups = ((plan.rows < form ? plan.rows : form) + kJoinRows - 1) / kJoinRows;
-    return launch_kernel_block(kernel, (plan.ctas - 1) * groups, kJoinThreads, 0, st, c, a, plan, form, groups);
+    int sms = 0;
+    if (cudaError_t e = sm_count(&sms)) return e;
+    const int rows = plan.rows < form ? plan.rows : form;
+    int splits = 1;  // as many as run at once
+    while (splits < rows && 2 * splits * plan.words <= 4 * sms) splits *= 2;
+    const int per = (rows + splits - 1) / splits;
+    splits = (rows + per - 1) / per;
+    return launch_kernel_block(kernel, plan.words * splits, kJoinThreads, 0, st, c, a, plan, form, per, splits);
 }
 
 }  // namespace

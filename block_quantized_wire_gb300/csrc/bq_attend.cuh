@@ -43,6 +43,8 @@ constexpr int kMaxAttendCtas = 608;               // four on each of 152 SMs
 struct AttendPlan {
     int rows, share, chunks, items;  // query rows and query heads of a key-value head; items = heads * chunks
     int ctas;                        // of the launch
+    int words;                       // of the workspace that say which items are joined: one an item, or else one a CTA
+    bool by_item;
     Divisor by_share, by_page, by_chunks;
 };
 
@@ -135,12 +137,10 @@ __device__ __forceinline__ void find_share(const Kv4Cache &c, const Kv4Attend &a
     spot = found;
 }
 
-// The workspace: a word a CTA that says whether an item goes on after its share and how many shares take part, then two
-// partial sums a CTA (an item that began before its share, one that goes on after it): [kRows] references, [kRows]
-// totals, [kRows][kDim] sums.
-struct Split {
-    int b, item, parts, unused;
-};
+// The workspace: words, then two partial sums a CTA (an item that began before its share, one that goes on after it):
+// [kRows] references, [kRows] totals, [kRows][kDim] sums. Word i is item i's, written by the CTA that begins it, where
+// a call has at most kMaxAttendCtas items; else CTA i's, for the item that goes on after its share. It says whose item, on how
+// many shares, from which one.
 __host__ __device__ __forceinline__ int64_t partial_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
 __host__ __device__ __forceinline__ float *partial_of(float *workspace, int cta, bool goes_on, int64_t floats)
 {
@@ -356,25 +356,23 @@ struct Feed {
                 const int64_t page = __shfl_sync(kFull, entry, 0);
                 const int64_t at = page * c.page_stride + at_head + first * c.token_stride;
                 const int64_t at_s = page * c.page_stride_s + at_head_s + place * c.token_stride_s;
-                if constexpr (32 % F::kChunks == 0) {
-                    const int t0 = lane / F::kChunks, ch = lane % F::kChunks;
-                    const int64_t step = 32 / F::kChunks * c.token_stride;
-                    const uint8_t *k = c.k + at + t0 * c.token_stride + 16 * ch, *v = c.v + (k - c.k);
+                const uint8_t *const k = c.k + at, *const v = c.v + at;
+                if (c.token_stride == F::kDim / 2) {  // one run of bytes
 #pragma unroll
                     for (int i = 0; i < F::kChunks; i++) {
-                        const uint32_t to = stage + 16 * chunk_at<F::kDim>(32 / F::kChunks * i + t0, ch);
-                        lane_copy16(to, k);
-                        lane_copy16(to + F::kCodeBytes, v);
-                        k += step, v += step;
+                        const int piece = 32 * i + lane;
+                        const uint32_t to = stage + 16 * chunk_at<F::kDim>(piece / F::kChunks, piece % F::kChunks);
+                        lane_copy16(to, k + 16 * lane + 512 * i);
+                        lane_copy16(to + F::kCodeBytes, v + 16 * lane + 512 * i);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < F::kChunks; i++) {
                         const int piece = 32 * i + lane, t = piece / F::kChunks, ch = piece % F::kChunks;
-                        const int64_t from = at + t * c.token_stride + 16 * ch;
+                        const int64_t from = t * c.token_stride + 16 * ch;
                         const uint32_t to = stage + 16 * chunk_at<F::kDim>(t, ch);
-                        lane_copy16(to, c.k + from);
-                        lane_copy16(to + F::kCodeBytes, c.v + from);
+                        lane_copy16(to, k + from);
+                        lane_copy16(to + F::kCodeBytes, v + from);
                     }
                 }
 #pragma unroll
@@ -421,30 +419,41 @@ struct Rows {
     uint32_t qsum[kSums][2][F::kHalves];                    // fragments of a group's sum of scaled queries, times kUnit
     float2 f[F::kHalves];                                   // from a score in units to its log2
     float2 ref[F::kHalves];                                 // A
+    int level;                                              // log2 of the largest scale so far
     float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
     float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
     float eights[(F::kGroups + 1) / 2][F::kHalves][4];      // of 8 p s, in units: a group in c0 c1, the next in c2 c3
 
-    __device__ __forceinline__ void start(const Kv4Attend &a, const AttendPlan &plan, int b, int head, int row0, int lane)
+    // The lane's queries of an item.
+    using Queries = uint4[F::kHalves][F::kChunks];
+    static __device__ __forceinline__ void fetch(const Kv4Attend &a, const AttendPlan &plan, int b, int head, int row0, int lane,
+                                                 Queries &raw)
     {
         const int r = lane >> 2, q = lane & 3;
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
             const int row = row0 + r + 8 * h;
-            uint4 raw[F::kGroups][F::kWords];
             const int i = (int)divide_by(row < plan.rows ? row : 0, plan.by_share), in = (row < plan.rows ? row : 0) - i * plan.share;
             const T *from = static_cast<const T *>(a.q) + b * a.q_batch + i * a.q_query +
                             (int64_t)(head * plan.share + in) * a.q_head + 8 * q;
+#pragma unroll
+            for (int w = 0; w < F::kChunks; w++) raw[h][w] = row < plan.rows ? ld_keep_v4(from + 32 * w) : make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    __device__ __forceinline__ void start(const Kv4Attend &a, int lane, const Queries &raw)
+    {
+        level = -60;
+        const int q = lane & 3;
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) {
             uint32_t top = 0;
 #pragma unroll
-            for (int g = 0; g < F::kGroups; g++)
-#pragma unroll
-                for (int w = 0; w < F::kWords; w++) {
-                    uint4 &x = raw[g][w];
-                    x = row < plan.rows ? ld_keep_v4(from + g * F::kGroup + 32 * w) : make_uint4(0, 0, 0, 0);
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                                 __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                }
+            for (int w = 0; w < F::kChunks; w++) {
+                const uint4 &x = raw[h][w];
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                             __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+            }
             top = max(top & 0xffffu, top >> 16);
             top = max(top, __shfl_xor_sync(kFull, top, 1));
             top = max(top, __shfl_xor_sync(kFull, top, 2));
@@ -460,7 +469,8 @@ struct Rows {
                 float total_q = 0.0f;
 #pragma unroll
                 for (int w = 0; w < F::kWords; w++) {
-                    const uint32_t u[4] = {raw[g][w].x, raw[g][w].y, raw[g][w].z, raw[g][w].w};
+                    const uint4 &x = raw[h][g * F::kWords + w];
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                     float v[8];
 #pragma unroll
                     for (int k = 0; k < 8; k++) {
@@ -589,7 +599,7 @@ struct Rows {
     {
         const int r = lane >> 2;
         const uint32_t pairs = stage + 2 * F::kCodeBytes + F::kPairBytes;
-        // log2 of the largest scale of the tile's values; offsets count 2^-24, so that sums of p z stay in range
+        // log2 of the scales of the lane's token among the values; offsets count 2^-24, so that sums of p z stay in range
         int k;
         {
             uint32_t w[F::kGroups];
@@ -608,35 +618,48 @@ struct Rows {
                     if (finite_bits<T>(z)) k = max(k, exponent_of<T>(z) - 23);
                 }
             }
-            k = __reduce_max_sync(kFull, k);
         }
         const auto sees = [&](int h, int odd, int n, int t) { return !kMasked || ((seen[h][odd] >> (16 * n + 8 * t + r)) & 1); };
-        bool grown = false;
-        float2 now[F::kHalves];
-#pragma unroll
-        for (int h = 0; h < F::kHalves; h++) {
-            float2 top = splat(-INFINITY);
+        float2 y[2][2][F::kHalves];
+        float most = -INFINITY;
+        const auto exponents = [&] {
 #pragma unroll
             for (int n = 0; n < 2; n++)
 #pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    if (sees(h, 0, n, t)) top.x = fmaxf(top.x, x[n][t][h].x);
-                    if (sees(h, 1, n, t)) top.y = fmaxf(top.y, x[n][t][h].y);
-                }
+                for (int t = 0; t < 2; t++)
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, d));
-                top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
-            }
-            const float up = (float)k - kLift;
-            now[h].x = top.x > -INFINITY ? __fadd_rn(__fmul_rn(top.x, f[h].x), up) : -INFINITY;
-            now[h].y = top.y > -INFINITY ? __fadd_rn(__fmul_rn(top.y, f[h].y), up) : -INFINITY;
-            grown |= now[h].x > __fadd_rn(ref[h].x, 1.0f) || now[h].y > __fadd_rn(ref[h].y, 1.0f);
-        }
-        if (__any_sync(kFull, grown)) {
+                    for (int h = 0; h < F::kHalves; h++) {
+                        float2 &v = y[n][t][h];
+                        v = fma2(x[n][t][h], f[h], make_float2(-ref[h].x, -ref[h].y));
+                        if (!sees(h, 0, n, t)) v.x = -INFINITY;
+                        if (!sees(h, 1, n, t)) v.y = -INFINITY;
+                        most = max3f(most, v.x, v.y);
+                    }
+        };
+        exponents();
+        // p s stays within 2^14 as long as no scale passes the level and no p 2^(14 - level): every lane looks at its own
+        // tokens, and the rows' largest scores are looked for where one does
+        if (__any_sync(kFull, most > kLift + 1.0f - (float)level || k > level)) {
+            level = max(level, __reduce_max_sync(kFull, k));
 #pragma unroll
             for (int h = 0; h < F::kHalves; h++) {
-                const float2 next = make_float2(fmaxf(ref[h].x, now[h].x), fmaxf(ref[h].y, now[h].y));
+                float2 top = splat(-INFINITY);
+#pragma unroll
+                for (int n = 0; n < 2; n++)
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        if (sees(h, 0, n, t)) top.x = fmaxf(top.x, x[n][t][h].x);
+                        if (sees(h, 1, n, t)) top.y = fmaxf(top.y, x[n][t][h].y);
+                    }
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, d));
+                    top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
+                }
+                const float up = (float)level - kLift;
+                float2 next = ref[h];
+                if (top.x > -INFINITY) next.x = fmaxf(next.x, __fadd_rn(__fmul_rn(top.x, f[h].x), up));
+                if (top.y > -INFINITY) next.y = fmaxf(next.y, __fadd_rn(__fmul_rn(top.y, f[h].y), up));
                 const float2 keep = make_float2(exp2_fast(__fsub_rn(ref[h].x, next.x)), exp2_fast(__fsub_rn(ref[h].y, next.y)));
                 ref[h] = next;
                 total[h] = mul2(total[h], keep);
@@ -651,6 +674,7 @@ struct Rows {
 #pragma unroll
                     for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? keep.y : keep.x);
             }
+            exponents();
         }
 #pragma unroll
         for (int n = 0; n < 2; n++)
@@ -658,12 +682,8 @@ struct Rows {
             for (int t = 0; t < 2; t++)
 #pragma unroll
                 for (int h = 0; h < F::kHalves; h++) {
-                    const float2 y = fma2(x[n][t][h], f[h], make_float2(-ref[h].x, -ref[h].y));
-                    float2 &p = x[n][t][h];
-                    p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                    if (!sees(h, 0, n, t)) p.x = 0.0f;
-                    if (!sees(h, 1, n, t)) p.y = 0.0f;
-                    total[h] = add2(total[h], p);
+                    x[n][t][h] = make_float2(exp2_fast(y[n][t][h].x), exp2_fast(y[n][t][h].y));  // p from here on
+                    total[h] = add2(total[h], x[n][t][h]);
                 }
 #pragma unroll
         for (int n = 0; n < 2; n++) {
@@ -851,7 +871,7 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
     Share share;
     Spot now;
     find_share(c, a, plan, share, now);
-    if (threadIdx.x == 0) st_v4(a.workspace + 4 * blockIdx.x, make_uint4(0, 0, 0, 0));
+    if (threadIdx.x == 0 && !plan.by_item) st_v4(a.workspace + 4 * blockIdx.x, make_uint4(0, 0, 0, 0));
     if ((int)blockIdx.x >= share.ctas) return;
     const int64_t places = share.first(blockIdx.x + 1) - share.first(blockIdx.x);
 
@@ -871,7 +891,9 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
         const int64_t left = places - now.base;
         const int last = left < now.tiles ? (int)left : now.tiles;  // of the item in this share
         const int head = (int)divide_by(now.item, plan.by_chunks), row0 = (now.item - head * plan.chunks) * F::kRows;
-        x.start(a, plan, now.b, head, row0, lane);
+        typename Rows<T, F>::Queries queries;
+        x.fetch(a, plan, now.b, head, row0, lane, queries);
+        x.start(a, lane, queries);
         // the positions that the lane's rows see, and that all rows of the item do
         int lo[F::kHalves][2], hi[F::kHalves][2];
 #pragma unroll
@@ -907,6 +929,19 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                 x.template take<true>(stage, lane, s, seen);
             }
         }
+        const int b = now.b, item = now.item, rest = now.tiles - last;
+        const bool from_start = now.tile == 0;
+        turn += last - now.tile;
+        now.base = rest ? places : now.base + now.tiles + kSetup;
+        now.tile = 0;
+        if (now.base < places) {
+            if (++now.item == plan.items) {
+                now.item = 0;
+                now.b++;
+                sequence_range(c, a, now.b, now.begin, now.end);
+                now.tiles = tiles_of(now.begin, now.end);
+            }
+        }
         x.finish();
         // warps 2 and 3 to 0 and 1, then 1 to 0; the last step's place is read by warp 0 before the next item's first
         // barrier, and the first step's before this item's second
@@ -918,7 +953,13 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
         if (warp == 0) {
             J::add(x, joins + 2 * kPartial, lane);
             const int r = lane >> 2, q = lane & 3;
-            if (now.tile == 0 && last == now.tiles) {
+            if (from_start && lane == 0 && (rest || plan.by_item)) {
+                const int64_t after = rest + share.per - 1;
+                const int more = after < 0x7fffffff ? (int)((uint32_t)after / (uint32_t)share.per) : (int)(after / share.per);
+                st_v4(a.workspace + 4 * (plan.by_item ? (int64_t)b * plan.items + item : blockIdx.x),
+                      make_uint4(b, item, 1 + more, blockIdx.x));
+            }
+            if (from_start && rest == 0) {
 #pragma unroll
                 for (int h = 0; h < F::kHalves; h++) {
 #pragma unroll
@@ -927,7 +968,7 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                         const float total = odd ? x.total[h].y : x.total[h].x, by = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
                         if (row < plan.rows) {
                             int64_t at;
-                            T *to = static_cast<T *>(a.out) + out_row(a, plan, now.b, head, row, &at);
+                            T *to = static_cast<T *>(a.out) + out_row(a, plan, b, head, row, &at);
                             if (r == 0 && a.lse && dbg_ok(a.lse + at, 4, true))
                                 a.lse[at] = lse_of(odd ? x.ref[h].y : x.ref[h].x, total);
 #pragma unroll
@@ -940,13 +981,7 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                     }
                 }
             } else {
-                const bool goes_on = now.tile == 0;
-                float *const to = partial_of(a.workspace, blockIdx.x, goes_on, kPartial);
-                if (goes_on && lane == 0) {
-                    const int64_t rest = now.tiles - last + share.per - 1;
-                    const int more = rest < 0x7fffffff ? (int)((uint32_t)rest / (uint32_t)share.per) : (int)(rest / share.per);
-                    st_v4(a.workspace + 4 * blockIdx.x, make_uint4(now.b, now.item, 1 + more, 0));
-                }
+                float *const to = partial_of(a.workspace, blockIdx.x, from_start, kPartial);
 #pragma unroll
                 for (int h = 0; h < F::kHalves; h++) {
                     if (r == 0) {
@@ -963,16 +998,6 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                         }
                 }
             }
-        }
-        turn += last - now.tile;
-        if (last < now.tiles) break;
-        now.base += now.tiles + kSetup;
-        now.tile = 0;
-        if (now.base < places && ++now.item == plan.items) {
-            now.item = 0;
-            now.b++;
-            sequence_range(c, a, now.b, now.begin, now.end);
-            now.tiles = tiles_of(now.begin, now.end);
         }
     }
     lane_copy_wait<0>();
@@ -991,6 +1016,8 @@ cudaError_t launch_form(const Kv4Cache &c, const Kv4Attend &a, AttendPlan &plan,
     const int64_t tiles = (int64_t)(a.batch < 4096 ? a.batch : 4096) * plan.items * longest;
     if (cudaError_t e = grid_for((const void *)kernel, tiles, &plan.ctas, F::kSmem, kAttendThreads)) return e;
     if (plan.ctas > kMaxAttendCtas) plan.ctas = kMaxAttendCtas;
+    plan.by_item = a.batch <= kMaxAttendCtas / plan.items;
+    plan.words = plan.by_item ? a.batch * plan.items : plan.ctas;
     return launch_kernel_block(kernel, plan.ctas, kAttendThreads, F::kSmem, st, c, a, plan);
 }
 
