@@ -59,8 +59,13 @@ __device__ __forceinline__ void sequence_range(const Kv4Cache &c, const Kv4Atten
     begin = a.window > 0 && first > a.window ? first - a.window : 0;
     end = length;
 }
-// A sequence without positions is one tile too: its rows are written.
-__device__ __forceinline__ int tiles_of(int begin, int end) { return end > begin ? (end - begin - 1) / kTokens + 1 : 1; }
+// Tiles begin at multiples of 32, so that a window's tiles lie in pages as all others do. A sequence without positions is one
+// tile too: its rows are written.
+__device__ __forceinline__ int first_of(int begin) { return begin & -kTokens; }
+__device__ __forceinline__ int tiles_of(int begin, int end)
+{
+    return end > begin ? (end - first_of(begin) - 1) / kTokens + 1 : 1;
+}
 
 // What an item costs beside its tiles (its queries, the join of its warps), in tiles.
 constexpr int kSetup = 12;
@@ -333,10 +338,10 @@ struct Feed {
     {
         entry = -1;
         if (!walk.more) return;
-        const int j = walk.at.begin + walk.at.tile * kTokens + lane;
+        const int j = first_of(walk.at.begin) + walk.at.tile * kTokens + lane;
         const int column = (int)divide_by(j, plan.by_page);
         place = j - column * c.page;
-        if (j < walk.at.end) {
+        if (j >= walk.at.begin && j < walk.at.end) {
             const int32_t *p = a.table + walk.at.b * a.ld_table + column;
             if (dbg_ok(p, 4, false)) entry = __ldg(p);
         }
@@ -913,7 +918,7 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
             const int fill = slot == 0 ? F::kStages - 1 : slot - 1;
             feed.issue(c, a, plan, lane, ring + fill * F::kStage, &valid[warp][fill]);
             if (++slot == F::kStages) slot = 0;
-            const int at = now.begin + t * kTokens;
+            const int at = first_of(now.begin) + t * kTokens;
             float2 s[2][2][F::kHalves];
             x.scores(stage, lane, s);
             uint32_t seen[F::kHalves][2];
