@@ -122,7 +122,8 @@ cudaError_t launch_kv4_attend(int type, const Kv4Cache &c, const Kv4Attend &a, c
 {
     AttendPlan plan = {};
     plan.share = a.q_heads / c.heads, plan.rows = a.n_q * plan.share;
-    plan.by_share = divisor((uint32_t)plan.share), plan.by_page = divisor((uint32_t)c.page);
+    plan.by_share = divisor((uint32_t)plan.share), plan.page_tiles = c.page % kTokens ? 0 : c.page / kTokens;
+    plan.by_page = divisor((uint32_t)(plan.page_tiles ? plan.page_tiles : c.page));
     const bool bf16 = type == kBf16;
     if (cudaError_t e = bf16 ? launch_attend_bf16(c, a, plan, st) : launch_attend_f16(c, a, plan, st)) return e;
     if (plan.ctas == 1) return cudaSuccess;  // nothing is shared

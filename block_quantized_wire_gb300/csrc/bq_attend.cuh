@@ -45,7 +45,8 @@ struct AttendPlan {
     int ctas;                        // of the launch
     int words;                       // of the workspace that say which items are joined: one an item, or else one a CTA
     bool by_item;
-    Divisor by_share, by_page, by_chunks;
+    int page_tiles;                  // of a page, 0 where pages are no whole number of tiles
+    Divisor by_share, by_page, by_chunks;  // by_page: tokens, or tiles where page_tiles > 0
 };
 
 // ---------------------------------------------------------------- the run of tiles
@@ -160,10 +161,11 @@ struct Form {
     static constexpr int kChunks = kDim / 32;                            // 16-byte pieces of a row of codes
     static constexpr int kCodeBytes = kDim == 192 ? 16 * (kTokens * 6 + kTokens / 4) : 16 * kTokens * kChunks;
     static constexpr int kPairBytes = kTokens * 4 * kGroups;
-    static constexpr int kStage = 2 * (kCodeBytes + kPairBytes);
+    static constexpr int kValid = 2 * (kCodeBytes + kPairBytes);  // a bit a token that is there
+    static constexpr int kStage = kValid + 16;
     static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
     // CTAs of an SM by their registers: the sums of 8 rows of 64 columns fit 128 a thread, of 128 columns 168
-        static constexpr int kCtas = kRows == 8 && kDim <= 128 ? (kDim == 64 ? 4 : 3) : 2;
+        static constexpr int kCtas = kRows == 8 && kDim <= 128 ? 3 : 2;
     static constexpr int kRoom = (227 * 1024 / kCtas - 1024 - 512 - kJoin) / (kAttendWarps * kStage);
     static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
     static constexpr int kSmem = kJoin + kAttendWarps * kStages * kStage;
@@ -291,28 +293,42 @@ __device__ __forceinline__ bool finite_bits(uint32_t bits)
     return bits < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
 }
 
+// The largest (scale, offset) bits without signs whose scale is below 2^level and offset below 2^(level + 24).
+template <class T>
+__device__ __forceinline__ uint32_t limit_of(int level)
+{
+    constexpr int kBits = std::is_same<T, __half>::value ? 10 : 7, kBias = std::is_same<T, __half>::value ? 15 : 127;
+    constexpr int kLargest = std::is_same<T, __half>::value ? 0x7bff : 0x7f7f;
+    const auto below = [](int e) { return e + kBias <= 0 ? 0 : min(((e + kBias) << kBits) - 1, kLargest); };
+    return (uint32_t)below(level) | (uint32_t)below(level + 24) << 16;
+}
+
 // ---------------------------------------------------------------- the warps' walk over tiles
 struct Walk {
     Spot at;
     int64_t n;  // places of the CTA's share
-    bool more;  // `at` is one of them
+    int stop;   // the item's tiles in this share end here; none left if at.tile is not below
 
+    __device__ __forceinline__ bool more() const { return at.tile < stop; }
+    __device__ __forceinline__ void enter()
+    {
+        const int64_t left = n - at.base;
+        stop = left >= at.tiles ? at.tiles : left > 0 ? (int)left : 0;
+    }
     __device__ __forceinline__ void step(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int count)
     {
         at.tile += count;
-        while (at.tile >= at.tiles) {
+        while (at.tile >= stop && stop == at.tiles) {
             at.tile -= at.tiles;
             at.base += at.tiles + kSetup;
-            more = at.base < n;
-            if (!more) return;
-            if (++at.item == plan.items) {
+            if (at.base < n && ++at.item == plan.items) {
                 at.item = 0;
                 at.b++;
                 sequence_range(c, a, at.b, at.begin, at.end);
                 at.tiles = tiles_of(at.begin, at.end);
             }
+            enter();
         }
-        more = at.base + at.tile < n;
     }
 };
 
@@ -323,44 +339,58 @@ __device__ __forceinline__ uint32_t divide_by(uint32_t n, const Divisor &d) { re
 template <class T, class F>
 struct Feed {
     Walk walk;
-    int entry, place;
-    int64_t at_head, at_head_s;  // of the walk's head, and the lane's part of a page where tokens lie at equal steps
+    int entry, place;             // the tile's page and first place in it, or each lane's token's
+    const int32_t *row;           // of the table
+    int64_t at_head, at_head_s;
 
-    __device__ __forceinline__ void new_item(const Kv4Cache &c, const AttendPlan &plan, int lane)
+    __device__ __forceinline__ void new_item(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan)
     {
         const int head = (int)divide_by(walk.at.item, plan.by_chunks);
         at_head = head * c.head_stride;
         at_head_s = head * c.head_stride_s;
+        row = a.table + walk.at.b * a.ld_table;
     }
+    __device__ __forceinline__ int first_position() const { return first_of(walk.at.begin) + walk.at.tile * kTokens; }
 
-    // a lane's token of the walk's tile
-    __device__ __forceinline__ void look_up(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int lane)
+    __device__ __forceinline__ void look_up(const Kv4Cache &c, const AttendPlan &plan, int lane)
     {
         entry = -1;
-        if (!walk.more) return;
-        const int j = first_of(walk.at.begin) + walk.at.tile * kTokens + lane;
-        const int column = (int)divide_by(j, plan.by_page);
-        place = j - column * c.page;
-        if (j >= walk.at.begin && j < walk.at.end) {
-            const int32_t *p = a.table + walk.at.b * a.ld_table + column;
-            if (dbg_ok(p, 4, false)) entry = __ldg(p);
+        if (!walk.more()) return;
+        const int at = first_position();
+        if (plan.page_tiles) {
+            const int tile = at / kTokens, column = (int)divide_by(tile, plan.by_page);
+            place = (tile - column * plan.page_tiles) * kTokens;
+            if (at < walk.at.end && dbg_ok(row + column, 4, false)) entry = __ldg(row + column);
+        } else {
+            const int j = at + lane, column = (int)divide_by(j, plan.by_page);
+            place = j - column * c.page;
+            if (j >= walk.at.begin && j < walk.at.end && dbg_ok(row + column, 4, false)) entry = __ldg(row + column);
         }
     }
 
-    __device__ __forceinline__ void issue(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int lane, uint32_t stage,
-                                          uint32_t *valid)
+    __device__ __forceinline__ void issue(const Kv4Cache &c, const Kv4Attend &a, const AttendPlan &plan, int lane, uint32_t stage)
     {
-        if (walk.more) {
-            const bool ok = entry >= 0 && entry < c.pages;
-            const uint32_t there = __ballot_sync(kFull, ok);
-            if (lane == 0) *valid = there;
+        if (walk.more()) {
+            bool ok = entry >= 0 && entry < c.pages;
+            const int from = first_position();
+            bool one_page = true;  // whole tiles of one page: tokens at equal steps
+            int page = entry, first = place;
+            uint32_t there = kFull;
+            if (!(plan.page_tiles && ok && from >= walk.at.begin && from + kTokens <= walk.at.end)) {
+                if (plan.page_tiles) {
+                    ok = ok && from + lane >= walk.at.begin && from + lane < walk.at.end;
+                    place += lane;
+                }
+                there = __ballot_sync(kFull, ok);
+                first = __shfl_sync(kFull, place, 0), page = __shfl_sync(kFull, entry, 0);
+                one_page = there == kFull && first + kTokens <= c.page;
+            }
+            if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(stage + F::kValid), "r"(there) : "memory");
             constexpr int kSize = F::kGroups % 4 == 0 ? 16 : F::kGroups % 2 == 0 ? 8 : 4;
             const uint32_t to_s = stage + 2 * F::kCodeBytes + 4 * F::kGroups * lane;
-            const int first = __shfl_sync(kFull, place, 0);
-            if (there == kFull && first + kTokens <= c.page) {  // one page: tokens at equal steps
-                const int64_t page = __shfl_sync(kFull, entry, 0);
-                const int64_t at = page * c.page_stride + at_head + first * c.token_stride;
-                const int64_t at_s = page * c.page_stride_s + at_head_s + place * c.token_stride_s;
+            if (one_page) {
+                const int64_t at = page * c.page_stride + at_head + first * (int64_t)c.token_stride;
+                const int64_t at_s = page * c.page_stride_s + at_head_s + (first + lane) * (int64_t)c.token_stride_s;
                 const uint8_t *const k = c.k + at, *const v = c.v + at;
                 if (c.token_stride == F::kDim / 2) {  // one run of bytes
 #pragma unroll
@@ -374,7 +404,7 @@ struct Feed {
 #pragma unroll
                     for (int i = 0; i < F::kChunks; i++) {
                         const int piece = 32 * i + lane, t = piece / F::kChunks, ch = piece % F::kChunks;
-                        const int64_t from = t * c.token_stride + 16 * ch;
+                        const int64_t from = t * (int64_t)c.token_stride + 16 * ch;
                         const uint32_t to = stage + 16 * chunk_at<F::kDim>(t, ch);
                         lane_copy16(to, k + from);
                         lane_copy16(to + F::kCodeBytes, v + from);
@@ -386,9 +416,9 @@ struct Feed {
                     lane_copy_part<kSize>(to_s + F::kPairBytes + i, c.v_scales + at_s + i, kSize);
                 }
             } else {
-                const int64_t page = ok ? entry : 0;
-                const int64_t at = ok ? page * c.page_stride + at_head + place * c.token_stride : 0;
-                const int64_t at_s = ok ? page * c.page_stride_s + at_head_s + place * c.token_stride_s : 0;
+                const int64_t page = ok ? entry : 0;  // each lane its own token
+                const int64_t at = ok ? page * c.page_stride + at_head + place * (int64_t)c.token_stride : 0;
+                const int64_t at_s = ok ? page * c.page_stride_s + at_head_s + place * (int64_t)c.token_stride_s : 0;
 #pragma unroll
                 for (int i = 0; i < F::kChunks; i++) {
                     const int piece = 32 * i + lane, t = piece / F::kChunks, ch = piece % F::kChunks;
@@ -405,9 +435,10 @@ struct Feed {
                 }
             }
             const int item = walk.at.item;
+            const int b = walk.at.b;
             walk.step(c, a, plan, kAttendWarps);
-            if (item != walk.at.item) new_item(c, plan, lane);
-            look_up(c, a, plan, lane);
+            if (item != walk.at.item || b != walk.at.b) new_item(c, a, plan);
+            look_up(c, plan, lane);
         }
         lane_copy_commit();
     }
@@ -424,7 +455,8 @@ struct Rows {
     uint32_t qsum[kSums][2][F::kHalves];                    // fragments of a group's sum of scaled queries, times kUnit
     float2 f[F::kHalves];                                   // from a score in units to its log2
     float2 ref[F::kHalves];                                 // A
-    int level;                                              // log2 of the largest scale so far
+    int level;                                              // log2 of the largest scale so far, and the largest (scale, offset)
+    uint32_t limit;                                         // bits that do not pass it: offsets count 2^-24
     float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
     float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
     float eights[(F::kGroups + 1) / 2][F::kHalves][4];      // of 8 p s, in units: a group in c0 c1, the next in c2 c3
@@ -449,6 +481,7 @@ struct Rows {
     __device__ __forceinline__ void start(const Kv4Attend &a, int lane, const Queries &raw)
     {
         level = -60;
+        limit = limit_of<T>(level);
         const int q = lane & 3;
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
@@ -604,26 +637,11 @@ struct Rows {
     {
         const int r = lane >> 2;
         const uint32_t pairs = stage + 2 * F::kCodeBytes + F::kPairBytes;
-        // log2 of the scales of the lane's token among the values; offsets count 2^-24, so that sums of p z stay in range
-        int k;
-        {
-            uint32_t w[F::kGroups];
-            lds_words<F::kGroups>(pairs + 4 * F::kGroups * lane, w);
-            uint32_t top = 0;
+        // Do the lane's token's scales, and its offsets times 2^-24 (so that sums of p z stay in range), stay below the level?
+        uint32_t mine[F::kGroups], above = limit;
+        lds_words<F::kGroups>(pairs + 4 * F::kGroups * lane, mine);
 #pragma unroll
-            for (int g = 0; g < F::kGroups; g++) top = __vmaxu2(top, w[g] & 0x7fff7fffu);
-            k = -60;
-            if (finite_bits<T>(top & 0xffffu) && finite_bits<T>(top >> 16)) {
-                k = max(k, max(exponent_of<T>(top & 0xffffu) + 1, exponent_of<T>(top >> 16) - 23));
-            } else {
-#pragma unroll
-                for (int g = 0; g < F::kGroups; g++) {
-                    const uint32_t s = w[g] & 0x7fffu, z = (w[g] >> 16) & 0x7fffu;
-                    if (finite_bits<T>(s)) k = max(k, exponent_of<T>(s) + 1);
-                    if (finite_bits<T>(z)) k = max(k, exponent_of<T>(z) - 23);
-                }
-            }
-        }
+        for (int g = 0; g < F::kGroups; g++) above = __vmaxu2(above, mine[g] & 0x7fff7fffu);
         const auto sees = [&](int h, int odd, int n, int t) { return !kMasked || ((seen[h][odd] >> (16 * n + 8 * t + r)) & 1); };
         float2 y[2][2][F::kHalves];
         float most = -INFINITY;
@@ -644,8 +662,16 @@ struct Rows {
         exponents();
         // p s stays within 2^14 as long as no scale passes the level and no p 2^(14 - level): every lane looks at its own
         // tokens, and the rows' largest scores are looked for where one does
-        if (__any_sync(kFull, most > kLift + 1.0f - (float)level || k > level)) {
-            level = max(level, __reduce_max_sync(kFull, k));
+        if (__any_sync(kFull, most > kLift + 1.0f - (float)level || above != limit)) {
+            int k = level;
+#pragma unroll
+            for (int g = 0; g < F::kGroups; g++) {
+                const uint32_t scale = mine[g] & 0x7fffu, offset = (mine[g] >> 16) & 0x7fffu;
+                if (finite_bits<T>(scale)) k = max(k, exponent_of<T>(scale) + 1);
+                if (finite_bits<T>(offset)) k = max(k, exponent_of<T>(offset) - 23);
+            }
+            level = __reduce_max_sync(kFull, k);
+            limit = limit_of<T>(level);
 #pragma unroll
             for (int h = 0; h < F::kHalves; h++) {
                 float2 top = splat(-INFINITY);
@@ -867,7 +893,6 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
     attend_kernel(const __grid_constant__ Kv4Cache c, const __grid_constant__ Kv4Attend a, const __grid_constant__ AttendPlan plan)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ uint32_t valid[kAttendWarps][F::kStages];
     using J = Join<T, F>;
     constexpr int64_t kPartial = (int64_t)F::kRows * (F::kDim + 2);
     pdl_begin();
@@ -883,15 +908,16 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
     float *const joins = reinterpret_cast<float *>(smem);
     const uint32_t ring = smem_u32(smem) + F::kJoin + warp * F::kStages * F::kStage;
     Feed<T, F> feed;
-    feed.walk = Walk{now, places, now.base + now.tile < places};
+    feed.walk = Walk{now, places, 0};
+    feed.walk.enter();
     feed.walk.step(c, a, plan, warp);
-    feed.new_item(c, plan, lane);
-    feed.look_up(c, a, plan, lane);
+    feed.new_item(c, a, plan);
+    feed.look_up(c, plan, lane);
 #pragma unroll
-    for (int s = 0; s < F::kStages - 1; s++) feed.issue(c, a, plan, lane, ring + s * F::kStage, &valid[warp][s]);
+    for (int s = 0; s < F::kStages - 1; s++) feed.issue(c, a, plan, lane, ring + s * F::kStage);
 
     Rows<T, F> x;
-    int slot = 0;
+    uint32_t stage = ring, fill = ring + (F::kStages - 1) * F::kStage;  // the tile's, and the one that is free
     for (int turn = 0; now.base + now.tile < places;) {
         const int64_t left = places - now.base;
         const int last = left < now.tiles ? (int)left : now.tiles;  // of the item in this share
@@ -914,10 +940,8 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
         for (int t = now.tile + ((warp - turn) & (kAttendWarps - 1)); t < last; t += kAttendWarps) {
             lane_copy_wait<F::kStages - 2>();
             __syncwarp();
-            const uint32_t stage = ring + slot * F::kStage, there = valid[warp][slot];
-            const int fill = slot == 0 ? F::kStages - 1 : slot - 1;
-            feed.issue(c, a, plan, lane, ring + fill * F::kStage, &valid[warp][fill]);
-            if (++slot == F::kStages) slot = 0;
+            feed.issue(c, a, plan, lane, fill);
+            const uint32_t there = lds_u32(stage + F::kValid);
             const int at = first_of(now.begin) + t * kTokens;
             float2 s[2][2][F::kHalves];
             x.scores(stage, lane, s);
@@ -933,6 +957,8 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                 }
                 x.template take<true>(stage, lane, s, seen);
             }
+            fill = stage;
+            stage = stage == ring + (F::kStages - 1) * F::kStage ? ring : stage + F::kStage;
         }
         const int b = now.b, item = now.item, rest = now.tiles - last;
         const bool from_start = now.tile == 0;
