@@ -37,6 +37,7 @@ constexpr int kTokens = 32;                       // of a tile
 constexpr float kNothing = -3.0e38f;              // the reference of a row that has seen nothing
 constexpr float kUnit = 0x1p-24f;                 // of a code held as an FP16's lowest mantissa bits
 constexpr float kLift = 13.0f;                    // log2 of the largest p s beside a fresh reference
+constexpr int kLowest = -80;                      // level of the smallest scales: 2^31 weights of 2^(14 - level) are 2^125
 constexpr int kMaxAttendCtas = 608;               // four on each of 152 SMs
 
 // What a call's kernels share beside its arguments.
@@ -164,8 +165,9 @@ struct Form {
     static constexpr int kValid = 2 * (kCodeBytes + kPairBytes);  // a bit a token that is there
     static constexpr int kStage = kValid + 16;
     static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
-    // CTAs of an SM by their registers: the sums of 8 rows of 64 columns fit 128 a thread, of 128 columns 168
-        static constexpr int kCtas = kRows == 8 && kDim <= 128 ? 3 : 2;
+    // CTAs of an SM by their registers: the sums of 8 rows of up to 128 columns fit 168 a thread. 4 CTAs at 128 registers:
+    // 64 sequences of up to 8192 tokens took 85.7 us for 76.1, 2 at 255 the same 76.1 with more of a call's parts shared less.
+    static constexpr int kCtas = kRows == 8 && kDim <= 128 ? 3 : 2;
     static constexpr int kRoom = (227 * 1024 / kCtas - 1024 - 512 - kJoin) / (kAttendWarps * kStage);
     static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
     static constexpr int kSmem = kJoin + kAttendWarps * kStages * kStage;
@@ -459,7 +461,7 @@ struct Rows {
     uint32_t limit;                                         // bits that do not pass it: offsets count 2^-24
     float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
     float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
-    float eights[(F::kGroups + 1) / 2][F::kHalves][4];      // of 8 p s, in units: a group in c0 c1, the next in c2 c3
+    float eights[F::kGroups][F::kHalves][4];                // of 8 p s, in units, c0 c1 as c2 c3: groups apart, for their NaNs
 
     // The lane's queries of an item.
     using Queries = uint4[F::kHalves][F::kChunks];
@@ -480,7 +482,7 @@ struct Rows {
 
     __device__ __forceinline__ void start(const Kv4Attend &a, int lane, const Queries &raw)
     {
-        level = -60;
+        level = kLowest;
         limit = limit_of<T>(level);
         const int q = lane & 3;
 #pragma unroll
@@ -550,7 +552,7 @@ struct Rows {
 #pragma unroll
                 for (int k = 0; k < 4; k++) sum[m][h][k] = 0.0f;
 #pragma unroll
-            for (int g = 0; g < (F::kGroups + 1) / 2; g++)
+            for (int g = 0; g < F::kGroups; g++)
 #pragma unroll
                 for (int k = 0; k < 4; k++) eights[g][h][k] = 0.0f;
         }
@@ -701,7 +703,7 @@ struct Rows {
 #pragma unroll
                     for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? keep.y : keep.x);
 #pragma unroll
-                for (int g = 0; g < (F::kGroups + 1) / 2; g++)
+                for (int g = 0; g < F::kGroups; g++)
 #pragma unroll
                     for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? keep.y : keep.x);
             }
@@ -743,10 +745,7 @@ struct Rows {
 #pragma unroll
                 for (int h = 0; h < F::kHalves; h++) {
                     constexpr uint32_t kEight = 0x00080008u;
-                    if (g & 1)
-                        mma_f16<false>(eights[g / 2][h], 0u, kEight, 0u, kEight, b[h][0], b[h][1]);
-                    else
-                        mma_f16<false>(eights[g / 2][h], kEight, 0u, kEight, 0u, b[h][0], b[h][1]);
+                    mma_f16<false>(eights[g][h], kEight, kEight, kEight, kEight, b[h][0], b[h][1]);
                 }
                 values(stage + F::kCodeBytes, lane, n, g, b, codes);
             }
@@ -794,7 +793,7 @@ struct Rows {
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         const float u = k & 1 ? __fmul_rn(v[i], 0.0625f) : v[i];
-                        const float c = eights[g / 2][h][2 * (g & 1) + (i & 1)];
+                        const float c = eights[g][h][i];
                         v[i] = __fmaf_rn(__fsub_rn(u, c), 1.0f / kUnit, i & 1 ? z.y : z.x);
                     }
                 }
