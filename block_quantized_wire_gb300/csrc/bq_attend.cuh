@@ -16,12 +16,18 @@
 // largest value to 2^14 .. 2^15, which FP16 then holds exactly down to 2^-28 of that. Only p s is rounded, to FP16
 // (2^-11): it is used rounded in the sum over u and in the -8 correction (a mma with a constant matrix), so that
 // u's offset does not enlarge that error. p's reference A takes in the size of s, p = 2^(y - A), A = max y + log2 max s
-// - 13, so that p s stays within 2^15 and is exact to 2^-11 down to 2^-28 of the largest.
+// - 13, so that p s stays within 2^14 and is exact to 2^-11 down to 2^-28 of the largest.
 //
 // Fragments. Codes are the m side of both products: tokens of the keys, columns of the values, which ldmatrix and its
 // transposing form deliver as they lie. Scores come with tokens as rows and queries as columns; p s, rounded, is
 // turned over by movmatrix into the n side of the second product. So up to 8 query rows cost half the mma that 16 do, and all
 // that belongs to a query row (reference, sums, weights) lies in the lanes that hold its columns.
+//
+// What bounds it: the cache's bytes are the floor (144 a token and head at head_dim 128 and groups of 64), and the
+// instructions that turn codes into operands come next: 5 logic instructions for 8 codes, two cycles of a scheduler each, and an mma of eight
+// cycles for 512 codes (twice that for more than 8 rows), which overlap in small part only. At head_dim 128, groups of
+// 64 and 8 rows the copies alone run at 6.9 TB/s, the arithmetic alone as fast as 5.9 TB/s of cache would come, both at 5.5; a
+// call's ends (lengths, first tiles, joins) take about 12 us more. One sequence of 131072 tokens: 40 us; 64 of up to 8192: 75 us.
 #pragma once
 
 #include <cmath>
@@ -38,7 +44,7 @@ constexpr float kNothing = -3.0e38f;              // the reference of a row that
 constexpr float kUnit = 0x1p-24f;                 // of a code held as an FP16's lowest mantissa bits
 constexpr float kLift = 13.0f;                    // log2 of the largest p s beside a fresh reference
 constexpr int kLowest = -80;                      // level of the smallest scales: 2^31 weights of 2^(14 - level) are 2^125
-constexpr int kMaxAttendCtas = 608;               // four on each of 152 SMs
+constexpr int kMaxAttendCtas = 456;               // three on each of 152 SMs
 
 // What a call's kernels share beside its arguments.
 struct AttendPlan {
@@ -165,9 +171,9 @@ struct Form {
     static constexpr int kValid = 2 * (kCodeBytes + kPairBytes);  // a bit a token that is there
     static constexpr int kStage = kValid + 16;
     static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
-    // CTAs of an SM by their registers: the sums of 8 rows of up to 128 columns fit 168 a thread. 4 CTAs at 128 registers:
-    // 64 sequences of up to 8192 tokens took 85.7 us for 76.1, 2 at 255 the same 76.1 with more of a call's parts shared less.
-    static constexpr int kCtas = kRows == 8 && kDim <= 128 ? 3 : 2;
+    // CTAs of an SM by their registers: 8 rows of 64 columns fit 168 a thread, all else up to 255. 8 rows of 128 columns with
+    // three CTAs (168, some spilled): 64 sequences of up to 8192 tokens took 77.3 us for 74.6; with four (128): 85.7.
+    static constexpr int kCtas = kRows == 8 && kDim == 64 ? 3 : 2;
     static constexpr int kRoom = (227 * 1024 / kCtas - 1024 - 512 - kJoin) / (kAttendWarps * kStage);
     static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
     static constexpr int kSmem = kJoin + kAttendWarps * kStages * kStage;

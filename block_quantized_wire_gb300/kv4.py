@@ -142,8 +142,8 @@ def _query_shape(call: str, q: torch.Tensor, cache: Cache):
 
 
 def empty_workspace(q: torch.Tensor, cache: Cache) -> torch.Tensor:
-    """Scratch for ``attend`` calls with q's queries and heads, of any batch and any lengths. Calls that may
-    run at the same time (other streams, graphs that are replayed together) need one each."""
+    """Scratch for ``attend`` calls with q's queries and heads, of any batch and any lengths: 2 to 8 MB. Calls that
+    may run at the same time (other streams, graphs that are replayed together) need one each."""
     _, n_q, q_heads, dim = _query_shape("empty_workspace", q, cache)
     size = load().bq_kv4_workspace_bytes(cache.heads, dim, max(n_q, 1), max(q_heads, cache.heads))
     if size < 0:
