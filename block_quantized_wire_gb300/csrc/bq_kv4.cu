@@ -3,8 +3,10 @@
 // Both kernels are one pass: a lane takes 16 columns of a key and of its value (32 bytes each, one 256-bit access
 // where the rows allow it) and their 8 bytes of codes; a group's 2, 4 or 8 lanes share its pair. Key and value lie at the same
 // offsets of the cache, so that one slot is looked up and one place computed for both.
-// Reading 65536 tokens of 8 heads of 128 columns takes 54 us, 6.3 TB/s; writing 32768 and reading them back 65 us, of which
-// about 37 are the write's: 4.8 TB/s, bound by its instructions.
+// Reading 65536 tokens of 8 heads of 128 columns takes 54 us, 6.3 TB/s; writing 32768 and reading them back 63 us, of which
+// about 36 are the write's: 4.9 TB/s, bound by its instructions.
+#include <type_traits>
+
 #include "bq_codes.cuh"
 #include "bq_kv4.cuh"
 
@@ -136,18 +138,30 @@ __device__ __forceinline__ void quantize(const uint4 &lo4, const uint4 &hi4, uin
     const float z = Value<T>::widen(z_bits);
     if (!(s <= 3.0e38f)) s_bits = z_bits = 0x7fffu, s = 0.0f;  // infinity or NaN: a NaN of both types
     uint32_t w[16];
-    if (s >= 0x1p-90f) {
+    // Quotients run from -8 to 7 but for the roundings of s and of the offset. Where the offset is at most 32 s it is off by
+    // s / 8 at most (BF16: 2^-8 of it), and a normal s by 2^-8 of itself: quotients stay between -8.13 and 7.19, and
+    // their nearest integers in the range. Only warps with another group hold them to it.
+    constexpr float kNormal = std::is_same<T, __half>::value ? 0x1p-14f : 0x1p-126f;
+    const bool far = __any_sync(kFull, fabsf(z) > 32.0f * s || s < kNormal);
+    const auto quotients = [&](auto held) {
         const float2 neg_z = splat(-z), r = splat(__frcp_rn(s)), neg_s = splat(-s), up = splat(kRound);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const float2 v = make_float2(Value<T>::widen((uint16_t)(x[i] & 0xffffu)), Value<T>::widen((uint16_t)(x[i] >> 16)));
             const float2 d = add2(v, neg_z), t = mul2(d, r);
             float2 q = fma2(fma2(t, neg_s, d), r, t);
-            q = make_float2(fminf(fmaxf(q.x, -8.0f), 7.0f), fminf(fmaxf(q.y, -8.0f), 7.0f));
+            if constexpr (decltype(held)::value)
+                q = make_float2(fminf(fmaxf(q.x, -8.0f), 7.0f), fminf(fmaxf(q.y, -8.0f), 7.0f));
             const float2 n = add2(q, up);
             w[2 * i] = __float_as_uint(n.x);
             w[2 * i + 1] = __float_as_uint(n.y);
         }
+    };
+    if (s >= 0x1p-90f) {
+        if (far)
+            quotients(std::true_type());
+        else
+            quotients(std::false_type());
     } else if (s > 0.0f) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {

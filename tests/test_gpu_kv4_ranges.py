@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from block_quantized_wire_gb300 import kv4
-from tests.test_gpu_kv4 import (TYPES, check, fill, guarded_cache, reference, run, same_bits, table_of)
+from tests.test_gpu_kv4 import (TYPES, check, fill, guarded_cache, quantized, reference, run, same_bits, table_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +20,23 @@ def problem(seed, lens, n_q, q_heads, heads, dim, group, page, dtype=torch.bfloa
     lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
     q = torch.from_numpy(rng.standard_normal((len(lens), n_q, q_heads, dim)).astype(np.float32)).to(dtype).cuda()
     return q, cache, table, lengths
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_rows_with_offsets_of_any_size_beside_their_range(name, group):
+    # means of 0 to 1000 ranges, around 32 steps too; ranges down to the smallest values of the type
+    dtype = TYPES[name][0]
+    torch.manual_seed(group)
+    x = torch.randn(2048, 2, 128, device="cuda")
+    x = x + torch.randn(2048, 2, 1, device="cuda").sign() * torch.logspace(-1, 3, 2048, device="cuda")[:, None, None]
+    x = (x * torch.logspace(-7, 1, 8, device="cuda").repeat(256)[:, None, None]).to(dtype)
+    cache = kv4.empty_cache(32, 2, 64, 128, group, dtype)
+    kv4.write(x, -x, torch.arange(2048, device="cuda"), cache)
+    for rows, codes, pairs in ((x, cache.k, cache.k_scales), (-x, cache.v, cache.v_scales)):
+        want, want_pairs, _ = quantized(rows, group)
+        assert np.array_equal(codes.transpose(1, 2).reshape(2048, 2, 64).cpu().numpy(), want)
+        assert torch.equal(pairs.transpose(1, 2).reshape(want_pairs.shape).cpu(), want_pairs)
 
 
 @pytest.mark.parametrize("n", [1, 31, 32, 33, 63, 64, 65, 127, 128, 129, 160, 161])
