@@ -905,8 +905,8 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Share share;
     Spot now;
-    find_share(c, a, plan, share, now);
     if (threadIdx.x == 0 && !plan.by_item) st_v4(a.workspace + 4 * blockIdx.x, make_uint4(0, 0, 0, 0));
+    find_share(c, a, plan, share, now);  // its barriers order that before other threads' word
     if ((int)blockIdx.x >= share.ctas) return;
     const int64_t places = share.first(blockIdx.x + 1) - share.first(blockIdx.x);
 
@@ -927,43 +927,49 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
         const int64_t left = places - now.base;
         const int last = left < now.tiles ? (int)left : now.tiles;  // of the item in this share
         const int head = (int)divide_by(now.item, plan.by_chunks), row0 = (now.item - head * plan.chunks) * F::kRows;
-        typename Rows<T, F>::Queries queries;
-        x.fetch(a, plan, now.b, head, row0, lane, queries);
-        x.start(a, lane, queries);
-        // the positions that the lane's rows see, and that all rows of the item do
-        int lo[F::kHalves][2], hi[F::kHalves][2];
+        // One tile is one warp's item, without a join: the others are at the next one meanwhile.
+        const bool alone = last - now.tile == 1;
+        const int writer = alone ? turn & (kAttendWarps - 1) : 0;
+        const bool mine = !alone || warp == writer;
+        if (mine) {
+            typename Rows<T, F>::Queries queries;
+            x.fetch(a, plan, now.b, head, row0, lane, queries);
+            x.start(a, lane, queries);
+            // the positions that the lane's rows see, and that all rows of the item do
+            int lo[F::kHalves][2], hi[F::kHalves][2];
 #pragma unroll
-        for (int i = 0; i < 2 * F::kHalves; i++) {
-            const int row = min(row0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1), plan.rows - 1);
-            int &end = hi[i >> 1][i & 1];
-            end = now.end - a.n_q + 1 + (int)divide_by(row, plan.by_share);
-            lo[i >> 1][i & 1] = a.window > 0 && end > a.window ? end - a.window : 0;
-        }
-        const int all_hi = now.end - a.n_q + 1 + (int)divide_by(row0, plan.by_share);
-        const int last_hi = now.end - a.n_q + 1 + (int)divide_by(min(row0 + F::kRows, plan.rows) - 1, plan.by_share);
-        const int all_lo = a.window > 0 && last_hi > a.window ? last_hi - a.window : 0;
-        for (int t = now.tile + ((warp - turn) & (kAttendWarps - 1)); t < last; t += kAttendWarps) {
-            lane_copy_wait<F::kStages - 2>();
-            __syncwarp();
-            feed.issue(c, a, plan, lane, fill);
-            const uint32_t there = lds_u32(stage + F::kValid);
-            const int at = first_of(now.begin) + t * kTokens;
-            float2 s[2][2][F::kHalves];
-            x.scores(stage, lane, s);
-            uint32_t seen[F::kHalves][2];
-            if (there == kFull && at >= all_lo && at + kTokens <= all_hi) {
-                x.template take<false>(stage, lane, s, seen);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * F::kHalves; i++) {
-                    const int from = max(lo[i >> 1][i & 1] - at, 0), to = min(hi[i >> 1][i & 1] - at, kTokens);
-                    const uint32_t above = from < kTokens ? kFull << from : 0u, below = to <= 0 ? 0u : kFull >> (kTokens - to);
-                    seen[i >> 1][i & 1] = there & above & below;
-                }
-                x.template take<true>(stage, lane, s, seen);
+            for (int i = 0; i < 2 * F::kHalves; i++) {
+                const int row = min(row0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1), plan.rows - 1);
+                int &end = hi[i >> 1][i & 1];
+                end = now.end - a.n_q + 1 + (int)divide_by(row, plan.by_share);
+                lo[i >> 1][i & 1] = a.window > 0 && end > a.window ? end - a.window : 0;
             }
-            fill = stage;
-            stage = stage == ring + (F::kStages - 1) * F::kStage ? ring : stage + F::kStage;
+            const int all_hi = now.end - a.n_q + 1 + (int)divide_by(row0, plan.by_share);
+            const int last_hi = now.end - a.n_q + 1 + (int)divide_by(min(row0 + F::kRows, plan.rows) - 1, plan.by_share);
+            const int all_lo = a.window > 0 && last_hi > a.window ? last_hi - a.window : 0;
+            for (int t = now.tile + ((warp - turn) & (kAttendWarps - 1)); t < last; t += kAttendWarps) {
+                lane_copy_wait<F::kStages - 2>();
+                __syncwarp();
+                feed.issue(c, a, plan, lane, fill);
+                const uint32_t there = lds_u32(stage + F::kValid);
+                const int at = first_of(now.begin) + t * kTokens;
+                float2 s[2][2][F::kHalves];
+                x.scores(stage, lane, s);
+                uint32_t seen[F::kHalves][2];
+                if (there == kFull && at >= all_lo && at + kTokens <= all_hi) {
+                    x.template take<false>(stage, lane, s, seen);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * F::kHalves; i++) {
+                        const int from = max(lo[i >> 1][i & 1] - at, 0), to = min(hi[i >> 1][i & 1] - at, kTokens);
+                        const uint32_t above = from < kTokens ? kFull << from : 0u, below = to <= 0 ? 0u : kFull >> (kTokens - to);
+                        seen[i >> 1][i & 1] = there & above & below;
+                    }
+                    x.template take<true>(stage, lane, s, seen);
+                }
+                fill = stage;
+                stage = stage == ring + (F::kStages - 1) * F::kStage ? ring : stage + F::kStage;
+            }
         }
         const int b = now.b, item = now.item, rest = now.tiles - last;
         const bool from_start = now.tile == 0;
@@ -978,16 +984,19 @@ __global__ void __launch_bounds__(kAttendThreads, F::kCtas)
                 now.tiles = tiles_of(now.begin, now.end);
             }
         }
+        if (!mine) continue;
         x.finish();
         // warps 2 and 3 to 0 and 1, then 1 to 0; the last step's place is read by warp 0 before the next item's first
         // barrier, and the first step's before this item's second
-        if (warp >= 2) J::put(x, joins + (warp - 2) * kPartial, lane);
-        __syncthreads();
-        if (warp < 2) J::add(x, joins + warp * kPartial, lane);
-        if (warp == 1) J::put(x, joins + 2 * kPartial, lane);
-        __syncthreads();
-        if (warp == 0) {
-            J::add(x, joins + 2 * kPartial, lane);
+        if (!alone) {
+            if (warp >= 2) J::put(x, joins + (warp - 2) * kPartial, lane);
+            __syncthreads();
+            if (warp < 2) J::add(x, joins + warp * kPartial, lane);
+            if (warp == 1) J::put(x, joins + 2 * kPartial, lane);
+            __syncthreads();
+            if (warp == 0) J::add(x, joins + 2 * kPartial, lane);
+        }
+        if (warp == writer) {
             const int r = lane >> 2, q = lane & 3;
             if (from_start && lane == 0 && (rest || plan.by_item)) {
                 const int64_t after = rest + share.per - 1;
