@@ -64,7 +64,9 @@ def decode_layer(x: torch.Tensor, ranks: Sequence[HeadWeights], caches: Sequence
                  lengths: torch.Tensor, mode: str = "i8_a2a", queries: int = 1, rotate: Optional[Callable] = None,
                  window: int = 0) -> List[torch.Tensor]:
     """The whole layer: every rank's part, summed through the wire mode ``mode`` and returned as
-    ``moe.decode_layer`` does. All ranks' caches go by the same table."""
+    ``moe.decode_layer`` does. Each rank has a cache of its own; all go by the same table."""
     reduce = moe.reduction(mode)
+    if len(ranks) != len(caches):
+        raise ValueError(f"decode_layer: {len(ranks)} ranks need a cache each, got {len(caches)} caches")
     parts = [decode_part(x, w, cache, table, lengths, queries, rotate, window=window) for w, cache in zip(ranks, caches)]
     return moe.summed(parts, reduce)
