@@ -45,7 +45,7 @@ def decode_part(x: torch.Tensor, w: HeadWeights, cache: kv4.Cache, table: torch.
     batch, dim = lengths.shape[0], cache.head_dim
     both = torch.empty((x.shape[0], w.qkv[0].shape[0]), dtype=x.dtype, device=x.device)
     w4.matvec_w4(x, *w.qkv, both)
-    q, k, v = both.view(batch, queries, -1, dim).split([w.q_heads, w.heads, w.heads], dim=2)
+    q, k, v = both.view(batch, queries, w.q_heads + 2 * w.heads, dim).split([w.q_heads, w.heads, w.heads], dim=2)
     positions = lengths[:, None] - queries + torch.arange(queries, dtype=torch.int32, device=x.device)
     if rotate is not None:
         q, k = rotate(q, k, positions)
@@ -56,7 +56,7 @@ def decode_part(x: torch.Tensor, w: HeadWeights, cache: kv4.Cache, table: torch.
         workspace = kv4.empty_workspace(q, cache)
     kv4.attend(q, cache, table, lengths, heads, workspace, window=window)
     out = torch.empty_like(x)
-    w4.matvec_w4(heads.view(x.shape[0], -1), *w.out, out)
+    w4.matvec_w4(heads.view(x.shape[0], w.q_heads * dim), *w.out, out)
     return out
 
 
