@@ -39,7 +39,10 @@ def decode_part(x: torch.Tensor, w: HeadWeights, cache: kv4.Cache, table: torch.
                 window: int = 0) -> torch.Tensor:
     """One rank's part of the layer's output for x [batch * queries, hidden], the last ``queries`` tokens of
     each sequence; ``table`` and ``lengths`` as ``kv4.attend`` takes them, these tokens counted. A
-    sequence whose length is 0 (a padded request) writes nothing and gives zeros.
+    sequence whose length is 0 (a padded request) writes nothing and gives zeros. Lengths stay on the device and are not checked:
+    give a sequence its pages before it needs them. Of one longer than its table (``table.shape[1] * cache.page``) the tokens past
+    the table are not written, and its queries see what queries of a sequence that just fills the table see; other sequences are
+    as always.
     ``rotate(q, k, positions)`` maps queries [batch, queries, q_heads, head_dim] and keys [batch, queries, heads, head_dim]
     at positions [batch, queries] to what is attended with and cached."""
     batch, dim = lengths.shape[0], cache.head_dim
