@@ -3,7 +3,7 @@ sequences that fill their table, every kind of wire mode. The layer of test_gpu_
 import pytest
 import torch
 
-from block_quantized_wire_gb300 import attention, kv4, w4
+from block_quantized_wire_gb300 import attention, kv4, topology, w4
 from tests.test_gpu_kv4 import a_layer
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +46,61 @@ def test_a_sequence_past_its_table_writes_nothing_and_sees_what_is_held(queries)
     out = torch.empty_like(x)
     w4.matvec_w4(heads.view(4 * queries, 256), *rank.out, out)
     assert torch.equal(got, out) and torch.equal(got[2 * queries:], want[2 * queries:])
+
+
+def by_hand(x, rank, cache, table, lengths, queries, window):
+    """A part's operators one after another, the slots of the tokens found position by position."""
+    batch, dim = len(lengths), cache.head_dim
+    both = torch.empty(x.shape[0], rank.qkv[0].shape[0], dtype=x.dtype, device="cuda")
+    w4.matvec_w4(x, *rank.qkv, both)
+    nq, nk = rank.q_heads * dim, rank.heads * dim
+    q, k, v = (both[:, a:b].contiguous() for a, b in ((0, nq), (nq, nq + nk), (nq + nk, nq + 2 * nk)))
+    at = []
+    for b, n in enumerate(lengths.tolist()):
+        for j in range(n - queries, n):
+            at.append(int(table[b, j // cache.page]) * cache.page + j % cache.page if j >= 0 else -1)
+    kv4.write(k.view(-1, rank.heads, dim), v.view(-1, rank.heads, dim), torch.tensor(at, device="cuda"), cache)
+    q = q.view(batch, queries, rank.q_heads, dim)
+    heads, out = torch.empty_like(q), torch.empty_like(x)
+    kv4.attend(q, cache, table, lengths, heads, kv4.empty_workspace(q, cache), window=window)
+    w4.matvec_w4(heads.view(x.shape[0], nq), *rank.out, out)
+    return out
+
+
+@pytest.mark.parametrize("queries,window", [(1, 0), (1, 7), (4, 0), (5, 12)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_part_is_its_operators_one_after_another(dtype, queries, window):
+    torch.manual_seed(queries + window)
+    hidden, q_heads, heads, dim, page, lens = 256, 6, 2, 128, 16, [70, 3, 0, 33, 16]
+    qkv = (torch.randn((q_heads + 2 * heads) * dim, hidden, device="cuda") / 16).to(dtype)
+    o = (torch.randn(hidden, q_heads * dim, device="cuda") / 28).to(dtype)
+    rank = attention.quantize_heads(q_heads, heads, qkv, o)
+    a, b = (kv4.empty_cache(30, heads, page, dim, 64, dtype) for _ in range(2))
+    rows = torch.randn(480, heads, dim, device="cuda").to(dtype)
+    for c in (a, b):
+        for t in (c.k, c.v, c.k_scales, c.v_scales):
+            t.zero_()
+        kv4.write(rows, rows * 0.5, torch.arange(480, device="cuda"), c)
+    table = torch.randperm(30, device="cuda")[:25].int().view(5, 5)
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = kv4.empty_workspace(torch.empty(5, queries, q_heads, dim, dtype=dtype, device="cuda"), a)
+    for step in range(2):
+        x = torch.randn(5 * queries, hidden, device="cuda").to(dtype)
+        got = attention.decode_part(x, rank, a, table, lengths, queries, workspace=ws, window=window)
+        want = by_hand(x, rank, b, table, lengths, queries, window)
+        assert torch.equal(got, want) and bool(torch.isfinite(got.float()).all())
+        assert not got.view(5, queries, hidden)[2].any()  # the padded request
+        for s, t in zip((a.k, a.v, a.k_scales, a.v_scales), (b.k, b.v, b.k_scales, b.v_scales)):
+            assert torch.equal(s, t)
+        lengths = torch.where(lengths > 0, lengths + queries, 0).int()
+
+
+@pytest.mark.parametrize("mode", ["i8_ag", "e4m3_ag", "mx_ring", "mx_a2a"])
+def test_a_layer_sums_its_parts_as_the_wire_mode_does(mode):
+    ranks, caches, table, lengths, (x,) = a_layer(mode, steps=1)
+    lengths += 1
+    parts = [attention.decode_part(x, r, c, table, lengths) for r, c in zip(ranks, caches)]
+    want = topology.MODES[mode](parts)[2]
+    got = attention.decode_layer(x, ranks, caches, table, lengths, mode)  # writes the same rows once more
+    want = [want] if isinstance(want, torch.Tensor) else list(want)
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
