@@ -1,0 +1,87 @@
+"""Attention over the 4-bit cache by checks that see a single lost position, and over values of every size."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from block_quantized_wire_gb300 import kv4
+from tests.kv4_checks import BITS, check_rows, check_shares, marked_codes, rows_of, shares
+from tests.test_gpu_kv4 import TYPES, fill, run, table_of
+from tests.test_gpu_kv4_ranges import problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("shape", [([9000, 100], 1, 8, 1, 64, 32, 64), ([2049, 1, 700], 1, 8, 4, 128, 64, 32), ([3000], 4, 16, 2, 128, 128, 100),
+                                   ([40, 33, 0, 500], 2, 15, 3, 192, 64, 24), ([1500], 1, 4, 2, 256, 32, 16), ([70] * 60, 1, 4, 4, 64, 64, 10)])
+def test_rows_are_as_accurate_as_their_roundings(shape, name):
+    lens, *rest = shape
+    q, cache, table, lengths = problem(sum(lens), lens, *rest, dtype=TYPES[name][0])
+    out, lse = run(q, cache, table, lengths)
+    check_rows(out, lse, rows_of(q, cache, table, lengths, rest[3] ** -0.5), BITS[name])
+
+
+# lengths, queries, q heads, heads, dim, group, page, window: one and many CTAs a sequence, shares that begin within sequences, one-tile
+# items, more items than words, 8 and 16 rows, several chunks of rows
+SHARES = [([65000], 1, 1, 1, 64, 64, 64, 0), ([20000], 1, 8, 1, 64, 32, 64, 0), ([20000, 0, 33], 1, 9, 1, 128, 64, 32, 0),
+          ([5000, 9000, 1, 31, 32, 64, 0, 2], 1, 8, 2, 128, 32, 100, 0), ([700] * 70, 1, 8, 8, 64, 64, 16, 0),
+          ([65] * 600, 1, 2, 2, 64, 32, 24, 0), ([20] * 200, 8, 16, 4, 64, 64, 32, 0), ([6000, 90], 40, 4, 1, 128, 128, 64, 0),
+          ([3000, 200], 3, 12, 2, 192, 32, 10, 0), ([4000], 1, 8, 1, 256, 128, 128, 0), ([9000, 50], 1, 4, 1, 64, 64, 64, 1000),
+          ([900, 2, 400], 5, 4, 2, 256, 64, 48, 33), ([128 * 37] * 5, 1, 8, 4, 128, 64, 128, 0)]
+
+
+@pytest.mark.parametrize("shape", SHARES)
+def test_every_position_counts_once(shape):
+    # scores of zero and values that mark their position: a position lost or counted twice, anywhere, moves a column
+    lens, n_q, q_heads, heads, dim, group, page, window = shape
+    rng = np.random.default_rng(sum(lens))
+    pages = sum(-(-n // page) for n in lens) + 2
+    cache = kv4.empty_cache(pages, heads, page, dim, group, torch.float16)
+    fill(rng, cache)
+    table = table_of(rng, lens, page, -(-max(lens) // page) + 1, pages)
+    cache.v.zero_()
+    cache.v_scales[..., 0], cache.v_scales[..., 1] = 1.0, 0.0
+    codes = torch.from_numpy(marked_codes(max(lens), dim)).cuda()
+    packed = ((codes[:, 0::2] & 15) | ((codes[:, 1::2] & 15) << 4)).to(torch.uint8)
+    for b, n in enumerate(lens):
+        at = kv4.slots(table[b:b + 1], torch.arange(n, device="cuda")[None], page)[0]
+        cache.v[at // page, :, at % page] = packed[:n, None]
+    q = torch.zeros(len(lens), n_q, q_heads, dim, dtype=torch.float16, device="cuda")
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = run(q, cache, table, lengths, window=window)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        want = shares(n, n_q, window, dim)
+        for h in range(q_heads):
+            check_shares(out[b, :, h], want)
+        for i in range(n_q):
+            count = max(0, min(n - n_q + i + 1, window or n))
+            assert np.all(np.abs(lse[b, i] - math.log(count)) <= 2.0 ** -20 * (1 + math.log(count))) if count else \
+                np.all(np.isneginf(lse[b, i]))
+
+
+# ---------------------------------------------------------------- values of every size
+@pytest.mark.parametrize("up", [-70, -40, 0, 40, 60, 95, 97, 111, 112, 116, 120])
+def test_rows_of_scales_of_any_size(up):
+    # the values' scales and offsets times a power of two, which the output follows
+    q, cache, table, lengths = problem(5, [900, 33], 1, 4, 1, 128, 64, 32)
+    cache.v_scales *= 2.0 ** up
+    check_rows(*run(q, cache, table, lengths), rows_of(q, cache, table, lengths, 128 ** -0.5), 8)
+    cache.v_scales[..., 1] = 0  # without offsets, and with nothing else
+    check_rows(*run(q, cache, table, lengths), rows_of(q, cache, table, lengths, 128 ** -0.5), 8)
+    cache.v_scales[..., 1], cache.v_scales[..., 0] = 2.0 ** up, 0
+    check_rows(*run(q, cache, table, lengths), rows_of(q, cache, table, lengths, 128 ** -0.5), 8)
+
+
+def test_offsets_of_any_size_beside_no_steps():
+    # scales of 0, scores of 0: the mean of the offsets, binary32 sums and one rounding
+    q, cache, table, lengths = problem(6, [300, 40, 1], 1, 8, 2, 64, 32, 16)
+    q.zero_()
+    cache.v_scales[..., 0] = 0
+    for up in (0, 100, 20):
+        cache.v_scales[..., 1] *= 2.0 ** up  # 1, 2^100, 2^120
+        out = run(q, cache, table, lengths)[0].double().cpu().numpy()
+        for at, want, _, w, _, _, z in rows_of(q, cache, table, lengths, 0.125):
+            assert np.all(np.abs(out[at] - want) <= 2.0 ** -8 * np.abs(want) + (len(w) / 16 + 64) * 2.0 ** -23 * (w @ np.abs(z)))
