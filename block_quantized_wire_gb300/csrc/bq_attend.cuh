@@ -44,6 +44,9 @@ constexpr float kNothing = -3.0e38f;              // the reference of a row that
 constexpr float kUnit = 0x1p-24f;                 // of a code held as an FP16's lowest mantissa bits
 constexpr float kLift = 13.0f;                    // log2 of the largest p s beside a fresh reference
 constexpr int kLowest = -80;                      // level of the smallest scales: 2^31 weights of 2^(14 - level) are 2^125
+// The level that a reference takes in at most: the largest weight is 2^-83, and what ex2.approx.ftz makes zero (below 2^-126) 2^-43 of
+// it. Larger scales (BF16's reach 2^128) come down by the rest, a power of two that the sums of p s get back at the end.
+constexpr int kHighest = 96;
 constexpr int kMaxAttendCtas = 456;               // three on each of 152 SMs
 
 // What a call's kernels share beside its arguments.
@@ -204,6 +207,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 __device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+// Binary places that scales come down by.
+template <class T>
+__device__ __forceinline__ int places_down(int level)
+{
+    return std::is_same<T, __half>::value ? 0 : max(level - kHighest, 0);
+}
 
 // N pairs at a shared address, in the widest loads that its alignment (the largest power of two in 4 N bytes) allows.
 template <int N>
@@ -222,6 +231,11 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N])
 #pragma unroll
         for (int i = 0; i < N; i++) w[i] = lds_u32(at + 4 * i);
     }
+}
+
+__device__ __forceinline__ void sts_u16(uint32_t at, uint16_t v)
+{
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
 }
 
 // 8x8 matrices of 16-bit elements, the row of lane 8 m + i row i of matrix m.
@@ -465,6 +479,7 @@ struct Rows {
     float2 ref[F::kHalves];                                 // A
     int level;                                              // log2 of the largest scale so far, and the largest (scale, offset)
     uint32_t limit;                                         // bits that do not pass it: offsets count 2^-24
+    float bound;                                            // log2 of p that may not be passed; nothing passes it where scales come down
     float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
     float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
     float eights[F::kGroups][F::kHalves][4];                // of 8 p s, in units, c0 c1 as c2 c3: groups apart, for their NaNs
@@ -488,8 +503,7 @@ struct Rows {
 
     __device__ __forceinline__ void start(const Kv4Attend &a, int lane, const Queries &raw)
     {
-        level = kLowest;
-        limit = limit_of<T>(level);
+        set_level(kLowest);
         const int q = lane & 3;
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
@@ -562,6 +576,13 @@ struct Rows {
 #pragma unroll
                 for (int k = 0; k < 4; k++) eights[g][h][k] = 0.0f;
         }
+    }
+
+    __device__ __forceinline__ void set_level(int to)
+    {
+        level = to;
+        limit = limit_of<T>(to);
+        bound = places_down<T>(to) > 0 ? -INFINITY : kLift + 1.0f - (float)to;
     }
 
     // x[n][t]: in units, of token 16 n + 8 t + r
@@ -668,9 +689,9 @@ struct Rows {
                     }
         };
         exponents();
-        // p s stays within 2^14 as long as no scale passes the level and no p 2^(14 - level): every lane looks at its own
+        // p s, s come down, stays within 2^14 as long as no scale passes the level and no p 2^(14 - level): every lane looks at its own
         // tokens, and the rows' largest scores are looked for where one does
-        if (__any_sync(kFull, most > kLift + 1.0f - (float)level || above != limit)) {
+        if (__any_sync(kFull, most > bound || above != limit)) {
             int k = level;
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++) {
@@ -678,8 +699,18 @@ struct Rows {
                 if (finite_bits<T>(scale)) k = max(k, exponent_of<T>(scale) + 1);
                 if (finite_bits<T>(offset)) k = max(k, exponent_of<T>(offset) - 23);
             }
-            level = __reduce_max_sync(kFull, k);
-            limit = limit_of<T>(level);
+            k = __reduce_max_sync(kFull, k);
+            const float less = power_of_2(places_down<T>(level) - places_down<T>(k));  // for sums of p s
+            set_level(k);
+            // Scales that come down do so in the tile itself, each lane its token's: every such tile comes here (a product for each
+            // scale where it is used cost 64 sequences of up to 8192 tokens 1 %).
+            if (places_down<T>(k) > 0) {
+                const float down = power_of_2(-places_down<T>(k));
+#pragma unroll
+                for (int g = 0; g < F::kGroups; g++)
+                    sts_u16(pairs + 4 * (F::kGroups * lane + g), Value<T>::round(__fmul_rn(pair_values<T>(mine[g]).x, down)));
+                __syncwarp();
+            }
 #pragma unroll
             for (int h = 0; h < F::kHalves; h++) {
                 float2 top = splat(-INFINITY);
@@ -695,7 +726,7 @@ struct Rows {
                     top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, d));
                     top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
                 }
-                const float up = (float)level - kLift;
+                const float up = (float)(level - places_down<T>(level)) - kLift;
                 float2 next = ref[h];
                 if (top.x > -INFINITY) next.x = fmaxf(next.x, __fadd_rn(__fmul_rn(top.x, f[h].x), up));
                 if (top.y > -INFINITY) next.y = fmaxf(next.y, __fadd_rn(__fmul_rn(top.y, f[h].y), up));
@@ -704,14 +735,15 @@ struct Rows {
                 total[h] = mul2(total[h], keep);
 #pragma unroll
                 for (int g = 0; g < F::kGroups; g++) off[h][g] = mul2(off[h][g], keep);
+                const float2 keep_ps = mul2(keep, splat(less));
 #pragma unroll
                 for (int m = 0; m < F::kDim / 16; m++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? keep.y : keep.x);
+                    for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? keep_ps.y : keep_ps.x);
 #pragma unroll
                 for (int g = 0; g < F::kGroups; g++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? keep.y : keep.x);
+                    for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? keep_ps.y : keep_ps.x);
             }
             exponents();
         }
@@ -781,6 +813,7 @@ struct Rows {
     // The lanes' parts brought together: total in every lane of a row, sum the true sums of p v.
     __device__ __forceinline__ void finish()
     {
+        const float up = power_of_2(24 + places_down<T>(level));  // 1 / kUnit and what scales came down by
         const auto all = [](float2 v) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)
@@ -800,7 +833,7 @@ struct Rows {
                     for (int i = 0; i < 4; i++) {
                         const float u = k & 1 ? __fmul_rn(v[i], 0.0625f) : v[i];
                         const float c = eights[g][h][i];
-                        v[i] = __fmaf_rn(__fsub_rn(u, c), 1.0f / kUnit, i & 1 ? z.y : z.x);
+                        v[i] = __fmaf_rn(__fsub_rn(u, c), up, i & 1 ? z.y : z.x);
                     }
                 }
             }

@@ -477,7 +477,7 @@ BQ_API bq_status bq_kv4_read(const bq_kv4_cache *cache, const void *slots, int s
  * width * page < 2^31 - 2^20; window <= 2^30. Products and sums are binary32 (the tensor cores may
  * truncate where a binary32 addition would round); a softmax weight times a value's scale is rounded to
  * FP16, at a common power of two that keeps what is 2^-28 or more of the largest (of scales of 2^-80 and
- * more); the output is rounded once. A call repeated gives the same bits. Made for a few rows, queries
+ * more; beside one of 2^96 and more, of 2^-48 and more); the output is rounded once. A call repeated gives the same bits. Made for a few rows, queries
  * times heads that share a key-value head: the cache is read once for every 16 of them, 8 where head_dim >
  * 128. Two launches; sequences of all lengths share the GPU evenly. */
 BQ_API bq_status bq_kv4_attend(const bq_kv4_cache *cache, const void *q, int64_t q_ld_batch, int64_t q_ld_query,

@@ -75,6 +75,37 @@ def test_rows_of_scales_of_any_size(up):
     check_rows(*run(q, cache, table, lengths), rows_of(q, cache, table, lengths, 128 ** -0.5), 8)
 
 
+def winner_of(n, winner, below, q_heads=4, n_q=1, dtype=torch.bfloat16, dim=64):
+    """A sequence whose position `winner` has a score of `below` ln 2 above all others, for every query; values of about 1."""
+    cache = kv4.empty_cache(-(-n // 32), 1, 32, dim, 32, dtype)
+    fill(np.random.default_rng(n), cache)
+    cache.k.zero_()
+    cache.k_scales[..., 0], cache.k_scales[..., 1] = 1.0, 0.0
+    cache.k[winner // 32, 0, winner % 32, 0] = 7
+    table = torch.arange(-(-n // 32), dtype=torch.int32, device="cuda")[None]
+    q = torch.zeros(1, n_q, q_heads, dim, dtype=dtype, device="cuda")
+    q[..., 0] = 1
+    return q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), below * math.log(2) / 7
+
+
+@pytest.mark.parametrize("up", [60, 97, 112, 120, 124])
+@pytest.mark.parametrize("n,below", [(40000, 15), (500, 16), (300, 8), (130000, 17)])
+def test_many_small_weights_beside_a_large_one(n, below, up):
+    # their sum is what counts in lse and in the output, whatever the values' size
+    q, cache, table, lengths, scale = winner_of(n, n // 3, below)
+    cache.v_scales[..., 0], cache.v_scales[..., 1] = 2.0 ** up, 0.0
+    cache.v.fill_(0x33)  # values of 3 scales, the winner's of 1
+    cache.v[n // 3 // 32, 0, n // 3 % 32] = 0x11
+    out, lse = run(q, cache, table, lengths, scale=scale)
+    all_of = 2.0 ** below + n - 1
+    steps = (n / 16 + 64) * 2.0 ** -23
+    # scores: one product, a rounding each of scale, of its product with log2 e and with x, ex2 and log: 8 steps of 2^-23 of 17 ln 2
+    assert bool(((lse.double() - math.log(all_of)).abs() <= 8 * 17 * 2.0 ** -23 + steps + 2.0 ** -21).all())
+    want = (2.0 ** below + 3 * (n - 1)) / all_of
+    # the output's rounding, the weights' to FP16, sums of code + 8 less 8 times the weights; the scores' error above
+    assert bool(((out.double() * 2.0 ** -up - want).abs() <= want * (2.0 ** -8 + 2.0 ** -11 + 16 * 17 * 2.0 ** -23) + 19 * steps).all())
+
+
 def test_offsets_of_any_size_beside_no_steps():
     # scales of 0, scores of 0: the mean of the offsets, binary32 sums and one rounding
     q, cache, table, lengths = problem(6, [300, 40, 1], 1, 8, 2, 64, 32, 16)
