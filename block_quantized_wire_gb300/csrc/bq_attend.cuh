@@ -15,8 +15,9 @@
 // eight codes costs five logic instructions. q is scaled by a power of two per row that brings its
 // largest value to 2^14 .. 2^15, which FP16 then holds exactly down to 2^-28 of that. Only p s is rounded, to FP16
 // (2^-11): it is used rounded in the sum over u and in the -8 correction (a mma with a constant matrix), so that
-// u's offset does not enlarge that error. p's reference A takes in the size of s, p = 2^(y - A), A = max y + log2 max s
-// - 13, so that p s stays within 2^14 and is exact to 2^-11 down to 2^-28 of the largest.
+// u's offset does not enlarge that error. p's reference A takes in the size of s, p = 2^(y - A), A = max(y + log2 s) - 9
+// or less over what the row sees, so that p s stays within 2^14, is exact to 2^-11 down to 2^-22 of the row's largest, and
+// to 2^-33 of that below.
 //
 // Fragments. Codes are the m side of both products: tokens of the keys, columns of the values, which ldmatrix and its
 // transposing form deliver as they lie. Scores come with tokens as rows and queries as columns; p s, rounded, is
@@ -42,11 +43,15 @@ constexpr int kAttendWarps = 4, kAttendThreads = 32 * kAttendWarps;
 constexpr int kTokens = 32;                       // of a tile
 constexpr float kNothing = -3.0e38f;              // the reference of a row that has seen nothing
 constexpr float kUnit = 0x1p-24f;                 // of a code held as an FP16's lowest mantissa bits
-constexpr float kLift = 13.0f;                    // log2 of the largest p s beside a fresh reference
+constexpr float kLift = 13.0f;                    // log2 that p s may have beside a fresh reference; one more before there is another
 constexpr int kLowest = -80;                      // level of the smallest scales: 2^31 weights of 2^(14 - level) are 2^125
-// The level that a reference takes in at most: the largest weight is 2^-83, and what ex2.approx.ftz makes zero (below 2^-126) 2^-43 of
-// it. Larger scales (BF16's reach 2^128) come down by the rest, a power of two that the sums of p s get back at the end.
+// The level that a reference takes in at most: a row's largest weight is 2^-87 or more, and what ex2.approx.ftz makes zero
+// (below 2^-126) 2^-39 of it. Larger scales (BF16's reach 2^128) come down by the rest, a power of two that the sums of p s get back at the end.
 constexpr int kHighest = 96;
+// A fresh reference leaves a row's largest p s so many places below kLift. A tile is looked at more closely where a p could pass the
+// level, whatever its own s, and with less room that is more often: 64 sequences of up to 8192 tokens took 72.8 us with 4, 75.4 where
+// references went by max y and the level, which a value that a row does not see, or gives no weight, may put far above any of its p s.
+constexpr float kSlack = 4.0f;
 constexpr int kMaxAttendCtas = 456;               // three on each of 152 SMs
 
 // What a call's kernels share beside its arguments.
@@ -690,16 +695,17 @@ struct Rows {
         };
         exponents();
         // p s, s come down, stays within 2^14 as long as no scale passes the level and no p 2^(14 - level): every lane looks at its own
-        // tokens, and the rows' largest scores are looked for where one does
+        // tokens, and the rows' largest p s are looked for where one does
         if (__any_sync(kFull, most > bound || above != limit)) {
-            int k = level;
+            int k = kLowest;
 #pragma unroll
             for (int g = 0; g < F::kGroups; g++) {
                 const uint32_t scale = mine[g] & 0x7fffu, offset = (mine[g] >> 16) & 0x7fffu;
                 if (finite_bits<T>(scale)) k = max(k, exponent_of<T>(scale) + 1);
                 if (finite_bits<T>(offset)) k = max(k, exponent_of<T>(offset) - 23);
             }
-            k = __reduce_max_sync(kFull, k);
+            const int token = k;  // the lane's token's level
+            k = __reduce_max_sync(kFull, max(k, level));
             const float less = power_of_2(places_down<T>(level) - places_down<T>(k));  // for sums of p s
             set_level(k);
             // Scales that come down do so in the tile itself, each lane its token's: every such tile comes here (a product for each
@@ -711,6 +717,12 @@ struct Rows {
                     sts_u16(pairs + 4 * (F::kGroups * lane + g), Value<T>::round(__fmul_rn(pair_values<T>(mine[g]).x, down)));
                 __syncwarp();
             }
+            float add[2][2];  // log2 of what a token's p is multiplied by, at most
+#pragma unroll
+            for (int n = 0; n < 2; n++)
+#pragma unroll
+                for (int t = 0; t < 2; t++)
+                    add[n][t] = (float)max(__shfl_sync(kFull, token, 16 * n + 8 * t + r) - places_down<T>(k), kLowest);
 #pragma unroll
             for (int h = 0; h < F::kHalves; h++) {
                 float2 top = splat(-INFINITY);
@@ -718,18 +730,18 @@ struct Rows {
                 for (int n = 0; n < 2; n++)
 #pragma unroll
                     for (int t = 0; t < 2; t++) {
-                        if (sees(h, 0, n, t)) top.x = fmaxf(top.x, x[n][t][h].x);
-                        if (sees(h, 1, n, t)) top.y = fmaxf(top.y, x[n][t][h].y);
+                        const float2 v = fma2(x[n][t][h], f[h], splat(add[n][t]));
+                        if (sees(h, 0, n, t)) top.x = fmaxf(top.x, v.x);
+                        if (sees(h, 1, n, t)) top.y = fmaxf(top.y, v.y);
                     }
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
                     top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, d));
                     top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
                 }
-                const float up = (float)(level - places_down<T>(level)) - kLift;
                 float2 next = ref[h];
-                if (top.x > -INFINITY) next.x = fmaxf(next.x, __fadd_rn(__fmul_rn(top.x, f[h].x), up));
-                if (top.y > -INFINITY) next.y = fmaxf(next.y, __fadd_rn(__fmul_rn(top.y, f[h].y), up));
+                if (top.x > -INFINITY) next.x = fmaxf(next.x, __fadd_rn(top.x, kSlack - kLift));
+                if (top.y > -INFINITY) next.y = fmaxf(next.y, __fadd_rn(top.y, kSlack - kLift));
                 const float2 keep = make_float2(exp2_fast(__fsub_rn(ref[h].x, next.x)), exp2_fast(__fsub_rn(ref[h].y, next.y)));
                 ref[h] = next;
                 total[h] = mul2(total[h], keep);

@@ -106,6 +106,49 @@ def test_many_small_weights_beside_a_large_one(n, below, up):
     assert bool(((out.double() * 2.0 ** -up - want).abs() <= want * (2.0 ** -8 + 2.0 ** -11 + 16 * 17 * 2.0 ** -23) + 19 * steps).all())
 
 
+# products of a weight and a scale are rounded at a power of two of the row's own: to 2^-33 of the row's largest
+@pytest.mark.parametrize("name,up", [("bf16", 40), ("bf16", 100), ("f16", 23)])
+@pytest.mark.parametrize("n_q,window", [(3, 0), (3, 40), (16, 70)])
+def test_large_values_that_a_query_does_not_see_are_nothing_to_it(name, up, n_q, window):
+    # the last position, which the last query alone sees, and with a window the first one of the first query
+    dtype = TYPES[name][0]
+    q, cache, table, lengths = problem(up + n_q, [200, 77, 130], n_q, 4, 2, 128, 32, 32, dtype)
+    if name == "f16":
+        cache.v_scales *= 2.0 ** -10
+    clean, clean_lse = run(q, cache, table, lengths, window=window)
+    for b, n in enumerate(lengths.tolist()):
+        for j in ([n - 1, n - n_q + 1 - window] if window else [n - 1]):
+            if j >= 0:
+                cache.v_scales[table[b, j // 32], :, j % 32] *= 2.0 ** up
+    out, lse = run(q, cache, table, lengths, window=window)
+    scale = 128 ** -0.5
+    check_rows(out, lse, rows_of(q, cache, table, lengths, scale, window), BITS[name])
+    between = slice(1 if window else 0, n_q - 1)
+    rows = [r for r in rows_of(q, cache, table, lengths, scale, window) if between.start <= r[0][1] < between.stop]
+    check_rows(clean, clean_lse, rows, BITS[name])
+
+
+@pytest.mark.parametrize("name,up", [("bf16", 30), ("bf16", 50), ("bf16", 90), ("f16", 23)])
+@pytest.mark.parametrize("n", [33, 500, 5000])
+def test_large_values_of_no_weight(name, up, n):
+    # a position 2^up times larger than all others whose weight is 2^-(up + 20) of theirs
+    dtype = TYPES[name][0]
+    q, cache, table, lengths, scale = winner_of(n, n // 2, up + 20, dtype=dtype)
+    if name == "f16":
+        cache.v_scales *= 2.0 ** -10
+    cache.v_scales[n // 2 // 32, 0, n // 2 % 32] *= 2.0 ** up
+    out, lse = run(q, cache, table, lengths, scale=-scale)
+    check_rows(out, lse, rows_of(q, cache, table, lengths, -scale), BITS[name])
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+def test_large_weights_of_small_values(name):
+    # a sink: one position takes nearly all weight and holds next to nothing, the others' part is the output
+    q, cache, table, lengths, scale = winner_of(3000, 0, 12, dtype=TYPES[name][0])
+    cache.v_scales[0, 0, 0] *= 2.0 ** -13
+    check_rows(*run(q, cache, table, lengths, scale=scale), rows_of(q, cache, table, lengths, scale), BITS[name])
+
+
 def test_offsets_of_any_size_beside_no_steps():
     # scales of 0, scores of 0: the mean of the offsets, binary32 sums and one rounding
     q, cache, table, lengths = problem(6, [300, 40, 1], 1, 8, 2, 64, 32, 16)
