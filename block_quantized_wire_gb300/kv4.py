@@ -29,7 +29,8 @@ class Cache:
     pairs. Any strides that keep rows contiguous and apart (a view that has tokens before heads, or
     keys and values of a page in one block, works), the same for keys and values; rows of codes
     start on 16-byte boundaries, rows of pairs on the largest power of two that divides their
-    bytes, at most 16. The tensors must stay where they are while the object is in use."""
+    bytes, at most 16. 1 to 1024 heads, 1 to 65536 tokens a page. The tensors must stay where they
+    are while the object is in use."""
 
     def __init__(self, k: torch.Tensor, k_scales: torch.Tensor, v: torch.Tensor, v_scales: torch.Tensor):
         dtype = k_scales.dtype
@@ -48,6 +49,8 @@ class Cache:
         if head_dim not in HEAD_DIMS or group not in GROUPS or groups * group != head_dim:
             raise ValueError(f"Cache: head_dim {head_dim} with {groups} scales a row: head_dim must be 64, 128, 192 or "
                              "256, and a scale covers 32, 64 or 128 columns")
+        if not 1 <= heads <= 1024 or not 1 <= page <= 65536:  # BQ_KV4_MAX_HEADS, BQ_KV4_MAX_PAGE
+            raise ValueError(f"Cache: 1 to 1024 heads and 1 to 65536 tokens a page, got {heads} and {page}")
         for t, last in ((k, (1,)), (v, (1,)), (k_scales, (2, 1)), (v_scales, (2, 1))):
             if t.stride()[3:] != last and not (t.dim() == 5 and groups == 1 and t.stride(4) == 1):
                 raise ValueError("Cache: rows of codes and of scales must be contiguous")
@@ -138,6 +141,8 @@ def _query_shape(call: str, q: torch.Tensor, cache: Cache):
     if len(shape) != 4 or shape[3] != cache.head_dim or shape[2] % cache.heads:
         raise ValueError(f"{call}: q must be [batch, queries, a multiple of {cache.heads} heads, {cache.head_dim}], got "
                          f"{tuple(shape)}")
+    if shape[2] > 1 << 16 or shape[1] * shape[2] > 1 << 20:
+        raise ValueError(f"{call}: {shape[1]} queries of {shape[2]} heads are more than a call takes")
     return shape
 
 
