@@ -359,8 +359,6 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ uint32_t divide_by(uint32_t n, const Divisor &d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
-
 // A warp's copies: the tile after next is looked up in the table while the tile before it is
 // still on its way, so that no copy waits for its page number.
 template <class T, class F>

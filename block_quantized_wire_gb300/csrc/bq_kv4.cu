@@ -13,8 +13,6 @@
 namespace bqk {
 namespace {
 
-__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor &d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
-
 struct RowUnits {
     Kv4Cache c;
     Kv4Rows k, v;
@@ -35,8 +33,8 @@ struct Place {
 
     __device__ __forceinline__ Place(const RowUnits &a, uint32_t u)
     {
-        const uint32_t r = divide(u, a.per_row), piece = u - r * a.per_row.d;
-        const uint32_t token = divide(r, a.heads), head = r - token * a.heads.d;
+        const uint32_t r = divide_by(u, a.per_row), piece = u - r * a.per_row.d;
+        const uint32_t token = divide_by(r, a.heads), head = r - token * a.heads.d;
         row[0] = static_cast<T *>(a.k.p) + token * a.k.ld_token + head * a.k.ld_head + 16 * piece;
         row[1] = static_cast<T *>(a.v.p) + token * a.v.ld_token + head * a.v.ld_head + 16 * piece;
         int64_t slot = -1;
@@ -52,7 +50,7 @@ struct Place {
         int64_t page;
         uint32_t in_page;
         if (a.n_slots < (1ll << 31)) {
-            page = divide((uint32_t)slot, a.page);
+            page = divide_by((uint32_t)slot, a.page);
             in_page = (uint32_t)slot - (uint32_t)page * a.page.d;
         } else {
             page = slot / a.c.page;

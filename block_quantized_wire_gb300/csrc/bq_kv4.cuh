@@ -6,6 +6,9 @@
 
 namespace bqk {
 
+// n < 2^31
+__device__ __forceinline__ uint32_t divide_by(uint32_t n, const Divisor &d) { return (__umulhi(n, d.mul) + n) >> d.shift; }
+
 // The two floats of a (scale, offset) pair.
 template <class T>
 __device__ __forceinline__ float2 pair_values(uint32_t w)
