@@ -46,12 +46,16 @@ constexpr float kUnit = 0x1p-24f;                 // of a code held as an FP16's
 constexpr float kLift = 13.0f;                    // log2 that p s may have beside a fresh reference; one more before there is another
 constexpr int kLowest = -80;                      // level of the smallest scales: 2^31 weights of 2^(14 - level) are 2^125
 // The level that a reference takes in at most: a row's largest weight is 2^-87 or more, and what ex2.approx.ftz makes zero
-// (below 2^-126) 2^-39 of it. Larger scales (BF16's reach 2^128) come down by the rest, a power of two that the sums of p s get back at the end.
+// (below 2^-126) 2^-39 of it. Larger scales (BF16's reach 2^128) come down by the rest, a power of two that the sums of p s get
+// back at the end.
 constexpr int kHighest = 96;
 // A fresh reference leaves a row's largest p s so many places below kLift. A tile is looked at more closely where a p could pass the
-// level, whatever its own s, and with less room that is more often: 64 sequences of up to 8192 tokens took 72.8 us with 4, 75.4 where
-// references went by max y and the level, which a value that a row does not see, or gives no weight, may put far above any of its p s.
-constexpr float kSlack = 4.0f;
+// level, whatever its own s, and with less room that is more often: 64 sequences of up to 8192 BF16 tokens took 78.9 us with 0, 76.1
+// with 1, 74.4 with 2, 72.5 with 4, 72.1 with 6. But sums that a tile's products stand far above lose more where the tensor cores
+// truncate: FP16 outputs (32 sequences of up to 4001, groups of 32), of whose relative error 2.07e-4 is their own rounding, were
+// 2.15e-4 off with 0, 2.16e-4 with 1 (32.6 us) and 2.22e-4 with 4 (31.9 us). BF16's rounding, 1.66e-3, leaves no difference.
+template <class T>
+constexpr float kSlack = std::is_same<T, __half>::value ? 1.0f : 4.0f;
 constexpr int kMaxAttendCtas = 456;               // three on each of 152 SMs
 
 // What a call's kernels share beside its arguments.
@@ -738,8 +742,8 @@ struct Rows {
                     top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
                 }
                 float2 next = ref[h];
-                if (top.x > -INFINITY) next.x = fmaxf(next.x, __fadd_rn(top.x, kSlack - kLift));
-                if (top.y > -INFINITY) next.y = fmaxf(next.y, __fadd_rn(top.y, kSlack - kLift));
+                if (top.x > -INFINITY) next.x = fmaxf(next.x, __fadd_rn(top.x, kSlack<T> - kLift));
+                if (top.y > -INFINITY) next.y = fmaxf(next.y, __fadd_rn(top.y, kSlack<T> - kLift));
                 const float2 keep = make_float2(exp2_fast(__fsub_rn(ref[h].x, next.x)), exp2_fast(__fsub_rn(ref[h].y, next.y)));
                 ref[h] = next;
                 total[h] = mul2(total[h], keep);
