@@ -24,11 +24,14 @@
 // turned over by movmatrix into the n side of the second product. So up to 8 query rows cost half the mma that 16 do, and all
 // that belongs to a query row (reference, sums, weights) lies in the lanes that hold its columns.
 //
-// What bounds it: the cache's bytes are the floor (144 a token and head at head_dim 128 and groups of 64), and the
-// instructions that turn codes into operands come next: 5 logic instructions for 8 codes, two cycles of a scheduler each, and an mma of eight
-// cycles for 512 codes (twice that for more than 8 rows), which overlap in small part only. At head_dim 128, groups of
-// 64 and 8 rows the copies alone run at 6.9 TB/s, the arithmetic alone as fast as 5.9 TB/s of cache would come, both at 5.5; a
-// call's ends (lengths, first tiles, joins) take about 12 us more. One sequence of 131072 tokens: 40 us; 64 of up to 8192: 75 us.
+// What bounds it: the cache's bytes are the floor (144 a token and head at head_dim 128 and groups of 64), and a warp's chain of
+// instructions that turn codes into operands comes next: 5 logic instructions for 8 codes, two cycles of a scheduler each, and an
+// mma of eight cycles for 256 codes (twice that for more than 8 rows). No pipe is full: for 64 sequences of up to 8192 tokens a
+// scheduler issues in 46 % of its cycles, the integer pipe is busy in 44 %, the tensor cores in 26 %, DRAM runs at 56 % of its
+// nominal rate. With 213 registers a scheduler has two warps, and the first stall is an instruction's own latency. With the
+// arithmetic taken out the copies ran at 6.9 TB/s, with the copies taken out the arithmetic at 5.9 TB/s of cache (each measured on a
+// changed copy of the kernel), both together at 5.6; a call's ends (lengths, first tiles, joins) take about 11 us more. One
+// sequence of 131072 tokens: 38 us; 64 of up to 8192: 72 us.
 #pragma once
 
 #include <cmath>
@@ -87,7 +90,8 @@ __device__ __forceinline__ int tiles_of(int begin, int end)
     return end > begin ? (end - first_of(begin) - 1) / kTokens + 1 : 1;
 }
 
-// What an item costs beside its tiles (its queries, the join of its warps), in tiles.
+// What an item costs beside its tiles (its queries, the join of its warps), in tiles: chosen where 8 rows of 128 columns share a key
+// head, and kept for all forms (64 sequences of up to 8192 tokens, when it was chosen: 78.7 us with 8, 76.0 with 12, 77.7 with 18).
 constexpr int kSetup = 12;
 
 // CTA i takes the run from i * per on. An item is kSetup places without a tile, then its tiles.
@@ -183,8 +187,10 @@ struct Form {
     static constexpr int kValid = 2 * (kCodeBytes + kPairBytes);  // a bit a token that is there
     static constexpr int kStage = kValid + 16;
     static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
-    // CTAs of an SM by their registers: 8 rows of 64 columns fit 168 a thread, all else up to 255. 8 rows of 128 columns with
-    // three CTAs (168, some spilled): 64 sequences of up to 8192 tokens took 77.3 us for 74.6; with four (128): 85.7.
+    // CTAs of an SM by their registers: 8 rows of 64 columns fit 168 a thread, all else up to 255, of which a few forms spill
+    // (at most 172 bytes of stores and 252 of loads a thread: 16 rows of 128 columns with groups of 32 and 64, 8 rows of 192 and
+    // 256 columns with groups of 32 and, of 256, 64). 8 rows of 128 columns with three CTAs (168, some spilled) took 77.3 us for 64
+    // sequences of up to 8192 tokens where two took 74.6, with four (128) 85.7; the other forms were not tried with more.
     static constexpr int kCtas = kRows == 8 && kDim == 64 ? 3 : 2;
     static constexpr int kRoom = (227 * 1024 / kCtas - 1024 - 512 - kJoin) / (kAttendWarps * kStage);
     static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
@@ -1113,7 +1119,8 @@ cudaError_t launch_form(const Kv4Cache &c, const Kv4Attend &a, AttendPlan &plan,
     return launch_kernel_block(kernel, plan.ctas, kAttendThreads, F::kSmem, st, c, a, plan);
 }
 
-// Rows of a form: what fits the registers.
+// Rows of a form: 16 where their sums, fragments of queries and corrections leave at most the spills named above. 16 rows of 192
+// columns would hold 96 sums and 48 fragments of queries, where 8 rows of 256, 64 and 32 of them, spill already.
 __host__ __device__ inline int form_rows(int rows, int dim) { return rows > 8 && dim <= 128 ? 16 : 8; }
 
 template <class T>

@@ -3,8 +3,9 @@
 // Both kernels are one pass: a lane takes 16 columns of a key and of its value (32 bytes each, one 256-bit access
 // where the rows allow it) and their 8 bytes of codes; a group's 2, 4 or 8 lanes share its pair. Key and value lie at the same
 // offsets of the cache, so that one slot is looked up and one place computed for both.
-// Reading 65536 tokens of 8 heads of 128 columns takes 54 us, 6.3 TB/s; writing 32768 and reading them back 63 us, of which
-// about 36 are the write's: 4.9 TB/s, bound by its instructions.
+// Reading 65536 tokens of 8 heads of 128 columns takes 54 us, 6.3 TB/s; writing 32768 of them 34 us, 5.2 TB/s (BF16 and FP16 within
+// 3 %). The write fills nothing: its schedulers issue in 61 % of their cycles, the integer pipe is busy in 52 %, and the first
+// stall of its 29 warps an SM is for their loads.
 #include <type_traits>
 
 #include "bq_codes.cuh"
@@ -95,7 +96,8 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half)
 // fl(t + r (d - t s)) is the correctly rounded quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990: t is off by one unit in the last place at most, and d - t s is exact): two paired
 // fused multiply-adds. BF16 rows have exact ties in half of all warps, so no shortcut around them pays: with a division
-// for values near a tie 32768 tokens of 8 heads took 73 us. Below 2^-90 remainders could lose bits: every value divides there.
+// for values near a tie 32768 tokens of 8 heads took 73 us, where this takes 37 (both a single cold launch under ncu).
+// Below 2^-90 remainders could lose bits: every value divides there.
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to the nearest integer
 
 __device__ __forceinline__ float exact_code(float d, float s)  // kRound + code

@@ -104,3 +104,28 @@ def test_a_layer_sums_its_parts_as_the_wire_mode_does(mode):
     got = attention.decode_layer(x, ranks, caches, table, lengths, mode)  # writes the same rows once more
     want = [want] if isinstance(want, torch.Tensor) else list(want)
     assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_captured_layer_follows_its_inputs():
+    ranks, caches, table, lengths, xs = a_layer("", steps=3)
+    again = [kv4.Cache(*(t.clone() for t in (c.k, c.k_scales, c.v, c.v_scales))) for c in caches]
+    x, lens, tab = xs[0].clone(), lengths.clone(), table.clone()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        attention.decode_layer(x, ranks, again, tab, torch.zeros_like(lens), "i8_a2a")  # writes nothing
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, = attention.decode_layer(x, ranks, again, tab, lens, "i8_a2a")
+    for step, new in enumerate(xs):
+        lengths += 1
+        if step == 2:
+            lengths[1] = 0  # a request that has ended
+            table[3] = table[3].roll(1)
+        want, = attention.decode_layer(new, ranks, caches, table, lengths, "i8_a2a")
+        x.copy_(new), lens.copy_(lengths), tab.copy_(table)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        for a, b in zip(caches, again):
+            assert torch.equal(a.k, b.k) and torch.equal(a.v_scales, b.v_scales)

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_quantized_wire_gb300 import kv4
+from block_quantized_wire_gb300 import _lib, build, codec, kv4
 from tests.kv4_checks import BITS, check_rows, check_shares, marked_codes, rows_of, shares
 from tests.test_gpu_kv4 import TYPES, fill, run, table_of
 from tests.test_gpu_kv4_ranges import problem
@@ -159,3 +159,14 @@ def test_offsets_of_any_size_beside_no_steps():
         out = run(q, cache, table, lengths)[0].double().cpu().numpy()
         for at, want, _, w, _, _, z in rows_of(q, cache, table, lengths, 0.125):
             assert np.all(np.abs(out[at] - want) <= 2.0 ** -8 * np.abs(want) + (len(w) / 16 + 64) * 2.0 ** -23 * (w @ np.abs(z)))
+
+
+def test_the_debug_build_declines_no_access_over_values_of_every_size(bq_lib):
+    with _lib.use_library(build.build_debug_library()):
+        codec.take_index_errors()
+        test_rows_of_scales_of_any_size(120)
+        test_large_values_of_no_weight("bf16", 90, 500)
+        test_every_position_counts_once(SHARES[5])
+        test_every_position_counts_once(SHARES[7])
+        torch.cuda.synchronize()
+        assert codec.take_index_errors() == 0
