@@ -54,11 +54,15 @@ constexpr int kLowest = -80;                      // level of the smallest scale
 constexpr int kHighest = 96;
 // A fresh reference leaves a row's largest p s so many places below kLift. A tile is looked at more closely where a p could pass the
 // level, whatever its own s, and with less room that is more often: 64 sequences of up to 8192 BF16 tokens took 78.9 us with 0, 76.1
-// with 1, 74.4 with 2, 72.5 with 4, 72.1 with 6. But sums that a tile's products stand far above lose more where the tensor cores
-// truncate: FP16 outputs (32 sequences of up to 4001, groups of 32), of whose relative error 2.07e-4 is their own rounding, were
-// 2.15e-4 off with 0, 2.16e-4 with 1 (32.6 us) and 2.22e-4 with 4 (31.9 us). BF16's rounding, 1.66e-3, leaves no difference.
+// with 1, 74.4 with 2, 72.5 with 4, 72.1 with 6 (before rows could be far, which costs about 1 us). But sums that a tile's products
+// stand far above lose more where the tensor cores truncate: FP16 outputs (32 sequences of up to 4001, groups of 32), of whose
+// relative error 2.07e-4 is their own rounding, were 2.15e-4 off with 0, 2.18e-4 with 2 (32.2 us) and 2.22e-4 with 4 (31.9 us).
+// BF16's rounding, 1.66e-3, leaves no difference.
 template <class T>
-constexpr float kSlack = std::is_same<T, __half>::value ? 1.0f : 4.0f;
+constexpr float kSlack = std::is_same<T, __half>::value ? 2.0f : 4.0f;
+// A warp one of whose references reaches this size is far from there on: a reference could not hold what the size of s adds to a
+// score. References are the largest scores themselves then, and scales come to within 2^kLift, up or down.
+constexpr float kFar = 0x1p21f;
 constexpr int kMaxAttendCtas = 456;               // three on each of 152 SMs
 
 // What a call's kernels share beside its arguments.
@@ -222,12 +226,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 __device__ __forceinline__ float power_of_2(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
-// Binary places that scales come down by.
-template <class T>
-__device__ __forceinline__ int places_down(int level)
-{
-    return std::is_same<T, __half>::value ? 0 : max(level - kHighest, 0);
-}
 
 // N pairs at a shared address, in the widest loads that its alignment (the largest power of two in 4 N bytes) allows.
 template <int N>
@@ -328,6 +326,24 @@ template <class T>
 __device__ __forceinline__ bool finite_bits(uint32_t bits)
 {
     return bits < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
+}
+
+// The level of a token's (scale, offset) pairs.
+template <class T, int N>
+__device__ __forceinline__ int level_of(const uint32_t (&pairs)[N])
+{
+    uint32_t most = 0;
+#pragma unroll
+    for (int g = 0; g < N; g++) most = __vmaxu2(most, pairs[g] & 0x7fff7fffu);
+    if (!finite_bits<T>(most & 0xffffu) || !finite_bits<T>(most >> 16)) {
+        most = 0;
+#pragma unroll
+        for (int g = 0; g < N; g++) {
+            const uint32_t scale = pairs[g] & 0x7fffu, offset = (pairs[g] >> 16) & 0x7fffu;
+            most = __vmaxu2(most, (finite_bits<T>(scale) ? scale : 0u) | (finite_bits<T>(offset) ? offset << 16 : 0u));
+        }
+    }
+    return max(kLowest, max(exponent_of<T>(most & 0xffffu) + 1, exponent_of<T>(most >> 16) - 23));
 }
 
 // The largest (scale, offset) bits without signs whose scale is below 2^level and offset below 2^(level + 24).
@@ -492,7 +508,8 @@ struct Rows {
     float2 ref[F::kHalves];                                 // A
     int level;                                              // log2 of the largest scale so far, and the largest (scale, offset)
     uint32_t limit;                                         // bits that do not pass it: offsets count 2^-24
-    float bound;                                            // log2 of p that may not be passed; nothing passes it where scales come down
+    float bound;                                            // log2 of p that may not be passed; all pass it where scales come down
+    bool far;                                               // the warp's rows, see kFar
     float2 total[F::kHalves], off[F::kHalves][F::kGroups];  // sums of p, and of p z
     float sum[F::kDim / 16][F::kHalves][4];                 // of p s u, in units
     float eights[F::kGroups][F::kHalves][4];                // of 8 p s, in units, c0 c1 as c2 c3: groups apart, for their NaNs
@@ -516,6 +533,7 @@ struct Rows {
 
     __device__ __forceinline__ void start(const Kv4Attend &a, int lane, const Queries &raw)
     {
+        far = false;
         set_level(kLowest);
         const int q = lane & 3;
 #pragma unroll
@@ -591,11 +609,41 @@ struct Rows {
         }
     }
 
+    // Binary places that scales come down by.
+    __device__ __forceinline__ int places() const
+    {
+        return far ? level - (int)kLift : std::is_same<T, __half>::value ? 0 : max(level - kHighest, 0);
+    }
     __device__ __forceinline__ void set_level(int to)
     {
         level = to;
         limit = limit_of<T>(to);
-        bound = places_down<T>(to) > 0 ? -INFINITY : kLift + 1.0f - (float)to;
+        bound = far || places() > 0 ? -INFINITY : kLift + 1.0f - (float)to;
+    }
+    // A row's sums after its reference has gone up: times keep, those of p s times less too.
+    __device__ __forceinline__ void move(int h, float2 keep, float less)
+    {
+        total[h] = mul2(total[h], keep);
+#pragma unroll
+        for (int g = 0; g < F::kGroups; g++) off[h][g] = mul2(off[h][g], keep);
+        const float2 keep_ps = mul2(keep, splat(less));
+#pragma unroll
+        for (int m = 0; m < F::kDim / 16; m++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? keep_ps.y : keep_ps.x);
+#pragma unroll
+        for (int g = 0; g < F::kGroups; g++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? keep_ps.y : keep_ps.x);
+    }
+    // A tile's scales come down, each lane its token's, whose pairs are `mine` as they were copied.
+    __device__ __forceinline__ void bring_down(uint32_t pairs, int lane, const uint32_t (&mine)[F::kGroups])
+    {
+        const float down = power_of_2(-places());
+#pragma unroll
+        for (int g = 0; g < F::kGroups; g++)
+            sts_u16(pairs + 4 * (F::kGroups * lane + g), Value<T>::round(__fmul_rn(pair_values<T>(mine[g]).x, down)));
+        __syncwarp();
     }
 
     // x[n][t]: in units, of token 16 n + 8 t + r
@@ -672,6 +720,71 @@ struct Rows {
         }
     }
 
+    // A tile of a far warp, or of one that may become so: references, sums and exponents. Products are rounded as references are, so
+    // that the largest score gives 0.
+    template <bool kMasked>
+    __device__ __forceinline__ void go_far(uint32_t pairs, int lane, const uint32_t (&mine)[F::kGroups], int k,
+                                           const float2 (&x)[2][2][F::kHalves], const uint32_t (&seen)[F::kHalves][2],
+                                           float2 (&y)[2][2][F::kHalves])
+    {
+        const int r = lane >> 2;
+        const auto sees = [&](int h, int odd, int n, int t) { return !kMasked || ((seen[h][odd] >> (16 * n + 8 * t + r)) & 1); };
+        const auto is_far = [](float ref) { return fabsf(ref) >= kFar && ref != kNothing; };
+        bool any = far;
+#pragma unroll
+        for (int h = 0; h < F::kHalves; h++) any = any || is_far(ref[h].x) || is_far(ref[h].y);
+        any = __any_sync(kFull, any);
+        const bool was = far;
+        const float less_by = (float)(level - places()) + kSlack<T> - kLift;  // what a reference that is not far holds beside a score
+        if (any) {
+            const int places_was = places();
+            far = true;
+            set_level(k);
+            bring_down(pairs, lane, mine);
+            const int up = places_was - places();  // from scales of 0 to the largest it can pass what a power holds
+            const float less = up < -126 ? 0.0f : power_of_2(up);
+#pragma unroll
+            for (int h = 0; h < F::kHalves; h++) {
+                float2 best = splat(-INFINITY);
+#pragma unroll
+                for (int n = 0; n < 2; n++)
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        const float2 v = mul2_unfused(x[n][t][h], f[h]);
+                        if (sees(h, 0, n, t)) best.x = fmaxf(best.x, v.x);
+                        if (sees(h, 1, n, t)) best.y = fmaxf(best.y, v.y);
+                    }
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    best.x = fmaxf(best.x, __shfl_xor_sync(kFull, best.x, d));
+                    best.y = fmaxf(best.y, __shfl_xor_sync(kFull, best.y, d));
+                }
+                // a row whose reference has become so large has nothing yet, or scores far below this tile's
+                const auto next_of = [&](float ref, float best) {
+                    if (was || ref == kNothing) return fmaxf(ref, best);
+                    return is_far(ref) ? best : fmaxf(best, ref - less_by);
+                };
+                const float2 next = make_float2(next_of(ref[h].x, best.x), next_of(ref[h].y, best.y));
+                const float2 keep = make_float2(exp2_fast(fminf(__fsub_rn(ref[h].x, next.x), 100.0f)),
+                                                exp2_fast(fminf(__fsub_rn(ref[h].y, next.y), 100.0f)));
+                ref[h] = next;
+                move(h, keep, less);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; n++)
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    float2 &v = y[n][t][h];
+                    const float2 a = make_float2(-ref[h].x, -ref[h].y);
+                    v = any ? add2(mul2_unfused(x[n][t][h], f[h]), a) : fma2(x[n][t][h], f[h], a);
+                    if (!sees(h, 0, n, t)) v.x = -INFINITY;
+                    if (!sees(h, 1, n, t)) v.y = -INFINITY;
+                }
+    }
+
     // A tile's values join the sums. seen: a bit a token for the rows 2 q and 2 q + 1 of each half; kMasked is false where
     // all are set.
     template <bool kMasked>
@@ -705,67 +818,52 @@ struct Rows {
         // p s, s come down, stays within 2^14 as long as no scale passes the level and no p 2^(14 - level): every lane looks at its own
         // tokens, and the rows' largest p s are looked for where one does
         if (__any_sync(kFull, most > bound || above != limit)) {
-            int k = kLowest;
-#pragma unroll
-            for (int g = 0; g < F::kGroups; g++) {
-                const uint32_t scale = mine[g] & 0x7fffu, offset = (mine[g] >> 16) & 0x7fffu;
-                if (finite_bits<T>(scale)) k = max(k, exponent_of<T>(scale) + 1);
-                if (finite_bits<T>(offset)) k = max(k, exponent_of<T>(offset) - 23);
-            }
-            const int token = k;  // the lane's token's level
-            k = __reduce_max_sync(kFull, max(k, level));
-            const float less = power_of_2(places_down<T>(level) - places_down<T>(k));  // for sums of p s
-            set_level(k);
-            // Scales that come down do so in the tile itself, each lane its token's: every such tile comes here (a product for each
-            // scale where it is used cost 64 sequences of up to 8192 tokens 1 %).
-            if (places_down<T>(k) > 0) {
-                const float down = power_of_2(-places_down<T>(k));
-#pragma unroll
-                for (int g = 0; g < F::kGroups; g++)
-                    sts_u16(pairs + 4 * (F::kGroups * lane + g), Value<T>::round(__fmul_rn(pair_values<T>(mine[g]).x, down)));
-                __syncwarp();
-            }
-            float add[2][2];  // log2 of what a token's p is multiplied by, at most
-#pragma unroll
-            for (int n = 0; n < 2; n++)
-#pragma unroll
-                for (int t = 0; t < 2; t++)
-                    add[n][t] = (float)max(__shfl_sync(kFull, token, 16 * n + 8 * t + r) - places_down<T>(k), kLowest);
-#pragma unroll
-            for (int h = 0; h < F::kHalves; h++) {
-                float2 top = splat(-INFINITY);
+            const int token = level_of<T>(mine);  // the lane's token's level
+            const int k = __reduce_max_sync(kFull, max(token, level));
+            float reach = INFINITY;
+            if (!far) {
+                reach = 0.0f;
+                const int places_was = places();
+                set_level(k);
+                // in the tile itself, all such tiles come here: a product for each scale where it is used cost 64 sequences of up
+                // to 8192 tokens 1 %
+                if (places() > 0) bring_down(pairs, lane, mine);
+                const float less = power_of_2(places_was - places());
+                // log2 of what a token's p is multiplied by, at most
+                const float its = (float)max(token - places(), kLowest);
+                float add[2][2];
 #pragma unroll
                 for (int n = 0; n < 2; n++)
 #pragma unroll
-                    for (int t = 0; t < 2; t++) {
-                        const float2 v = fma2(x[n][t][h], f[h], splat(add[n][t]));
-                        if (sees(h, 0, n, t)) top.x = fmaxf(top.x, v.x);
-                        if (sees(h, 1, n, t)) top.y = fmaxf(top.y, v.y);
+                    for (int t = 0; t < 2; t++) add[n][t] = __shfl_sync(kFull, its, 16 * n + 8 * t + r);
+#pragma unroll
+                for (int h = 0; h < F::kHalves; h++) {
+                    float2 top = splat(-INFINITY);
+#pragma unroll
+                    for (int n = 0; n < 2; n++)
+#pragma unroll
+                        for (int t = 0; t < 2; t++) {
+                            const float2 v = fma2(x[n][t][h], f[h], splat(add[n][t]));
+                            if (sees(h, 0, n, t)) top.x = fmaxf(top.x, v.x);
+                            if (sees(h, 1, n, t)) top.y = fmaxf(top.y, v.y);
+                        }
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, d));
+                        top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
                     }
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, d));
-                    top.y = fmaxf(top.y, __shfl_xor_sync(kFull, top.y, d));
+                    top = add2(top, splat(kSlack<T> - kLift));
+                    const float2 next = make_float2(fmaxf(ref[h].x, top.x), fmaxf(ref[h].y, top.y));
+                    const float2 keep = make_float2(exp2_fast(__fsub_rn(ref[h].x, next.x)), exp2_fast(__fsub_rn(ref[h].y, next.y)));
+                    ref[h] = next;
+                    reach = fmaxf(reach, fmaxf(fabsf(next.x), fabsf(next.y)));
+                    move(h, keep, less);
                 }
-                float2 next = ref[h];
-                if (top.x > -INFINITY) next.x = fmaxf(next.x, __fadd_rn(top.x, kSlack<T> - kLift));
-                if (top.y > -INFINITY) next.y = fmaxf(next.y, __fadd_rn(top.y, kSlack<T> - kLift));
-                const float2 keep = make_float2(exp2_fast(__fsub_rn(ref[h].x, next.x)), exp2_fast(__fsub_rn(ref[h].y, next.y)));
-                ref[h] = next;
-                total[h] = mul2(total[h], keep);
-#pragma unroll
-                for (int g = 0; g < F::kGroups; g++) off[h][g] = mul2(off[h][g], keep);
-                const float2 keep_ps = mul2(keep, splat(less));
-#pragma unroll
-                for (int m = 0; m < F::kDim / 16; m++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) sum[m][h][i] = __fmul_rn(sum[m][h][i], i & 1 ? keep_ps.y : keep_ps.x);
-#pragma unroll
-                for (int g = 0; g < F::kGroups; g++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) eights[g][h][i] = __fmul_rn(eights[g][h][i], i & 1 ? keep_ps.y : keep_ps.x);
             }
-            exponents();
+            if (__any_sync(kFull, reach >= kFar))
+                go_far<kMasked>(pairs, lane, mine, k, x, seen, y);
+            else
+                exponents();
         }
 #pragma unroll
         for (int n = 0; n < 2; n++)
@@ -833,7 +931,11 @@ struct Rows {
     // The lanes' parts brought together: total in every lane of a row, sum the true sums of p v.
     __device__ __forceinline__ void finish()
     {
-        const float up = power_of_2(24 + places_down<T>(level));  // 1 / kUnit and what scales came down by
+        const float up = power_of_2(min(24 + places(), 126));  // 1 / kUnit and what scales came down by
+        if (24 + places() > 126) {
+#pragma unroll
+            for (int h = 0; h < F::kHalves; h++) move(h, splat(1.0f), power_of_2(24 + places() - 126));
+        }
         const auto all = [](float2 v) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)

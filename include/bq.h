@@ -473,15 +473,15 @@ BQ_API bq_status bq_kv4_read(const bq_kv4_cache *cache, const void *slots, int s
  *   lse        [batch][n_q][q_heads] FP32 (written): log of the sum of exp(scale * <q, key>); or NULL
  *   workspace  bq_kv4_workspace_bytes(...) bytes, 16-byte aligned, scratch of this call: its content means
  *              nothing before and after. Calls that may run at the same time need one each.
- * scale is finite. q_heads a multiple of heads, at most 65536; n_q * q_heads <= 2^20;
- * width * page < 2^31 - 2^20; window <= 2^30. Products and sums are binary32 (the tensor cores may
- * truncate where a binary32 addition would round); a softmax weight times a value's scale is rounded to
- * FP16, at a power of two of the query's own: beside the largest such product of what it sees (or 2^-24 of
- * a weight times an offset) 2^-22 and more keep all bits, the rest is right to 2^-33 of it (of scales of
- * 2^-80 and more; beside one of 2^96 and more, of 2^-48 and more); the output is rounded once. A call
- * repeated gives the same bits. Made for a few rows, queries times heads that share a key-value head: the
- * cache is read once for every 16 of them, 8 where head_dim > 128. Two launches; sequences of all lengths
- * share the GPU evenly. */
+ * scale is finite, and scores may be of any finite size (beside scores of 2^20 and more, values up to 2^96).
+ * q_heads a multiple of heads, at most 65536; n_q * q_heads <= 2^20; width * page < 2^31 - 2^20; window <=
+ * 2^30. Products and sums are binary32 (the tensor cores may truncate where a binary32 addition would
+ * round); a softmax weight times a value's scale is rounded to FP16, at a power of two of the query's own:
+ * beside the largest such product of what it sees (or 2^-24 of a weight times an offset) 2^-22 and more
+ * keep all bits, the rest is right to 2^-33 of it (of scales of 2^-80 and more; beside one of 2^96 and more,
+ * of 2^-48 and more); the output is rounded once. A call repeated gives the same bits. Made for a few rows,
+ * queries times heads that share a key-value head: the cache is read once for every 16 of them, 8 where
+ * head_dim > 128. Two launches; sequences of all lengths share the GPU evenly. */
 BQ_API bq_status bq_kv4_attend(const bq_kv4_cache *cache, const void *q, int64_t q_ld_batch, int64_t q_ld_query,
                                int64_t q_ld_head, int64_t batch, int n_q, int q_heads, const int32_t *table,
                                int64_t ld_table, int64_t width, const int32_t *lengths, float scale, int64_t window,

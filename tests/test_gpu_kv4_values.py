@@ -161,6 +161,33 @@ def test_offsets_of_any_size_beside_no_steps():
             assert np.all(np.abs(out[at] - want) <= 2.0 ** -8 * np.abs(want) + (len(w) / 16 + 64) * 2.0 ** -23 * (w @ np.abs(z)))
 
 
+@pytest.mark.parametrize("name", list(TYPES))
+@pytest.mark.parametrize("up", [10, 18, 21, 22, 23, 24, 25, 26, 27, 28, 30, 34, 40, 60, 90])
+@pytest.mark.parametrize("kind", ["ties", "two levels", "rising", "falling below"])
+def test_scores_of_any_size(kind, up, name):
+    # scores of 2^up and more that are whole in binary32, ties among them; in other rows of the same warps minus that, zero and small ones
+    dtype = TYPES[name][0]
+    n = 700
+    q, cache, table, lengths, _ = winner_of(n, 0, 0, q_heads=5, dtype=dtype)
+    code = np.full(n, 7)
+    if kind == "two levels":
+        code[np.random.default_rng(up).random(n) < 0.5] = 6
+    elif kind == "rising":
+        code = np.arange(n) * 8 // n  # 0 to 7
+    elif kind == "falling below":
+        code = np.where(np.arange(n) < 40, 7, -np.arange(n) % 8)
+    at = torch.arange(n, device="cuda")
+    cache.k[at // 32, 0, at % 32, 0] = torch.from_numpy(code & 15).to(torch.uint8).cuda()
+    q[0, 0, :, 0] = torch.tensor([1.0, -1.0, 0.0, 2.0 ** -8, 1.5])
+    rows = list(rows_of(q, cache, table, lengths, 2.0 ** up))
+    check_rows(*run(q, cache, table, lengths, scale=2.0 ** up), rows, BITS[name])
+    # the same scores from large queries and keys, where the type holds them
+    half = min(up // 2, 12 if name == "f16" else 60)
+    q *= 2.0 ** half
+    cache.k_scales[..., 0] *= 2.0 ** half
+    check_rows(*run(q, cache, table, lengths, scale=2.0 ** (up - 2 * half)), rows, BITS[name])
+
+
 def test_the_debug_build_declines_no_access_over_values_of_every_size(bq_lib):
     with _lib.use_library(build.build_debug_library()):
         codec.take_index_errors()
