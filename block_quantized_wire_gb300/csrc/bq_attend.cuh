@@ -47,11 +47,11 @@ constexpr int kTokens = 32;                       // of a tile
 constexpr float kNothing = -3.0e38f;              // the reference of a row that has seen nothing
 constexpr float kUnit = 0x1p-24f;                 // of a code held as an FP16's lowest mantissa bits
 constexpr float kLift = 13.0f;                    // log2 that p s may have beside a fresh reference; one more before there is another
-constexpr int kLowest = -80;                      // level of the smallest scales: 2^31 weights of 2^(14 - level) are 2^125
-// The level that a reference takes in at most: a row's largest weight is 2^-87 or more, and what ex2.approx.ftz makes zero
-// (below 2^-126) 2^-39 of it. Larger scales (BF16's reach 2^128) come down by the rest, a power of two that the sums of p s get
-// back at the end.
-constexpr int kHighest = 96;
+// The levels that references take in. Beyond them scales come up or down by a power of two that the sums of p s get back at the end,
+// in every tile. References of one score then lie within 2^100 of each other, so that no factor between them is zero; a row's
+// largest weight is 2^-71 or more, and what ex2.approx.ftz makes zero (below 2^-126) 2^-55 of it; 2^31 weights of 2^(14 - level) are
+// 2^65. FP16's levels, -14 to 16, need none of that.
+constexpr int kLowest = -20, kHighest = 80;
 // A fresh reference leaves a row's largest p s so many places below kLift. A tile is looked at more closely where a p could pass the
 // level, whatever its own s, and with less room that is more often: 64 sequences of up to 8192 BF16 tokens took 78.9 us with 0, 76.1
 // with 1, 74.4 with 2, 72.5 with 4, 72.1 with 6 (before rows could be far, which costs about 1 us). But sums that a tile's products
@@ -328,6 +328,14 @@ __device__ __forceinline__ bool finite_bits(uint32_t bits)
     return bits < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
 }
 
+// The level of (scale, offset) bits without signs.
+template <class T>
+__device__ __forceinline__ int level_of_bits(uint32_t most)
+{
+    return max(exponent_of<T>(most & 0xffffu) + 1, exponent_of<T>(most >> 16) - 23);
+}
+__device__ __forceinline__ float power_or_0(int e) { return e < -126 ? 0.0f : power_of_2(e); }  // e <= 127
+
 // The level of a token's (scale, offset) pairs.
 template <class T, int N>
 __device__ __forceinline__ int level_of(const uint32_t (&pairs)[N])
@@ -343,7 +351,7 @@ __device__ __forceinline__ int level_of(const uint32_t (&pairs)[N])
             most = __vmaxu2(most, (finite_bits<T>(scale) ? scale : 0u) | (finite_bits<T>(offset) ? offset << 16 : 0u));
         }
     }
-    return max(kLowest, max(exponent_of<T>(most & 0xffffu) + 1, exponent_of<T>(most >> 16) - 23));
+    return level_of_bits<T>(most);
 }
 
 // The largest (scale, offset) bits without signs whose scale is below 2^level and offset below 2^(level + 24).
@@ -534,7 +542,7 @@ struct Rows {
     __device__ __forceinline__ void start(const Kv4Attend &a, int lane, const Queries &raw)
     {
         far = false;
-        set_level(kLowest);
+        set_level(level_of_bits<T>(0));
         const int q = lane & 3;
 #pragma unroll
         for (int h = 0; h < F::kHalves; h++) {
@@ -612,13 +620,14 @@ struct Rows {
     // Binary places that scales come down by.
     __device__ __forceinline__ int places() const
     {
-        return far ? level - (int)kLift : std::is_same<T, __half>::value ? 0 : max(level - kHighest, 0);
+        if (far) return max(level, -100) - (int)kLift;
+        return std::is_same<T, __half>::value ? 0 : max(level - kHighest, 0) + min(level - kLowest, 0);
     }
     __device__ __forceinline__ void set_level(int to)
     {
         level = to;
         limit = limit_of<T>(to);
-        bound = far || places() > 0 ? -INFINITY : kLift + 1.0f - (float)to;
+        bound = far || places() != 0 ? -INFINITY : kLift + 1.0f - (float)to;
     }
     // A row's sums after its reference has gone up: times keep, those of p s times less too.
     __device__ __forceinline__ void move(int h, float2 keep, float less)
@@ -741,8 +750,7 @@ struct Rows {
             far = true;
             set_level(k);
             bring_down(pairs, lane, mine);
-            const int up = places_was - places();  // from scales of 0 to the largest it can pass what a power holds
-            const float less = up < -126 ? 0.0f : power_of_2(up);
+            const float less = power_or_0(places_was - places());
 #pragma unroll
             for (int h = 0; h < F::kHalves; h++) {
                 float2 best = splat(-INFINITY);
@@ -827,8 +835,8 @@ struct Rows {
                 set_level(k);
                 // in the tile itself, all such tiles come here: a product for each scale where it is used cost 64 sequences of up
                 // to 8192 tokens 1 %
-                if (places() > 0) bring_down(pairs, lane, mine);
-                const float less = power_of_2(places_was - places());
+                if (places() != 0) bring_down(pairs, lane, mine);
+                const float less = power_or_0(places_was - places());
                 // log2 of what a token's p is multiplied by, at most
                 const float its = (float)max(token - places(), kLowest);
                 float add[2][2];

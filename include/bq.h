@@ -478,10 +478,11 @@ BQ_API bq_status bq_kv4_read(const bq_kv4_cache *cache, const void *slots, int s
  * 2^30. Products and sums are binary32 (the tensor cores may truncate where a binary32 addition would
  * round); a softmax weight times a value's scale is rounded to FP16, at a power of two of the query's own:
  * beside the largest such product of what it sees (or 2^-24 of a weight times an offset) 2^-22 and more
- * keep all bits, the rest is right to 2^-33 of it (of scales of 2^-80 and more; beside one of 2^96 and more,
- * of 2^-48 and more); the output is rounded once. A call repeated gives the same bits. Made for a few rows,
- * queries times heads that share a key-value head: the cache is read once for every 16 of them, 8 where
- * head_dim > 128. Two launches; sequences of all lengths share the GPU evenly. */
+ * keep all bits, the rest is right to 2^-33 of it (unless every scale that it sees is below 2^-20, or 2^-100
+ * of its sequence's largest, and smaller than that one); the output is rounded once. A call repeated gives
+ * the same bits. Made for a few rows, queries times heads that share a key-value head: the cache is read
+ * once for every 16 of them, 8 where head_dim > 128. Two launches; sequences of all lengths share the GPU
+ * evenly. */
 BQ_API bq_status bq_kv4_attend(const bq_kv4_cache *cache, const void *q, int64_t q_ld_batch, int64_t q_ld_query,
                                int64_t q_ld_head, int64_t batch, int n_q, int q_heads, const int32_t *table,
                                int64_t ld_table, int64_t width, const int32_t *lengths, float scale, int64_t window,

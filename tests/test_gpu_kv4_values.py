@@ -188,6 +188,47 @@ def test_scores_of_any_size(kind, up, name):
     check_rows(*run(q, cache, table, lengths, scale=2.0 ** (up - 2 * half)), rows, BITS[name])
 
 
+@pytest.mark.parametrize("scales", [[0.0, 2.0 ** 120], [2.0 ** 120, 0.0], [0.0, 2.0 ** 60, 1.0], [2.0 ** -70, 2.0 ** 60], [2.0 ** 60, 2.0 ** -70],
+                                    [0.0, 2.0 ** 96, 0.0, 2.0 ** 124], [2.0 ** -75, 1.0, 2.0 ** 90]])
+@pytest.mark.parametrize("n", [70, 700, 20000])
+@pytest.mark.parametrize("offsets", [False, True])
+def test_values_that_change_their_size_along_a_sequence(n, scales, offsets):
+    # the weights of all positions count, whatever was met first and by whom
+    q, cache, table, lengths, _ = winner_of(n, 0, 0, q_heads=3)
+    cache.k[..., 0] = torch.from_numpy(np.random.default_rng(n).integers(0, 16, cache.k.shape[:-1]).astype(np.uint8)).cuda()
+    at = torch.arange(n, device="cuda")
+    size = torch.tensor(scales, device="cuda")[at * len(scales) // n].to(torch.bfloat16)
+    cache.v_scales[at // 32, 0, at % 32, :, 0] = size[:, None]
+    cache.v_scales[at // 32, 0, at % 32, :, 1] = (size[:, None] if offsets else 0 * size[:, None])
+    q[0, 0, :, 0] = torch.tensor([0.0, 0.25, -1.0])
+    check_rows(*run(q, cache, table, lengths, scale=1.0), rows_of(q, cache, table, lengths, 1.0), 8)
+
+
+def test_the_largest_values_average_to_themselves():
+    q, cache, table, lengths = problem(4, [30000, 64], 1, 2, 1, 64, 64, 64)
+    cache.v_scales[..., 0], cache.v_scales[..., 1] = 0, torch.finfo(torch.bfloat16).max
+    out = run(q, cache, table, lengths)[0]
+    assert bool((out.double() >= torch.finfo(torch.bfloat16).max * (1 - 2.0 ** -7)).all()) and bool(torch.isfinite(out.float()).all())
+
+
+@pytest.mark.parametrize("name,scales", [("bf16", [0.0, 2.0 ** 90]), ("bf16", [2.0 ** 90, 0.0]), ("bf16", [2.0 ** -70, 2.0 ** 20]),
+                                         ("bf16", [1.0, 2.0 ** -60]), ("f16", [0.0, 64.0]), ("f16", [64.0, 2.0 ** -14])])
+@pytest.mark.parametrize("far", [0, 300, 699])
+def test_large_scores_beside_scales_of_any_size(name, scales, far):
+    # scores of 0, then of 2^30 and more from position `far` on; values of one size and then of another
+    dtype = TYPES[name][0]
+    q, cache, table, lengths, _ = winner_of(700, 0, 0, q_heads=5, dtype=dtype)
+    at = torch.arange(700, device="cuda")
+    cache.k[at // 32, 0, at % 32, 0] = torch.where(at >= far, 7, 0).to(torch.uint8)
+    cache.v_scales[..., 1] = 0
+    for part, scale in zip((at < 350, at >= 350), scales):
+        cache.v_scales[at[part] // 32, 0, at[part] % 32, :, 0] = scale
+    q[0, 0, :, 0] = torch.tensor([1.0, -1.0, 0.0, 2.0 ** -28, 1.5])
+    rows = [r for r in rows_of(q, cache, table, lengths, 2.0 ** 30) if np.any(r[1])]
+    assert rows
+    check_rows(*run(q, cache, table, lengths, scale=2.0 ** 30), rows, BITS[name])
+
+
 def test_the_debug_build_declines_no_access_over_values_of_every_size(bq_lib):
     with _lib.use_library(build.build_debug_library()):
         codec.take_index_errors()
