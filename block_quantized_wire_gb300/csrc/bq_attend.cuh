@@ -27,11 +27,11 @@
 // What bounds it: the cache's bytes are the floor (144 a token and head at head_dim 128 and groups of 64), and a warp's chain of
 // instructions that turn codes into operands comes next: 5 logic instructions for 8 codes, two cycles of a scheduler each, and an
 // mma of eight cycles for 256 codes (twice that for more than 8 rows). No pipe is full: for 64 sequences of up to 8192 tokens a
-// scheduler issues in 46 % of its cycles, the integer pipe is busy in 44 %, the tensor cores in 26 %, DRAM runs at 56 % of its
-// nominal rate. With 213 registers a scheduler has two warps, and the first stall is an instruction's own latency. With the
+// scheduler issues in 45 % of its cycles, the integer pipe is busy in 43 %, the tensor cores in 26 %, DRAM runs at 54 % of its
+// nominal rate. With 216 registers a scheduler has two warps, and the first stall is an instruction's own latency. With the
 // arithmetic taken out the copies ran at 6.9 TB/s, with the copies taken out the arithmetic at 5.9 TB/s of cache (each measured on a
-// changed copy of the kernel), both together at 5.6; a call's ends (lengths, first tiles, joins) take about 11 us more. One
-// sequence of 131072 tokens: 38 us; 64 of up to 8192: 72 us.
+// changed copy of the kernel), both together at 5.5; a call's ends (lengths, first tiles, joins) take about 11 us more. One
+// sequence of 131072 tokens: 38 us; 64 of up to 8192: 74 us.
 #pragma once
 
 #include <cmath>
@@ -192,7 +192,7 @@ struct Form {
     static constexpr int kStage = kValid + 16;
     static constexpr int kJoin = 3 * 4 * kRows * (kDim + 2);
     // CTAs of an SM by their registers: 8 rows of 64 columns fit 168 a thread, all else up to 255, of which a few forms spill
-    // (at most 172 bytes of stores and 252 of loads a thread: 16 rows of 128 columns with groups of 32 and 64, 8 rows of 192 and
+    // (at most 208 bytes of stores and 276 of loads a thread: 16 rows of 128 columns with groups of 32 and 64, 8 rows of 192 and
     // 256 columns with groups of 32 and, of 256, 64). 8 rows of 128 columns with three CTAs (168, some spilled) took 77.3 us for 64
     // sequences of up to 8192 tokens where two took 74.6, with four (128) 85.7; the other forms were not tried with more.
     static constexpr int kCtas = kRows == 8 && kDim == 64 ? 3 : 2;
