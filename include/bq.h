@@ -473,7 +473,8 @@ BQ_API bq_status bq_kv4_read(const bq_kv4_cache *cache, const void *slots, int s
  *   lse        [batch][n_q][q_heads] FP32 (written): log of the sum of exp(scale * <q, key>); or NULL
  *   workspace  bq_kv4_workspace_bytes(...) bytes, 16-byte aligned, scratch of this call: its content means
  *              nothing before and after. Calls that may run at the same time need one each.
- * scale is finite, and scores may be of any finite size (beside scores of 2^20 and more, values up to 2^96).
+ * scale is finite, and scores may be of any finite size: of keys up to 2^124 and queries up to 2^116 / |scale|
+ * (beside scores of 2^20 and more, of values up to 2^96).
  * q_heads a multiple of heads, at most 65536; n_q * q_heads <= 2^20; width * page < 2^31 - 2^20; window <=
  * 2^30. Products and sums are binary32 (the tensor cores may truncate where a binary32 addition would
  * round); a softmax weight times a value's scale is rounded to FP16, at a power of two of the query's own:

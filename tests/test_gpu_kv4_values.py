@@ -229,6 +229,18 @@ def test_large_scores_beside_scales_of_any_size(name, scales, far):
     check_rows(*run(q, cache, table, lengths, scale=2.0 ** 30), rows, BITS[name])
 
 
+@pytest.mark.parametrize("key,query", [(2.0 ** 123, 2.0 ** -123), (2.0 ** 100, 2.0 ** -99), (2.0 ** -110, 2.0 ** 112), (2.0 ** -20, 2.0 ** 21)])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_queries_and_keys_of_any_size(key, query, dim):
+    # powers of two that cancel, or nearly so, in the scores
+    q, cache, table, lengths = problem(dim, [300, 31], 2, 6, 2, dim, 32, 32)
+    cache.k_scales[..., 0], cache.k_scales[..., 1] = 2.0 ** -4, cache.k_scales[..., 1].clamp(-1, 1) * 0.25  # keys up to 3 / 4
+    cache.k_scales *= key
+    q = (q.float() * query).to(q.dtype)
+    out, lse = run(q, cache, table, lengths)
+    check_rows(out, lse, rows_of(q, cache, table, lengths, dim ** -0.5), 8)
+
+
 def test_the_debug_build_declines_no_access_over_values_of_every_size(bq_lib):
     with _lib.use_library(build.build_debug_library()):
         codec.take_index_errors()
